@@ -413,6 +413,140 @@ ig_status ig_append_kv(void* stream, ig_pool* pool, int layer, int B, int H, int
                        uint16_t* Kdense, uint16_t* Vdense);
 
 /* ------------------------------------------------------------------------------------
+ * Paged KV cache in HBM (serving beside the offloaded pool: a GB300's memory holds the whole
+ * cache of many requests; no counterpart in the paper).  A layer's keys and values are pages
+ *   K, V  dev [n_pages][Hkv][page][d]   fp16 or bf16 bit patterns, 16-byte aligned
+ * with `page` (a positive multiple of 8) tokens each.  Token t of a sequence is row t % page of
+ * the page its row of the page table names at t / page; one page number stands for the same
+ * page of every layer, and of K and V.  A token's slot is page_number * page + t % page.
+ * Query head h reads key/value head h / (Hq / Hkv) (Hq a multiple of Hkv).
+ * The calls below run on the current device, which must be the one that holds the buffers. */
+#define IG_F16 0
+#define IG_BF16 1
+
+/* Attention of one new token per sequence over its pages: for every b and query head h,
+ *   z_t = scale * q . K_t,  o = sum_t w_t V_t,  w = softmax_t(z),  t < L_valid[b]
+ *   lse = log(sum_t exp(z_t))        (natural logarithm; joins results over parts of a cache)
+ * in one pass over K and V, products in fp16/bf16 with fp32 sums, softmax in fp32, the weights
+ * in at least 22 bits.  L_valid[b] = 0 (or every z_t = -inf) gives o = 0 and lse = -inf.  What
+ * the pages hold past a sequence's last token may be anything, NaN included; a NaN or infinity
+ * in a row that is attended gives non-finite results for its heads.
+ *   q           dev [B][Hq][d] of `dtype`, 16-byte aligned
+ *   page_table  dev int32 [B][max_pages]; entries past a sequence's last page are not used.  A
+ *               page number outside [0, n_pages) sets IG_DEVERR_INDEX and its tokens are left out
+ *   L_valid     dev int32 [B], 0 <= L_valid[b] <= max_pages * page (else IG_DEVERR_INDEX, and the
+ *               nearer bound is used)
+ *   out         dev fp32 [B][Hq][d] out, 16-byte aligned
+ *   lse         dev fp32 [B][Hq] out, or NULL
+ *   workspace   dev, >= ig_paged_attend_workspace_bytes(B, Hq, Hkv, d) bytes, 256-byte aligned;
+ *               arbitrary content, not shared by calls that may run at the same time
+ * dtype: IG_F16 or IG_BF16 (q, K and V).  d must be 64 or 128; scale finite. */
+size_t ig_paged_attend_workspace_bytes(int B, int Hq, int Hkv, int d);
+ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page,
+                          int n_pages, int max_pages, float scale, const uint16_t* q,
+                          const uint16_t* K, const uint16_t* V, const int32_t* page_table,
+                          const int32_t* L_valid, float* out, float* lse, void* workspace,
+                          size_t workspace_bytes);
+
+/* Rotary frequencies on the host, as ig_qk_norm_rope takes them: turns[j] is the fraction of a
+ * turn that pair j moves per position, f_j / (2 pi) modulo 1, times 2^64 (so that the angle at
+ * position p is the low 64 bits of p * turns[j], exact for every 32-bit position).
+ *   f_j = theta^(-2 j / rot), j < rot / 2, changed for contexts longer than the trained one:
+ *   IG_ROPE_PLAIN   unchanged
+ *   IG_ROPE_LINEAR  f_j / factor (position interpolation)
+ *   IG_ROPE_BASE    theta * factor^(rot / (rot - 2)) in place of theta (rot > 2)
+ *   IG_ROPE_YARN    YaRN (Peng et al., 2023): f_j / factor * r_j + f_j (1 - r_j), r_j the ramp
+ *                   clamp((j - lo) / max(hi - lo, 0.001), 0, 1) from lo = max(floor(x(p0)), 0) to
+ *                   hi = min(ceil(x(p1)), rot - 1), x(n) = rot ln(context / (2 pi n)) / (2 ln theta)
+ *                   (p0 > p1 > 0 turns over the trained context, 32 and 1 in the paper; theta > 1);
+ *                   *rot_scale = 0.1 ln(factor) + 1 for factor > 1
+ *   IG_ROPE_BANDS   by wavelength w_j = 2 pi / f_j: f_j for w_j < context / p1, f_j / factor for
+ *                   w_j > context / p0, else f_j ((1 - s) / factor + s), s = (context / w_j - p0) /
+ *                   (p1 - p0) (p1 > p0 > 0)
+ *   context   the trained context length (YARN and BANDS; else ignored, as p0 and p1)
+ *   turns     host uint64 [rot / 2] out;  rot_scale host fp32 out: the factor on the rotated part
+ *             (1 but for YARN)
+ * rot: a positive multiple of 2; theta > 0; factor >= 1 (ignored by PLAIN). */
+#define IG_ROPE_PLAIN 0
+#define IG_ROPE_LINEAR 1
+#define IG_ROPE_BASE 2
+#define IG_ROPE_YARN 3
+#define IG_ROPE_BANDS 4
+ig_status ig_rope_turns(int rot, double theta, int scaling, double factor, int context, double p0,
+                        double p1, uint64_t* turns, float* rot_scale);
+
+/* Queries and keys of T tokens on their way from the projections: per head the RMS norm, then the
+ * rotation at the token's position, and the keys and values into their pages, in one pass:
+ *   y = x * (mean(x^2) + eps)^-1/2 * weight     (weights NULL: y = x)
+ *   (y_a, y_b) -> rot_scale * (y_a cos - y_b sin, y_a sin + y_b cos) for each pair j < rot / 2,
+ *   angle = position * f_j; (a, b) = (j, j + rot/2) with IG_ROPE_HALF, (2j, 2j + 1) with
+ *   IG_ROPE_PAIRS; elements from rot on are not rotated.
+ * All of it in fp32 from the stored values, rounded once to `dtype`; values are copied as they are.
+ *   q, k, v     dev, token t's heads dense at q + t * q_stride ([Hq][d]), k + t * k_stride and
+ *               v + t * v_stride ([Hkv][d]); strides in elements, multiples of 8, at least a token's
+ *               heads, so one fused projection's output serves; 16-byte aligned
+ *   q_weight, k_weight  dev [d] of `dtype`, 16-byte aligned, or NULL (each by itself): no norm
+ *   eps         >= 0 (used where there is a weight)
+ *   positions   dev int32 [T] (may be NULL when rot = 0)
+ *   turns       dev uint64 [rot / 2] from ig_rope_turns, 16-byte aligned (may be NULL when rot = 0)
+ *   q_out       dev [T][Hq][d] out, 16-byte aligned; q itself when q_stride = Hq * d, otherwise
+ *               outputs and inputs must not overlap
+ *   page > 0:   k_out, v_out are a layer's pages K, V (n_pages of them) and slot dev int32 [T] names
+ *               each token's slot.  A negative slot: the token's q is written, its k and v are not.
+ *               A slot >= n_pages * page: the same, and IG_DEVERR_INDEX.  No two tokens of a call
+ *               may have the same slot (which one's pieces stay is not defined).
+ *   page = 0:   k_out, v_out are dense [T][Hkv][d] (n_pages = 0, slot NULL); v and v_out may both be
+ *               NULL
+ * d must be 64 or 128; rot 0 or a multiple of 16 up to d; T >= 0. */
+#define IG_ROPE_HALF 0
+#define IG_ROPE_PAIRS 1
+ig_status ig_qk_norm_rope(void* stream, int dtype, int T, int Hq, int Hkv, int d, int rot, int layout,
+                          const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                          const uint16_t* v, int64_t v_stride, const uint16_t* q_weight,
+                          const uint16_t* k_weight, float eps, const int32_t* positions,
+                          const uint64_t* turns, float rot_scale, uint16_t* q_out, int page, int n_pages,
+                          const int32_t* slot, uint16_t* k_out, uint16_t* v_out);
+
+/* Page moves of every layer in one launch: for each move i < n, rows 0 .. rows-1 of page src go to
+ * the same rows of page dst, for every head of K and V of every layer; the other rows of dst stay.
+ *   K, V    host arrays [layers] of dev pages [n_pages][Hkv][page][d] (16-bit elements of any type)
+ *   moves   dev int32 [n][3]: src, dst, rows (0 <= rows <= page).  src < 0: the move is skipped.
+ *           A page or row count out of range sets IG_DEVERR_INDEX and the move is skipped.
+ *           The moves run in no order: a dst may appear once, and as no other move's src.
+ * At most 128 layers per call; d a multiple of 8; n >= 0. */
+ig_status ig_page_copy(void* stream, int layers, int n_pages, int Hkv, int page, int d,
+                       uint16_t* const* K, uint16_t* const* V, int n, const int32_t* moves);
+
+/* Host-side manager of the pages (needs no GPU): which pages each sequence has, with a count of
+ * the sequences that share a page.  New pages are the lowest free ones.  A manager is used by one
+ * thread at a time; a call that fails changes nothing.
+ * The device holds no copy of it: the caller copies the tables, lengths and slots to the device,
+ * and runs the moves a call gives (ig_page_copy) before anything else writes to the pages.  The
+ * moves of several ig_pages_extend calls with no other call between them may run as one list. */
+typedef struct ig_pages ig_pages;
+ig_status ig_pages_create(int n_pages, int page, int seqs, int max_pages, ig_pages** out);
+ig_status ig_pages_destroy(ig_pages* pages);
+/* Room for n more tokens of sequence seq (0 <= n): slots_out (host int32 [n], may be NULL) gets
+ * their slots.  When the first of them falls into a page that other sequences share, the sequence
+ * gets a page of its own (copy on write) and move_out (host int32 [3]: src, dst, rows) the move
+ * that fills it; else move_out[0] = -1.  IG_ERR_CAPACITY when pages or the table run out. */
+ig_status ig_pages_extend(ig_pages* pages, int seq, int n, int32_t* slots_out, int32_t* move_out);
+/* Sequence dst (which must be empty) becomes a copy of src: it shares all of src's pages. */
+ig_status ig_pages_fork(ig_pages* pages, int src, int dst);
+/* Keeps sequence seq's first n tokens (n <= its length) and gives back the pages after them that
+ * no sequence uses any more; n = 0 frees the sequence. */
+ig_status ig_pages_truncate(ig_pages* pages, int seq, int n);
+/* Moves the used pages to the lowest numbers: moves_out (host int32 [capacity][3]) gets *n_out
+ * moves (src, dst, page; each dst a free page, so they may run in any order), and the tables are
+ * changed to match.  IG_ERR_CAPACITY when more than `capacity` moves are needed (at most half the
+ * pages are). */
+ig_status ig_pages_compact(ig_pages* pages, int32_t* moves_out, int capacity, int* n_out);
+/* The page table (host int32 [seqs][max_pages], unused entries -1) and the lengths (host int32
+ * [seqs]); either may be NULL. */
+ig_status ig_pages_table(const ig_pages* pages, int32_t* table_out, int32_t* lengths_out);
+ig_status ig_pages_free_count(const ig_pages* pages, int* free_out);
+
+/* ------------------------------------------------------------------------------------
  * One decode step over every layer (native runtime of the calls above).  Section 3.2
  * (architecture) and section 3.4, "Decoding Stage", Step 5 with Fig 8: while layer i-1
  * attends, layer i is speculated from layer i-1's input and its rows are fetched on a side

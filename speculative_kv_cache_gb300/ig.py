@@ -42,8 +42,17 @@ IG_POOL_LRU = 2
 IG_POOL_NO_STORAGE = 1
 IG_POOL_FP8 = 2
 IG_POOL_INT4 = 4
+IG_F16 = 0
+IG_BF16 = 1
+IG_ROPE_HALF = 0
+IG_ROPE_PAIRS = 1
+IG_ROPE_PLAIN = 0
+IG_ROPE_LINEAR = 1
+IG_ROPE_BASE = 2
+IG_ROPE_YARN = 3
+IG_ROPE_BANDS = 4
 
-_vp, _i, _f, _sz = C.c_void_p, C.c_int, C.c_float, C.c_size_t
+_vp, _i, _f, _sz, _i64, _d = C.c_void_p, C.c_int, C.c_float, C.c_size_t, C.c_int64, C.c_double
 
 
 class IGError(RuntimeError):
@@ -108,6 +117,20 @@ _sig("ig_gather_attend_workspace_bytes", _sz, _i, _i, _i, _i)
 _sig("ig_gather_attend", _i, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i)
 _sig("ig_dense_attend", _i, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz)
 _sig("ig_append_kv", _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp)
+_sig("ig_paged_attend_workspace_bytes", _sz, _i, _i, _i, _i)
+_sig("ig_paged_attend", _i, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz)
+_sig("ig_rope_turns", _i, _i, _d, _i, _d, _i, _d, _d, _vp, C.POINTER(_f))
+_sig("ig_qk_norm_rope", _i, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f, _vp, _vp, _f,
+     _vp, _i, _i, _vp, _vp, _vp)
+_sig("ig_page_copy", _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp)
+_sig("ig_pages_create", _i, _i, _i, _i, _i, C.POINTER(_vp))
+_sig("ig_pages_destroy", _i, _vp)
+_sig("ig_pages_extend", _i, _vp, _i, _i, _vp, _vp)
+_sig("ig_pages_fork", _i, _vp, _i, _i)
+_sig("ig_pages_truncate", _i, _vp, _i, _i)
+_sig("ig_pages_compact", _i, _vp, _vp, _i, C.POINTER(_i))
+_sig("ig_pages_table", _i, _vp, _vp, _vp)
+_sig("ig_pages_free_count", _i, _vp, C.POINTER(_i))
 
 
 def header_functions() -> list[str]:
@@ -132,6 +155,16 @@ def _p(x):
             raise ValueError("array arguments must be C-contiguous")
         return x.ctypes.data
     raise TypeError(f"unsupported buffer argument {type(x)}")
+
+
+def _rows(x, stride):
+    """Address of a buffer of rows ``stride`` elements apart: as _p, and also a tensor whose first
+    dimension has that stride and whose others are dense (a slice of a fused projection)."""
+    if torch is not None and isinstance(x, torch.Tensor) and not x.is_contiguous():
+        if x.numel() and not (x[0].is_contiguous() and (x.shape[0] == 1 or x.stride(0) == stride)):
+            raise ValueError(f"tensor rows must be dense and {stride} elements apart")
+        return x.data_ptr()
+    return _p(x)
 
 
 def _s(stream):
@@ -402,6 +435,83 @@ def ig_append_kv(stream, pool, layer, B, H, d, k, Lcap, slot, cols, k_new, v_new
                  Vdense=None):
     _ok(_lib.ig_append_kv(_s(stream), pool, layer, B, H, d, k, Lcap, _p(slot), _p(cols), _p(k_new),
                           _p(v_new), _p(Kpart), _p(Kdense), _p(Vdense)), "ig_append_kv")
+
+
+def ig_paged_attend_workspace_bytes(B, Hq, Hkv, d) -> int:
+    return _lib.ig_paged_attend_workspace_bytes(B, Hq, Hkv, d)
+
+
+def ig_paged_attend(stream, dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scale, q, K, V, page_table, L_valid, out,
+                    lse, workspace, workspace_bytes):
+    _ok(_lib.ig_paged_attend(_s(stream), dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scale, _p(q), _p(K), _p(V),
+                             _p(page_table), _p(L_valid), _p(out), _p(lse), _p(workspace), workspace_bytes),
+        "ig_paged_attend")
+
+
+def ig_rope_turns(rot, theta, scaling, factor, context, p0, p1, turns) -> float:
+    """Fills turns (host uint64 or int64 [rot / 2]) and returns the factor on the rotated part."""
+    rs = C.c_float(0)
+    _ok(_lib.ig_rope_turns(rot, theta, scaling, factor, context, p0, p1, _p(turns), C.byref(rs)), "ig_rope_turns")
+    return rs.value
+
+
+def ig_qk_norm_rope(stream, dtype, T, Hq, Hkv, d, rot, layout, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight,
+                    eps, positions, turns, rot_scale, q_out, page, n_pages, slot, k_out, v_out):
+    _ok(_lib.ig_qk_norm_rope(_s(stream), dtype, T, Hq, Hkv, d, rot, layout, _rows(q, q_stride), q_stride,
+                             _rows(k, k_stride), k_stride, _rows(v, v_stride), v_stride, _p(q_weight), _p(k_weight), eps,
+                             _p(positions), _p(turns), rot_scale, _p(q_out), page, n_pages, _p(slot), _p(k_out),
+                             _p(v_out)), "ig_qk_norm_rope")
+
+
+def ig_page_copy(stream, layers, n_pages, Hkv, page, d, K, V, n, moves):
+    """K, V: lists of every layer's device pages."""
+    if len(K) != layers or len(V) != layers:
+        raise ValueError("one K and one V per layer")
+    K, V = _ptr_array(K), _ptr_array(V)
+    _ok(_lib.ig_page_copy(_s(stream), layers, n_pages, Hkv, page, d, C.cast(K, _vp), C.cast(V, _vp), n, _p(moves)),
+        "ig_page_copy")
+
+
+def ig_pages_create(n_pages, page, seqs, max_pages) -> int:
+    h = _vp()
+    _ok(_lib.ig_pages_create(n_pages, page, seqs, max_pages, C.byref(h)), "ig_pages_create")
+    return h.value
+
+
+def ig_pages_destroy(pages):
+    _ok(_lib.ig_pages_destroy(pages), "ig_pages_destroy")
+
+
+def ig_pages_extend(pages, seq, n, slots_out=None):
+    """Room for n more tokens of a sequence: fills slots_out (host int32 [n]) and returns the move
+    (src, dst, rows) to run first, or None."""
+    move = np.empty(3, dtype=np.int32)
+    _ok(_lib.ig_pages_extend(pages, seq, n, _p(slots_out), _p(move)), "ig_pages_extend")
+    return None if move[0] < 0 else tuple(int(x) for x in move)
+
+
+def ig_pages_fork(pages, src, dst):
+    _ok(_lib.ig_pages_fork(pages, src, dst), "ig_pages_fork")
+
+
+def ig_pages_truncate(pages, seq, n):
+    _ok(_lib.ig_pages_truncate(pages, seq, n), "ig_pages_truncate")
+
+
+def ig_pages_compact(pages, moves_out, capacity) -> int:
+    n = _i(0)
+    _ok(_lib.ig_pages_compact(pages, _p(moves_out), capacity, C.byref(n)), "ig_pages_compact")
+    return n.value
+
+
+def ig_pages_table(pages, table_out=None, lengths_out=None):
+    _ok(_lib.ig_pages_table(pages, _p(table_out), _p(lengths_out)), "ig_pages_table")
+
+
+def ig_pages_free_count(pages) -> int:
+    n = _i(0)
+    _ok(_lib.ig_pages_free_count(pages, C.byref(n)), "ig_pages_free_count")
+    return n.value
 
 
 def ig_append_kv_layers(stream, pool, layers, B, H, d, ks, Lcap, slot, cols, k_new, v_new, Kpart, Kdense=None,

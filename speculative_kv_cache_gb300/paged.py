@@ -1,0 +1,148 @@
+"""PagedCache: a paged KV cache in HBM over the C ABI (pages, page tables, forks, attention).
+
+It owns the pages of every layer, the host-side page manager (``ig_pages_*``) and the device copy
+of its tables, and runs a token's way through a layer: ``write`` (norm and rotation of q and k, the
+rows into their pages: ``ig_qk_norm_rope``) and ``attend`` (``ig_paged_attend``).  Sequences can be
+forked (pages shared until one writes), cut back, freed, and the pages packed (``ig_page_copy``).
+All device work is queued on torch's current stream.  The device tensors ``table`` and ``L`` stay in
+place, so a captured ``write`` + ``attend`` replays with what ``extend`` put there since.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+from . import ig
+
+_DTYPES = {torch.float16: ig.IG_F16, torch.bfloat16: ig.IG_BF16}
+
+
+class PagedCache:
+    def __init__(self, *, layers, Hq, Hkv, d, n_pages, seqs, max_pages, page=32, dtype=torch.float16, scale=None, rot=0,
+                 layout=ig.IG_ROPE_HALF, theta=10000.0, scaling=ig.IG_ROPE_PLAIN, factor=1.0, context=0, p0=0.0, p1=0.0,
+                 eps=1e-6, device="cuda:0"):
+        self.pages = None
+        self.layers, self.Hq, self.Hkv, self.d = layers, Hq, Hkv, d
+        self.n_pages, self.seqs, self.max_pages, self.page = n_pages, seqs, max_pages, page
+        self.dtype, self.dt = dtype, _DTYPES[dtype]
+        self.scale = float(scale if scale is not None else 1.0 / math.sqrt(d))
+        self.rot, self.layout, self.eps = rot, layout, eps
+        self.dev = torch.device(device)
+        torch.cuda.set_device(self.dev)
+        self.pages = ig.ig_pages_create(n_pages, page, seqs, max_pages)
+        shape = (n_pages, Hkv, page, d)
+        self.K = [torch.empty(shape, dtype=dtype, device=self.dev) for _ in range(layers)]
+        self.V = [torch.empty(shape, dtype=dtype, device=self.dev) for _ in range(layers)]
+        self.turns, self.rot_scale = None, 1.0
+        if rot:
+            turns = np.zeros(rot // 2, dtype=np.int64)
+            self.rot_scale = ig.ig_rope_turns(rot, theta, scaling, factor, context, p0, p1, turns)
+            self.turns = torch.from_numpy(turns).to(self.dev)
+        self.table_host = np.full((seqs, max_pages), -1, dtype=np.int32)
+        self.L_host = np.zeros(seqs, dtype=np.int32)
+        self.table = torch.full((seqs, max_pages), -1, dtype=torch.int32, device=self.dev)
+        self.L = torch.zeros(seqs, dtype=torch.int32, device=self.dev)
+        self.ws = torch.empty(ig.ig_paged_attend_workspace_bytes(seqs, Hq, Hkv, d), dtype=torch.uint8, device=self.dev)
+
+    # ------------------------------------------------------------------ the sequences
+    def _upload(self):
+        """The manager's tables and lengths, copied to the device (ordered on the current stream)."""
+        ig.ig_pages_table(self.pages, self.table_host, self.L_host)
+        self.table.copy_(torch.from_numpy(self.table_host))
+        self.L.copy_(torch.from_numpy(self.L_host))
+
+    def _run_moves(self, moves):
+        if len(moves):
+            m = torch.from_numpy(np.ascontiguousarray(moves, dtype=np.int32)).to(self.dev)
+            ig.ig_page_copy(None, self.layers, self.n_pages, self.Hkv, self.page, self.d, self.K, self.V, len(moves), m)
+
+    def extend(self, new):
+        """Room for ``new[sequence]`` more tokens of each named sequence; returns device int32 slots
+        and positions of the tokens, in that order.  Raises IGError (IG_ERR_CAPACITY) with nothing
+        changed when the pages or a table run out."""
+        slots, positions, moves, before = [], [], [], {}
+        failed = None
+        for seq, n in new.items():
+            s = np.empty(n, dtype=np.int32)
+            had = int(self.L_host[seq])
+            try:
+                move = ig.ig_pages_extend(self.pages, seq, n, s)
+            except ig.IGError as e:
+                failed = e
+                break
+            before[seq] = had
+            slots.append(s)
+            positions.append(np.arange(had, had + n, dtype=np.int32))
+            if move is not None:
+                moves.append(move)
+        if failed is not None:  # a page of its own that a sequence got stays with it, filled
+            for seq, had in before.items():
+                ig.ig_pages_truncate(self.pages, seq, had)
+        self._run_moves(moves)
+        self._upload()
+        if failed is not None:
+            raise failed
+        cat = lambda x: torch.from_numpy(np.concatenate(x) if x else np.empty(0, np.int32)).to(self.dev)  # noqa: E731
+        return cat(slots), cat(positions)
+
+    def fork(self, src, dst):
+        """Sequence ``dst`` (empty) becomes a copy of ``src``, sharing its pages."""
+        ig.ig_pages_fork(self.pages, src, dst)
+        self._upload()
+
+    def truncate(self, seq, n):
+        """Keeps the first ``n`` tokens of a sequence."""
+        ig.ig_pages_truncate(self.pages, seq, n)
+        self._upload()
+
+    def free(self, seq):
+        self.truncate(seq, 0)
+
+    def compact(self):
+        """Moves the used pages to the lowest numbers; returns how many moved."""
+        moves = np.empty((self.n_pages // 2 + 1, 3), dtype=np.int32)
+        n = ig.ig_pages_compact(self.pages, moves, len(moves))
+        self._run_moves(moves[:n])
+        self._upload()
+        return n
+
+    def free_pages(self):
+        return ig.ig_pages_free_count(self.pages)
+
+    # ------------------------------------------------------------------ a layer's step
+    def write(self, layer, q, k, v, slots, positions, q_weight=None, k_weight=None, q_out=None):
+        """Norms and rotates the tokens' q [T, Hq, d] and k [T, Hkv, d] and puts k and v [T, Hkv, d]
+        into ``layer``'s pages; returns the new q.  q, k and v may be slices of one projection
+        [T, heads * d] (the first dimension's stride is taken as it is)."""
+        T = q.shape[0]
+        if q_out is None:
+            q_out = torch.empty((T, self.Hq, self.d), dtype=self.dtype, device=self.dev)
+        # a lone row's stride may be anything: it is never used
+        qs, ks, vs = (x.stride(0) if T > 1 else h * self.d for x, h in ((q, self.Hq), (k, self.Hkv), (v, self.Hkv)))
+        ig.ig_qk_norm_rope(None, self.dt, T, self.Hq, self.Hkv, self.d, self.rot, self.layout, q, qs, k, ks, v, vs,
+                           q_weight, k_weight, self.eps, positions, self.turns, self.rot_scale, q_out, self.page,
+                           self.n_pages, slots, self.K[layer], self.V[layer])
+        return q_out
+
+    def attend(self, layer, q, out=None, lse=None):
+        """Attention of one token per sequence, q [seqs, Hq, d], over all its tokens: fp32
+        [seqs, Hq, d], zero for empty sequences."""
+        if out is None:
+            out = torch.empty((self.seqs, self.Hq, self.d), dtype=torch.float32, device=self.dev)
+        ig.ig_paged_attend(None, self.dt, self.seqs, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages,
+                           self.scale, q, self.K[layer], self.V[layer], self.table, self.L, out, lse, self.ws,
+                           self.ws.numel())
+        return out
+
+    def close(self):
+        if self.pages is not None:
+            ig.ig_pages_destroy(self.pages)
+            self.pages = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
