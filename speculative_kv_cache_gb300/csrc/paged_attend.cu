@@ -1,89 +1,762 @@
-// Attention of one new token over a paged KV cache.
+// Attention of one new token per sequence over a paged KV cache.
+//
+// Mathematics.  For a key/value head and the G = Hq / Hkv query heads that read it,
+//   z_t = scale q . K_t,  o = sum_t e^(z_t) V_t / sum_t e^(z_t)
+// in one pass over the tokens: every part of the tokens keeps its maximum m, l = sum e^(z - m) and
+// o = sum e^(z - m) V, and two parts join as m = max(m1, m2), l = sum l_i e^(m_i - m), o likewise.
+// Exponents are taken to base 2, with log2(e) folded into the scale.
+//
+// What bounds it.  Every key and value is read once from HBM and used by G queries: 4 d G flop for
+// 4 d bytes.  From G = 8 on that is more than the fp32 units do at HBM speed, so the products run
+// on the tensor cores (mma.sync: with at most 64 queries there is no 128-row tile for tcgen05 to
+// fill, and the copies, not the products, set the time).  Tokens are the 16 rows of an MMA, queries
+// its 8 columns: S^T = K Q^T, then O^T = V^T P^T, which costs no padding at G = 8 and at G = 1 leaves
+// the tensor cores far from full.
+//
+// Precision.  K, V, q enter as they are.  A weight in fp16 or bf16 alone would cost 2^-11 or 2^-8, so
+// it is split into 16-bit parts that are multiplied in turn: two for fp16 (scaled by 2^15 so that
+// the second part of a small weight stays normal; 22 bits), three for bf16 (24 bits).  Sums over the
+// tokens of one tile run in the tensor cores, which truncate; those over tiles in fp32 adds that
+// round to nearest, so that long sequences collect no bias.
+//
+// Work split.  The tokens of every (sequence, key head) are cut into tiles of 16 KB of keys and values,
+// and CTA c of G takes tiles [R c / G, R (c+1) / G) of all R, in sequence and head order: equal shares
+// whatever the lengths.  A head whose tiles lie in one CTA is finished there; a head cut by a CTA
+// boundary leaves one partial per CTA in the workspace (two slots per CTA: the head it starts with
+// and the head it ends with), joined in order by a second kernel, a programmatic dependent launch.
+// No atomics: the result does not depend on timing.
+//
+// A CTA is one producer warp and four consumer warps.  The producer walks the tiles, looks the
+// pages up one tile ahead, and moves each tile with TMA (a page's rows of one head are contiguous;
+// boxes of 64 columns, 128-byte swizzle) into a ring of stages; a stage is consumed by one warp (or,
+// for more than 16 queries, by as many warps as it takes, each with its own queries), the stages in
+// turn.  A warp folds its tiles into its own (m, l, o); the warps join where a head ends.
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include "ig_common.cuh"
+#include "tc_common.cuh"
 
 namespace ig {
 namespace {
 
-constexpr int kPaThreads = 128;
+constexpr int kPaWarps = 4;                       // consumer warps
+constexpr int kPaThreads = (kPaWarps + 1) * 32;   // and the producer
+constexpr int kPaCtasPerSm = 2;
+constexpr int kMaxPaCtas = 320;                   // upper bound of the grid (sizes the workspace)
+constexpr int kPaStageBytes = 16384;              // keys and values of one tile
+constexpr int kPaPartHead = 4;                    // a partial: [max, sum, -, -, output[D]]
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <int D>
+__host__ __device__ constexpr int pa_tokens() { return kPaStageBytes / (4 * D); }  // tokens of a tile: 32 or 64
+template <int NQ>
+__host__ __device__ constexpr int pa_stages() { return NQ == 1 ? 6 : 5; }  // two CTAs per SM
 
-// One CTA per (sequence, query head): thread i takes tokens i, i + kPaThreads, ... with a
-// running maximum, sum and output of its own, merged at the end.
-template <typename T, int D>
-__global__ void __launch_bounds__(kPaThreads) k_paged_attend(
-    const T* __restrict__ q, const T* __restrict__ K, const T* __restrict__ V, const int32_t* __restrict__ table,
-    const int32_t* __restrict__ L_valid, int Hq, int Hkv, int page, int n_pages, int max_pages, float scale,
-    float* __restrict__ out, float* __restrict__ lse, int* err) {
-  __shared__ float sm_m[kPaThreads], sm_l[kPaThreads], sm_o[kPaThreads];
-  const int b = blockIdx.x / Hq, h = blockIdx.x % Hq, hk = h / (Hq / Hkv);
-  int L = L_valid[b];
-  if (L < 0 || L > max_pages * page) {
-    if (threadIdx.x == 0) raise_error(err, IG_DEVERR_INDEX);
-    L = L < 0 ? 0 : max_pages * page;
-  }
-  const T* qr = q + ((size_t)b * Hq + h) * D;
-  float m = -INFINITY, l = 0.f, acc[D];
-#pragma unroll
-  for (int i = 0; i < D; ++i) acc[i] = 0.f;
-  for (int t = threadIdx.x; t < L; t += kPaThreads) {
-    const int g = table[(size_t)b * max_pages + t / page];
-    if (g < 0 || g >= n_pages) {
-      raise_error(err, IG_DEVERR_INDEX);
-      continue;
-    }
-    const size_t row = (((size_t)g * Hkv + hk) * page + t % page) * D;
-    float z = 0.f;
-    for (int i = 0; i < D; ++i) z = fmaf(to_f(qr[i]), to_f(K[row + i]), z);
-    z *= scale;
-    const float mn = fmaxf(m, z);
-    if (mn == -INFINITY) continue;
-    const float c = expf(m - mn), p = expf(z - mn);
-    l = l * c + p;
-#pragma unroll
-    for (int i = 0; i < D; ++i) acc[i] = fmaf(p, to_f(V[row + i]), acc[i] * c);
-    m = mn;
-  }
-  sm_m[threadIdx.x] = m;
-  sm_l[threadIdx.x] = l;
-  __syncthreads();
-  float M = -INFINITY, S = 0.f;
-  for (int i = 0; i < kPaThreads; ++i) M = fmaxf(M, sm_m[i]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int i = 0; i < kPaThreads; ++i) S += sm_l[i] * expf(sm_m[i] - base);
-  const float f = expf(m - base);
-  float* o = out + ((size_t)b * Hq + h) * D;
-#pragma unroll
-  for (int i = 0; i < D; ++i) {
-    sm_o[threadIdx.x] = acc[i] * f;
-    __syncthreads();
-    for (int w = kPaThreads / 2; w; w >>= 1) {
-      if (threadIdx.x < w) sm_o[threadIdx.x] += sm_o[threadIdx.x + w];
-      __syncthreads();
-    }
-    if (threadIdx.x == 0) o[i] = S == 0.f ? 0.f : sm_o[0] / S;
-    __syncthreads();
-  }
-  if (threadIdx.x == 0 && lse) lse[(size_t)b * Hq + h] = M + logf(S);
+// Where the work is: everything the kernels need beside the pointers.
+struct PaShape {
+  int B, Hq, Hkv, G, QT;   // G query heads per key head, in QT groups of the unit's rows
+  int page, n_pages, max_pages, box;  // box: rows of a TMA box, a power of two that divides page
+  float scale2;            // scale * log2(e)
+  int by_unit;             // info is indexed by unit (units <= CTAs) or by CTA
+};
+
+// shared memory behind the ring
+template <int D, int NQ>
+struct PaShared {
+  float merge[2][D / 16 * NQ * 4][32];       // joining warps' outputs, a lane's registers apart
+  float m[kPaWarps][NQ * 8], l[kPaWarps][NQ * 8];
+  unsigned long long valid[pa_stages<NQ>()]; // tokens of the stage that count
+  uint64_t full[pa_stages<NQ>()], empty[pa_stages<NQ>()];
+  int scan[kPaThreads / 32];
+  int start_b, start_off, total;
+  int abort;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
-template <typename T, int D>
-ig_status launch_paged(cudaStream_t st, int B, int Hq, int Hkv, int page, int n_pages, int max_pages, float scale,
-                       const uint16_t* q, const uint16_t* K, const uint16_t* V, const int32_t* table,
-                       const int32_t* L, float* out, float* lse) {
-  k_paged_attend<T, D><<<B * Hq, kPaThreads, 0, st>>>(
-      reinterpret_cast<const T*>(q), reinterpret_cast<const T*>(K), reinterpret_cast<const T*>(V), table, L, Hq, Hkv,
-      page, n_pages, max_pages, scale, out, lse, error_word());
+// c += a b, 16 x 8 x 16
+template <bool BF>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 as a pair of 16-bit values (x in the low half), and what the rounding left of them.
+template <bool BF>
+__device__ __forceinline__ uint32_t split2(float& x, float& y) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    x -= __low2float(h);
+    y -= __high2float(h);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(x, y);
+    x -= __low2float(h);
+    y -= __high2float(h);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPaWarps * 32) : "memory"); }
+
+// A wait that gives up together with the CTA's other waits.
+__device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  for (uint32_t i = 0; i < limit && !*abort; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
+// The tiles of a CTA's share, in order, head by head; all lanes of a warp walk together.
+template <int TT>
+struct PaWalk {
+  const int32_t* L_valid;
+  int B, per_seq, max_len;  // heads (times query groups) of a sequence; the table's length
+  int b, off, nt, L, left;  // sequence, tile in its work, tiles of a head, its length; tiles left
+  int base, len_here, len_next;
+
+  __device__ int bounded(int i) const {
+    const int v = i < B ? __ldg(L_valid + i) : 0;
+    return v < 0 ? 0 : v > max_len ? max_len : v;
+  }
+  __device__ void enter(int seq) {
+    b = seq;
+    L = __shfl_sync(0xffffffffu, len_here, seq - base);
+    nt = (L + TT - 1) / TT;
+  }
+  __device__ void start(int seq, int offset, int tiles) {
+    left = tiles;
+    off = offset;
+    base = seq;
+    const int lane = threadIdx.x & 31;
+    len_here = bounded(base + lane);
+    len_next = bounded(base + 32 + lane);
+    enter(seq);
+  }
+  // the head that the walk stands in
+  __device__ int unit() const { return off / nt; }
+  __device__ int tile() const { return off % nt; }
+  __device__ int run() const { return min(nt - off % nt, left); }
+  __device__ void advance(int n) {
+    left -= n;
+    off += n;
+    if (left <= 0 || off < nt * per_seq) return;
+    off = 0;
+    const int lane = threadIdx.x & 31;
+    unsigned more = __ballot_sync(0xffffffffu, len_here > 0 && base + lane > b);
+    while (!more) {  // tiles are left, so a sequence with tokens follows
+      base += 32;
+      len_here = len_next;
+      len_next = bounded(base + 32 + lane);
+      more = __ballot_sync(0xffffffffu, len_here > 0);
+      if (base >= B) break;
+    }
+    if (more) enter(base + __ffs(more) - 1);
+    else left = 0;
+  }
+};
+
+template <bool BF, int D, int NQ, int WQ>
+__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) k_paged_attend(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+    const uint16_t* __restrict__ q, const int32_t* __restrict__ table, const int32_t* __restrict__ L_valid,
+    const PaShape s, float* __restrict__ out, float* __restrict__ lse, float* __restrict__ part,
+    int2* __restrict__ info, int* err) {
+  constexpr int TT = pa_tokens<D>(), MT = TT / 16, NS = pa_stages<NQ>(), HALVES = D / 64;
+  constexpr int RU = 8 * NQ * WQ;          // query rows of a unit
+  constexpr int TG = kPaWarps / WQ;        // warps that take stages in turn
+  constexpr int PARTS = BF ? 3 : 2;        // 16-bit parts of a weight
+  constexpr uint32_t kHalfBytes = TT * 128, kKvBytes = kPaStageBytes / 2;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                         ~static_cast<uintptr_t>(1023));
+  auto& sh = *reinterpret_cast<PaShared<D, NQ>*>(ring + NS * kPaStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_seq = s.Hkv * s.QT, max_len = s.max_pages * s.page;
+  pdl_trigger();
+
+  // ---- this CTA's share of all tiles, and the sequence it starts in
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], WQ);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  const int per = (s.B + kPaThreads - 1) / kPaThreads;
+  const int b0 = min(s.B, (int)threadIdx.x * per), b1 = min(s.B, b0 + per);
+  auto tiles_of = [&](int b) -> int {
+    int L = __ldg(L_valid + b);
+    if (L < 0 || L > max_len) {
+      raise_error(err, IG_DEVERR_INDEX);
+      L = L < 0 ? 0 : max_len;
+    }
+    return (L + TT - 1) / TT * per_seq;
+  };
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sh.scan[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPaThreads / 32; ++w) {
+    before += w < warp ? sh.scan[w] : 0;
+    total += sh.scan[w];
+  }
+  // with fewer tiles than CTAs the first `ctas` get one each
+  const int ctas = min((int)gridDim.x, total), cta = blockIdx.x;
+  int r0 = 0, r1 = 0;
+  if (cta < ctas) {
+    r0 = (int)((long long)total * cta / ctas);
+    r1 = (int)((long long)total * (cta + 1) / ctas);
+    if (r0 >= before && r0 < before + mine) {  // in this thread's sequences
+      int at = before;
+      for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(b);
+        if (r0 < at + n) {
+          sh.start_b = b;
+          sh.start_off = r0 - at;
+          break;
+        }
+        at += n;
+      }
+    }
+  }
+  __syncthreads();
+  PaWalk<TT> w;
+  w.L_valid = L_valid;
+  w.B = s.B;
+  w.per_seq = per_seq;
+  w.max_len = max_len;
+  w.b = w.off = w.L = w.left = 0;
+  w.nt = 1;
+  if (r1 > r0) w.start(sh.start_b, sh.start_off, r1 - r0);
+
+  if (warp == kPaWarps) {
+    // ---- producer.  Lane i < boxes * 2 * HALVES moves one box: K or V, a half of the columns.
+    const int box = lane / (2 * HALVES), is_v = (lane / HALVES) & 1, half = lane % HALVES;
+    const int boxes = TT / s.box;
+    const int box_tokens = box * s.box;
+    auto page_of = [&](const PaWalk<TT>& at) -> int {  // the lane's page number, -1: nothing to move
+      const int t = at.tile() * TT + box_tokens;
+      if (at.left <= 0 || box >= boxes || t >= at.L) return -1;
+      const int g = __ldg(table + (size_t)at.b * s.max_pages + t / s.page);
+      return g;
+    };
+    uint32_t it = 0;
+    int g = page_of(w);
+    while (w.left > 0) {
+      const int tile = w.tile(), hk = w.unit() / s.QT, n = min(TT, w.L - tile * TT);
+      const bool want = box < boxes && box_tokens < n;
+      const int t = tile * TT + box_tokens;
+      const int mine_g = g;
+      w.advance(1);
+      g = page_of(w);  // the next tile's pages, while this one's stage is waited for
+      const bool ok = want && mine_g >= 0 && mine_g < s.n_pages;
+      if (want && !ok) raise_error(err, IG_DEVERR_INDEX);
+      const uint32_t st = it % NS, r = it / NS;
+      const bool freed = r == 0 || pa_wait(&sh.empty[st], (r - 1) & 1, &sh.abort, (uint32_t)kDefaultWaitIters);
+      if (!__all_sync(0xffffffffu, freed)) {  // one verdict for the warp
+        if (lane == 0) {
+          sh.abort = 1;
+          raise_error(err, IG_DEVERR_TIMEOUT);
+        }
+        break;
+      }
+      const unsigned moving = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, want && !ok);
+      if (lane == 0) {
+        unsigned long long v = n >= 64 ? ~0ull : (1ull << n) - 1;
+        for (unsigned m = bad; m; m &= m - 1) {
+          const int bt = (__ffs(m) - 1) / (2 * HALVES) * s.box;
+          v &= ~(((s.box >= 64 ? 0ull : 1ull << s.box) - 1) << bt);
+        }
+        sh.valid[st] = v;
+        mbar_arrive_expect_tx(&sh.full[st], (uint32_t)__popc(moving) * s.box * 128);
+      }
+      __syncwarp();
+      if (ok) {
+        const int row = (mine_g * s.Hkv + hk) * s.page + t % s.page;
+        tma_load_2d(ring + st * kPaStageBytes + is_v * kKvBytes + half * kHalfBytes + box_tokens * 128,
+                    is_v ? &map_v : &map_k, half * 64, row, &sh.full[st]);
+      }
+      ++it;
+    }
+    __syncwarp();
+    if (*(volatile int*)&sh.abort)  // let the copies already issued land before the CTA leaves
+      for (uint32_t st = 0; st < NS && st < it; ++st)
+        mbar_wait_bounded(&sh.full[st], ((it - 1 - st) / NS) & 1, 1u << 16);
+  } else {
+    // ---- consumers: warp = tg + TG * wq takes stages tg, tg + TG, ... for query rows wq
+    const int tg = warp % TG, wq = warp / TG;
+    const int gl = lane >> 2, tl = lane & 3;  // fragment row and column pair
+    const uint32_t limit = wait_limit(err);
+    // ldmatrix rows of this lane: keys (16 tokens x 16 columns), values transposed
+    const uint32_t k_row = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128, k_chunk = lane >> 4;
+    const uint32_t v_row = ((lane & 7) + (lane >> 4) * 8) * 128, v_chunk = (lane >> 3) & 1;
+    const uint32_t swz = lane & 7;
+    uint32_t it = 0;  // tile of this CTA
+    bool cut_one = false;
+    while (w.left > 0) {
+      const int u_in = w.unit(), hk = u_in / s.QT, qt = u_in % s.QT, b = w.b;
+      const int tile0 = w.tile(), nt = w.nt, run = w.run();
+      const int qrow = qt * RU + wq * 8 * NQ;  // of this warp, within the key head's G
+      const uint16_t* qp = q + ((size_t)b * s.Hq + (size_t)hk * s.G + qrow) * D;
+      uint32_t qf[D / 16][NQ][2];
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          const bool in = qrow + j * 8 + gl < s.G;
+          const uint16_t* p = qp + (size_t)(j * 8 + gl) * D + ks * 16 + tl * 2;
+          qf[ks][j][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+          qf[ks][j][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(p + 8)) : 0u;
+        }
+      float m[NQ][2], l[NQ][2], o[D / 16][NQ][4];
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        m[j][0] = m[j][1] = -INFINITY;
+        l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
+      }
+      // this warp's stages of the run
+      for (uint32_t x = it + (tg + TG - it % TG) % TG; x < it + run; x += TG) {
+        const uint32_t st = x % NS;
+        if (!pa_wait(&sh.full[st], (x / NS) & 1, &sh.abort, limit)) {
+          if (lane == 0 && !atomicExch(&sh.abort, 1)) raise_error(err, IG_DEVERR_TIMEOUT);
+          // the walk goes on without waiting, so that every warp meets the others' barriers
+        }
+        __syncwarp();
+        const uint32_t kb = smem_addr(ring + st * kPaStageBytes), vb = kb + kKvBytes;
+        const unsigned long long valid = sh.valid[st];
+        const bool whole = valid == (TT == 64 ? ~0ull : (1ull << TT) - 1);
+        float z[MT][NQ][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) z[i][j][0] = z[i][j][1] = z[i][j][2] = z[i][j][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t a[4];
+            ldsm4(a, kb + (ks / 4) * kHalfBytes + i * 2048 + k_row + ((((ks % 4) * 2 + k_chunk) ^ swz) << 4));
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) mma16816<BF>(z[i][j], a, qf[ks][j][0], qf[ks][j][1]);
+          }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[i][j][e] *= s.scale2;
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool in = (valid >> (i * 16 + gl + (e >> 1) * 8)) & 1;
+#pragma unroll
+              for (int j = 0; j < NQ; ++j) z[i][j][e] = in ? z[i][j][e] : -INFINITY;
+            }
+        }
+        // the running maximum; most tiles of a long sequence leave it as it is
+        float tm[NQ][2];
+        bool more = false;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x2 = fmaxf(z[0][j][e], z[0][j][e + 2]);
+#pragma unroll
+            for (int i = 1; i < MT; ++i) x2 = fmaxf(x2, fmaxf(z[i][j][e], z[i][j][e + 2]));
+            tm[j][e] = x2;
+            more |= x2 > m[j][e];
+          }
+        float corr[NQ][2];
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) corr[j][0] = corr[j][1] = 1.f;
+        if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x2 = tm[j][e];
+#pragma unroll
+              for (int sh2 = 4; sh2 < 32; sh2 <<= 1) x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, sh2));
+              const float mn = fmaxf(m[j][e], x2);
+              corr[j][e] = mn == -INFINITY ? 1.f : ex2(m[j][e] - mn);
+              m[j][e] = mn;
+              l[j][e] *= corr[j][e];
+            }
+        }
+        // the weights, as 16-bit parts in the layout of the second product's operand
+        uint32_t p[PARTS][MT][NQ][2];
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) {
+          const float m0 = m[j][0] == -INFINITY ? 0.f : m[j][0], m1 = m[j][1] == -INFINITY ? 0.f : m[j][1];
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              float x0 = ex2(z[i][j][2 * hh] - m0), x1 = ex2(z[i][j][2 * hh + 1] - m1);
+              if constexpr (!BF) {
+                x0 *= 32768.f;
+                x1 *= 32768.f;
+              }
+              l[j][0] += x0;
+              l[j][1] += x1;
+#pragma unroll
+              for (int pp = 0; pp < PARTS; ++pp) p[pp][i][j][hh] = transpose8(split2<BF>(x0, x1));
+            }
+        }
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+          float acc[NQ][4];
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            uint32_t a[4];
+            ldsm4_t(a, vb + (dt / 4) * kHalfBytes + i * 2048 + v_row + ((((dt % 4) * 2 + v_chunk) ^ swz) << 4));
+            if (!whole) {  // rows that do not count may hold anything: zero times NaN is NaN
+              const unsigned v0 = (unsigned)(valid >> (i * 16 + tl * 2)) & 3u, v1 = (unsigned)(valid >> (i * 16 + 8 + tl * 2)) & 3u;
+              const uint32_t k0 = (v0 & 1 ? 0xffffu : 0u) | (v0 & 2 ? 0xffff0000u : 0u);
+              const uint32_t k1 = (v1 & 1 ? 0xffffu : 0u) | (v1 & 2 ? 0xffff0000u : 0u);
+              a[0] &= k0;
+              a[1] &= k0;
+              a[2] &= k1;
+              a[3] &= k1;
+            }
+#pragma unroll
+            for (int pp = 0; pp < PARTS; ++pp)
+#pragma unroll
+              for (int j = 0; j < NQ; ++j) mma16816<BF>(acc[j], a, p[pp][i][j][0], p[pp][i][j][1]);
+          }
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[dt][j][e] = fmaf(o[dt][j][e], corr[j][e & 1], acc[j][e]);
+        }
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(&sh.empty[st])) : "memory");
+      }
+      it += run;
+      // ---- the head's end in this CTA: the sums of a query's lanes, then the warps
+#pragma unroll
+      for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int sh2 = 4; sh2 < 32; sh2 <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], sh2);
+      if constexpr (TG > 1) {
+        if (gl == 0)
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              sh.m[warp][j * 8 + tl * 2 + e] = m[j][e];
+              sh.l[warp][j * 8 + tl * 2 + e] = l[j][e];
+            }
+        consumer_sync();
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int c = j * 8 + tl * 2 + e;
+            float M = -INFINITY, Ls = 0.f;
+#pragma unroll
+            for (int x = 0; x < TG; ++x) M = fmaxf(M, sh.m[wq * TG + x][c]);
+            const float m0 = M == -INFINITY ? 0.f : M;
+#pragma unroll
+            for (int x = 0; x < TG; ++x) Ls += sh.l[wq * TG + x][c] * ex2(sh.m[wq * TG + x][c] - m0);
+            const float f = ex2(m[j][e] - m0);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][j][e] *= f;
+              o[i][j][e + 2] *= f;
+            }
+            m[j][e] = M;
+            l[j][e] = Ls;
+          }
+        // (w0 + w2) + (w1 + w3), or w0 + w1
+#pragma unroll
+        for (int step = TG / 2; step >= 1; step >>= 1) {
+          const int slot = TG == 4 ? tg % 2 : wq;
+          if (tg >= step && tg < 2 * step)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sh.merge[slot][(i * NQ + j) * 4 + e][lane] = o[i][j][e];
+          consumer_sync();
+          if (tg < step) {
+            const int from = TG == 4 ? (tg + step) % 2 : wq;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][j][e] += sh.merge[from][(i * NQ + j) * 4 + e][lane];
+          }
+          if (step > 1) consumer_sync();
+        }
+      }
+      const bool done = tile0 == 0 && run == nt;  // the whole head was here
+      const int unit = b * per_seq + u_in;
+      if (tg == 0) {
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = wq * 8 * NQ + j * 8 + tl * 2 + e, qi = qt * RU + row;
+            if (qi >= s.G) continue;
+            if (done) {
+              const size_t at = (size_t)b * s.Hq + (size_t)hk * s.G + qi;
+              const float inv = l[j][e] == 0.f ? 0.f : 1.f / l[j][e];
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                out[at * D + i * 16 + gl] = o[i][j][e] * inv;
+                out[at * D + i * 16 + 8 + gl] = o[i][j][e + 2] * inv;
+              }
+              if (lse && gl == 0) lse[at] = (m[j][e] + log2f(l[j][e]) - (BF ? 0.f : 15.f)) * 0.6931471805599453f;
+            } else {
+              // the head it starts with, begun by an earlier CTA, to slot 0; one it begins to slot 1
+              float* wp = part + ((size_t)(2 * cta + (tile0 == 0 ? 1 : 0)) * RU + row) * (D + kPaPartHead);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                wp[kPaPartHead + i * 16 + gl] = o[i][j][e];
+                wp[kPaPartHead + i * 16 + 8 + gl] = o[i][j][e + 2];
+              }
+              if (gl == 0) {
+                wp[0] = m[j][e];
+                wp[1] = l[j][e];
+              }
+            }
+          }
+      }
+      // what the second kernel joins: a head that begins here and goes on in later CTAs
+      if (threadIdx.x == 0) {
+        const bool cut = tile0 == 0 && !done;
+        if (cut || (s.by_unit && done)) {
+          int last = cta;  // the CTA that holds the head's last tile
+          if (cut) {
+            const long long end = (long long)r1 - run + nt - 1;  // a cut head is this CTA's last
+            last = (int)(end * ctas / total);
+            while (last + 1 < ctas && (long long)total * (last + 1) / ctas <= end) ++last;
+            while ((long long)total * last / ctas > end) --last;
+          }
+          if (s.by_unit) info[unit] = make_int2(cut ? cta : -1, last);
+          else info[cta] = make_int2(unit, last);
+          cut_one = true;
+        }
+      }
+      w.advance(run);
+    }
+    if (threadIdx.x == 0 && !s.by_unit && !cut_one) info[cta] = make_int2(-1, 0);
+    // sequences without a token
+    for (int b = cta; b < s.B; b += gridDim.x) {
+      if (__ldg(L_valid + b) > 0) continue;
+      for (int i = threadIdx.x; i < s.Hq * D / 4; i += kPaWarps * 32)
+        reinterpret_cast<float4*>(out + (size_t)b * s.Hq * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (lse)
+        for (int i = threadIdx.x; i < s.Hq; i += kPaWarps * 32) lse[(size_t)b * s.Hq + i] = -INFINITY;
+      if (s.by_unit)
+        for (int i = threadIdx.x; i < per_seq; i += kPaWarps * 32) info[b * per_seq + i] = make_int2(-1, 0);
+    }
+  }
+  __syncthreads();
+}
+
+// Joins the partials of the heads that were cut: block (x, y) takes unit x (or the head that CTA x
+// began) and rows y * RB ... of it; a row's partials are spread over the 8 / RB warps it has, taken
+// in order, and the warps join in order.
+constexpr int kPjWarps = 8;
+template <int D, int RB>
+__global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const float* __restrict__ part, const int2* __restrict__ info,
+                                                             const PaShape s, int RU, float scale_bits,
+                                                             float* __restrict__ out, float* __restrict__ lse) {
+  constexpr int VEC = D / 32, WPR = kPjWarps / RB;
+  __shared__ float sm[kPjWarps], sl[kPjWarps], so[kPjWarps][D];
+  pdl_wait();
+  const int2 e = info[blockIdx.x];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (e.x < 0) return;
+  const int unit = s.by_unit ? (int)blockIdx.x : e.x, c0 = s.by_unit ? e.x : (int)blockIdx.x;
+  const int per_seq = s.Hkv * s.QT, b = unit / per_seq, hk = unit % per_seq / s.QT, qt = unit % s.QT;
+  const int row = blockIdx.y * RB + warp / WPR, qi = qt * RU + row, n = e.y - c0 + 1;
+  const bool live = row < RU && qi < s.G;
+  float m = -INFINITY, l = 0.f, o[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) o[i] = 0.f;
+  if (live) {
+    // U partials' loads in flight
+    constexpr int U = 4;
+    for (int j0 = warp % WPR; j0 < n; j0 += WPR * U) {
+      float pm[U], pl[U], po[U][VEC];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const int j = j0 + x * WPR;
+        pm[x] = -INFINITY;
+        pl[x] = 0.f;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) po[x][i] = 0.f;
+        if (j < n) {
+          const float* p = part + ((size_t)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * RU + row) * (D + kPaPartHead);
+          const float2 h = *reinterpret_cast<const float2*>(p);
+          pm[x] = h.x;
+          pl[x] = h.y;
+#pragma unroll
+          for (int i = 0; i < VEC; i += 2) {
+            const float2 y = *reinterpret_cast<const float2*>(p + kPaPartHead + lane * VEC + i);
+            po[x][i] = y.x;
+            po[x][i + 1] = y.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        const float mn = fmaxf(m, pm[x]), m0 = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - m0), g = ex2(pm[x] - m0);
+        l = l * f + pl[x] * g;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) o[i] = o[i] * f + po[x][i] * g;
+        m = mn;
+      }
+    }
+  }
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) so[warp][lane * VEC + i] = o[i];
+    __syncthreads();
+    if (warp % WPR) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) m = fmaxf(m, sm[warp + x]);
+    const float m0 = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) {
+      const float f = ex2(sm[warp + x] - m0);
+      l += sl[warp + x] * f;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] += so[warp + x][lane * VEC + i] * f;
+    }
+  }
+  if (!live) return;
+  const size_t at = (size_t)b * s.Hq + (size_t)hk * s.G + qi;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) out[at * D + lane * VEC + i] = o[i] * inv;
+  if (lse && lane == 0) lse[at] = (m + log2f(l) - scale_bits) * 0.6931471805599453f;
+}
+
+// query rows of a unit: 8 per MMA column tile, up to two tiles a warp, then more warps
+inline int pa_rows(int G) { return G <= 8 ? 8 : G <= 16 ? 16 : G <= 32 ? 32 : 64; }
+
+// workspace: two partials per CTA, then the join's list
+inline size_t pa_part_bytes(int G, int d) {
+  return round_up((size_t)2 * kMaxPaCtas * pa_rows(G) * (d + kPaPartHead) * sizeof(float), 256);
+}
+inline size_t pa_info_bytes() { return round_up((size_t)kMaxPaCtas * sizeof(int2), 256); }
+
+template <bool BF, int D, int NQ, int WQ>
+ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint16_t* K, const uint16_t* V,
+                       const int32_t* table, const int32_t* L, float* out, float* lse, void* ws) {
+  constexpr int RU = 8 * NQ * WQ, TT = pa_tokens<D>();
+  s.QT = (s.G + RU - 1) / RU;
+  s.box = TT;
+  while (s.page % s.box) s.box >>= 1;
+  const long long most = (long long)s.B * ((s.max_pages * s.page + TT - 1) / TT) * s.Hkv * s.QT;
+  IG_REQUIRE(most < (1ll << 31), "B*max_pages*page*Hkv is too large: %lld tiles", most);
+  const int rows = s.n_pages * s.Hkv * s.page;
+  CUtensorMap mk, mv;
+  ig_status r = make_map(&mk, K, rows, D, s.box);
+  if (r == IG_OK) r = make_map(&mv, V, rows, D, s.box);
+  if (r != IG_OK) return r;
+  constexpr size_t smem = 1024 + (size_t)pa_stages<NQ>() * kPaStageBytes + sizeof(PaShared<D, NQ>);
+  cudaError_t e = cudaFuncSetAttribute(k_paged_attend<BF, D, NQ, WQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention smem attribute");
+  int grid = kPaCtasPerSm * sm_count(st);
+  if (grid > kMaxPaCtas) grid = kMaxPaCtas;
+  if (grid > most) grid = (int)most;
+  const long long units = (long long)s.B * s.Hkv * s.QT;
+  s.by_unit = units <= grid ? 1 : 0;
+  float* part = static_cast<float*>(ws);
+  int2* info = reinterpret_cast<int2*>(static_cast<char*>(ws) + pa_part_bytes(s.G, D));
+  k_paged_attend<BF, D, NQ, WQ><<<grid, kPaThreads, smem, st>>>(mk, mv, q, table, L, s, out, lse, part, info,
+                                                               error_word());
   IG_CHECK_LAUNCH("paged attention launch");
+  if (grid == 1) return IG_OK;  // nothing was cut
+  // a row's partials are many only when there are few units: then a row gets a whole block
+  const int rows_used = s.G < RU ? s.G : RU, list = s.by_unit ? (int)units : grid;
+  const float bits = BF ? 0.f : 15.f;
+  const float* cpart = part;
+  const int2* cinfo = info;
+  if (grid >= 16 * units)
+    e = launch_pdl(k_paged_join<D, 1>, dim3(list, rows_used), dim3(kPjWarps * 32), 0, st, cpart, cinfo, s, RU, bits, out,
+                   lse);
+  else
+    e = launch_pdl(k_paged_join<D, kPjWarps>, dim3(list, (rows_used + kPjWarps - 1) / kPjWarps), dim3(kPjWarps * 32), 0,
+                   st, cpart, cinfo, s, RU, bits, out, lse);
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention join launch");
+  IG_CHECK_LAUNCH("paged attention join launch");
   return IG_OK;
+}
+
+template <bool BF, int D>
+ig_status launch_rows(cudaStream_t st, const PaShape& s, const uint16_t* q, const uint16_t* K, const uint16_t* V,
+                      const int32_t* table, const int32_t* L, float* out, float* lse, void* ws) {
+  switch (pa_rows(s.G)) {
+    case 8: return launch_paged<BF, D, 1, 1>(st, s, q, K, V, table, L, out, lse, ws);
+    case 16: return launch_paged<BF, D, 2, 1>(st, s, q, K, V, table, L, out, lse, ws);
+    case 32: return launch_paged<BF, D, 2, 2>(st, s, q, K, V, table, L, out, lse, ws);
+    default: return launch_paged<BF, D, 2, 4>(st, s, q, K, V, table, L, out, lse, ws);
+  }
 }
 
 }  // namespace
@@ -93,7 +766,7 @@ using namespace ig;
 
 extern "C" size_t ig_paged_attend_workspace_bytes(int B, int Hq, int Hkv, int d) {
   if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (d != 64 && d != 128)) return 0;
-  return 256;
+  return pa_part_bytes(Hq / Hkv, d) + pa_info_bytes();
 }
 
 extern "C" ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page, int n_pages,
@@ -119,14 +792,19 @@ extern "C" ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int
   if (!workspace || workspace_bytes < need)
     return fail(IG_ERR_CAPACITY, "paged attention needs %zu workspace bytes", need);
   IG_REQUIRE(aligned(workspace, 256), "workspace must be 256-byte aligned");
-  cudaStream_t s = as_stream(stream);
-#define IG_PA(T, D) \
-  return launch_paged<T, D>(s, B, Hq, Hkv, page, n_pages, max_pages, scale, q, K, V, page_table, L_valid, out, lse)
-  if (dtype == IG_F16) {
-    if (d == 128) IG_PA(__half, 128);
-    IG_PA(__half, 64);
-  }
-  if (d == 128) IG_PA(__nv_bfloat16, 128);
-  IG_PA(__nv_bfloat16, 64);
-#undef IG_PA
+  cudaStream_t st = as_stream(stream);
+  PaShape s{};
+  s.B = B;
+  s.Hq = Hq;
+  s.Hkv = Hkv;
+  s.G = Hq / Hkv;
+  s.page = page;
+  s.n_pages = n_pages;
+  s.max_pages = max_pages;
+  s.scale2 = scale * 1.4426950408889634f;
+  if (dtype == IG_F16)
+    return d == 128 ? launch_rows<false, 128>(st, s, q, K, V, page_table, L_valid, out, lse, workspace)
+                    : launch_rows<false, 64>(st, s, q, K, V, page_table, L_valid, out, lse, workspace);
+  return d == 128 ? launch_rows<true, 128>(st, s, q, K, V, page_table, L_valid, out, lse, workspace)
+                  : launch_rows<true, 64>(st, s, q, K, V, page_table, L_valid, out, lse, workspace);
 }
