@@ -26,7 +26,7 @@
 // and the head it ends with), joined in order by a second kernel, a programmatic dependent launch.
 // No atomics: the result does not depend on timing.
 //
-// A CTA is one producer warp and four consumer warps.  The producer walks the tiles, looks the
+// A CTA is one producer warp and three or four consumer warps.  The producer walks the tiles, looks the
 // pages up one tile ahead, and moves each tile with TMA (a page's rows of one head are contiguous;
 // boxes of 64 columns, 128-byte swizzle) into a ring of stages; a stage is consumed by one warp (or,
 // for more than 16 queries, by as many warps as it takes, each with its own queries), the stages in
@@ -40,8 +40,6 @@
 namespace ig {
 namespace {
 
-constexpr int kPaWarps = 4;                       // consumer warps
-constexpr int kPaThreads = (kPaWarps + 1) * 32;   // and the producer
 constexpr int kPaCtasPerSm = 2;
 constexpr int kMaxPaCtas = 320;                   // upper bound of the grid (sizes the workspace)
 constexpr int kPaStageBytes = 16384;              // keys and values of one tile
@@ -49,8 +47,13 @@ constexpr int kPaPartHead = 4;                    // a partial: [max, sum, -, -,
 
 template <int D>
 __host__ __device__ constexpr int pa_tokens() { return kPaStageBytes / (4 * D); }  // tokens of a tile: 32 or 64
-template <int NQ>
-__host__ __device__ constexpr int pa_stages() { return NQ == 1 ? 6 : 5; }  // two CTAs per SM
+// warps that take stages in turn, and stages: a multiple of them, so that a stage is always the
+// same warps' (a warp that skipped a phase of a stage's barrier could not tell the phases' parity)
+__host__ __device__ constexpr int pa_turns(int WQ) { return WQ == 1 ? 3 : WQ == 2 ? 2 : 1; }
+__host__ __device__ constexpr int pa_stages(int WQ) { return WQ == 2 ? 4 : 6; }  // two CTAs per SM
+__host__ __device__ constexpr int pa_threads(int WQ) { return (pa_turns(WQ) * WQ + 1) * 32; }
+// joining warps' outputs held at once, per group of queries
+__host__ __device__ constexpr int pa_slots(int NQ, int WQ) { return pa_turns(WQ) == 1 ? 0 : NQ == 1 ? 2 : 1; }
 
 // Where the work is: everything the kernels need beside the pointers.
 struct PaShape {
@@ -61,13 +64,13 @@ struct PaShape {
 };
 
 // shared memory behind the ring
-template <int D, int NQ>
+template <int D, int NQ, int WQ>
 struct PaShared {
-  float merge[2][D / 16 * NQ * 4][32];       // joining warps' outputs, a lane's registers apart
-  float m[kPaWarps][NQ * 8], l[kPaWarps][NQ * 8];
-  unsigned long long valid[pa_stages<NQ>()]; // tokens of the stage that count
-  uint64_t full[pa_stages<NQ>()], empty[pa_stages<NQ>()];
-  int scan[kPaThreads / 32];
+  float merge[pa_slots(NQ, WQ) ? pa_slots(NQ, WQ) * WQ : 1][D / 16 * NQ * 4][32];  // a lane's registers apart
+  float m[pa_turns(WQ) * WQ][NQ * 8], l[pa_turns(WQ) * WQ][NQ * 8];
+  unsigned long long valid[pa_stages(WQ)];  // tokens of the stage that count
+  uint64_t full[pa_stages(WQ)], empty[pa_stages(WQ)];
+  int scan[pa_threads(WQ) / 32];
   int start_b, start_off, total;
   int abort;
 };
@@ -125,7 +128,10 @@ __device__ __forceinline__ uint32_t split2(float& x, float& y) {
   }
 }
 
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kPaWarps * 32) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 // A wait that gives up together with the CTA's other waits.
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
@@ -184,20 +190,22 @@ struct PaWalk {
 };
 
 template <bool BF, int D, int NQ, int WQ>
-__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) k_paged_attend(
+__global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
     const uint16_t* __restrict__ q, const int32_t* __restrict__ table, const int32_t* __restrict__ L_valid,
     const PaShape s, float* __restrict__ out, float* __restrict__ lse, float* __restrict__ part,
     int2* __restrict__ info, int* err) {
-  constexpr int TT = pa_tokens<D>(), MT = TT / 16, NS = pa_stages<NQ>(), HALVES = D / 64;
+  constexpr int TT = pa_tokens<D>(), MT = TT / 16, NS = pa_stages(WQ), HALVES = D / 64;
   constexpr int RU = 8 * NQ * WQ;          // query rows of a unit
-  constexpr int TG = kPaWarps / WQ;        // warps that take stages in turn
+  constexpr int TG = pa_turns(WQ);         // warps that take stages in turn
+  constexpr int kPaThreads = pa_threads(WQ), kPaWarps = TG * WQ, SLOTS = pa_slots(NQ, WQ);
+  static_assert(NS % TG == 0, "a stage is always the same warps'");
   constexpr int PARTS = BF ? 3 : 2;        // 16-bit parts of a weight
   constexpr uint32_t kHalfBytes = TT * 128, kKvBytes = kPaStageBytes / 2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
-  auto& sh = *reinterpret_cast<PaShared<D, NQ>*>(ring + NS * kPaStageBytes);
+  auto& sh = *reinterpret_cast<PaShared<D, NQ, WQ>*>(ring + NS * kPaStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_seq = s.Hkv * s.QT, max_len = s.max_pages * s.page;
   pdl_trigger();
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) k_paged_attend(
               sh.m[warp][j * 8 + tl * 2 + e] = m[j][e];
               sh.l[warp][j * 8 + tl * 2 + e] = l[j][e];
             }
-        consumer_sync();
+        consumer_sync<kPaWarps * 32>();
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -515,28 +523,27 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) k_paged_attend(
             m[j][e] = M;
             l[j][e] = Ls;
           }
-        // (w0 + w2) + (w1 + w3), or w0 + w1
+        // into warp tg = 0, in the warps' order
 #pragma unroll
-        for (int step = TG / 2; step >= 1; step >>= 1) {
-          const int slot = TG == 4 ? tg % 2 : wq;
-          if (tg >= step && tg < 2 * step)
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-              for (int j = 0; j < NQ; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sh.merge[slot][(i * NQ + j) * 4 + e][lane] = o[i][j][e];
-          consumer_sync();
-          if (tg < step) {
-            const int from = TG == 4 ? (tg + step) % 2 : wq;
+        for (int from = 1; from < TG; from += SLOTS) {
+          if (tg >= from && tg < from + SLOTS)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
 #pragma unroll
               for (int j = 0; j < NQ; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][j][e] += sh.merge[from][(i * NQ + j) * 4 + e][lane];
-          }
-          if (step > 1) consumer_sync();
+                for (int e = 0; e < 4; ++e) sh.merge[wq * SLOTS + tg - from][(i * NQ + j) * 4 + e][lane] = o[i][j][e];
+          consumer_sync<kPaWarps * 32>();
+          if (tg == 0)
+#pragma unroll
+            for (int x = 0; x < SLOTS && from + x < TG; ++x)
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[i][j][e] += sh.merge[wq * SLOTS + x][(i * NQ + j) * 4 + e][lane];
+          if (from + SLOTS < TG) consumer_sync<kPaWarps * 32>();
         }
       }
       const bool done = tile0 == 0 && run == nt;  // the whole head was here
@@ -717,7 +724,7 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
   ig_status r = make_map(&mk, K, rows, D, s.box);
   if (r == IG_OK) r = make_map(&mv, V, rows, D, s.box);
   if (r != IG_OK) return r;
-  constexpr size_t smem = 1024 + (size_t)pa_stages<NQ>() * kPaStageBytes + sizeof(PaShared<D, NQ>);
+  constexpr size_t smem = 1024 + (size_t)pa_stages(WQ) * kPaStageBytes + sizeof(PaShared<D, NQ, WQ>);
   cudaError_t e = cudaFuncSetAttribute(k_paged_attend<BF, D, NQ, WQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return cuda_fail(e, "paged attention smem attribute");
@@ -728,7 +735,7 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
   s.by_unit = units <= grid ? 1 : 0;
   float* part = static_cast<float*>(ws);
   int2* info = reinterpret_cast<int2*>(static_cast<char*>(ws) + pa_part_bytes(s.G, D));
-  k_paged_attend<BF, D, NQ, WQ><<<grid, kPaThreads, smem, st>>>(mk, mv, q, table, L, s, out, lse, part, info,
+  k_paged_attend<BF, D, NQ, WQ><<<grid, pa_threads(WQ), smem, st>>>(mk, mv, q, table, L, s, out, lse, part, info,
                                                                error_word());
   IG_CHECK_LAUNCH("paged attention launch");
   if (grid == 1) return IG_OK;  // nothing was cut

@@ -153,7 +153,8 @@ def test_attend_head_layouts(ig, Hq, Hkv, dt, d):
 
 @pytest.mark.parametrize("B,Hq,Hkv,d,page,dt,hi", [(1, 8, 2, 128, 64, "f16", 70001), (1, 1, 1, 64, 8, "bf16", 20000),
                                                    (1, 64, 1, 128, 32, "bf16", 30011), (300, 4, 2, 64, 16, "f16", 40),
-                                                   (5, 6, 3, 128, 48, "f16", 9000), (1500, 1, 1, 64, 8, "bf16", 9)])
+                                                   (5, 6, 3, 128, 48, "f16", 9000), (1500, 1, 1, 64, 8, "bf16", 9),
+                                                   (48, 32, 8, 128, 32, "bf16", 5000), (40, 16, 8, 64, 16, "f16", 7000)])
 def test_attend_splits_over_length_and_batch(ig, B, Hq, Hkv, d, page, dt, hi):
     lengths = [hi if b == B // 2 else (b * 7919) % (hi + 1) for b in range(B)]
     c = make_attend(B + hi, dt, lengths, Hq, Hkv, d, page)
