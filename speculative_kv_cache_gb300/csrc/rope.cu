@@ -8,113 +8,207 @@
 namespace ig {
 namespace {
 
-template <typename T>
-__device__ __forceinline__ float to_f(T x);
-template <>
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+// Eight 16-bit values in a uint4.
+template <bool BF>
+__device__ __forceinline__ void unpack8(const uint4& r, float (&f)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 v;
+    if constexpr (BF) v = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else v = h2_to_f2(w[i]);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+template <bool BF>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 16-byte load past L1 (every row is read once); not the read-only path, q may be written in place
+__device__ __forceinline__ uint4 ld_once(const uint16_t* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
 
 struct RopeArgs {
-  const void *q, *k, *v, *wq, *wk;
+  const uint16_t *q, *k, *v, *wq, *wk;
   int64_t sq, sk, sv;
   const int32_t *pos, *slot;
   const uint64_t* turns;
-  void *qo, *ko, *vo;
+  uint16_t *qo, *ko, *vo;
   int T, Hq, Hkv, rot, layout, page, n_pages;
   float eps, rscale;
+  int heads, chunk, chunks;  // rows of a token; rows of a work item, items of a token
 };
 
-// One warp per row (token, head), q heads first, then k, then v.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) k_qk_norm_rope(const RopeArgs a, int* err) {
-  const int heads = a.Hq + (a.vo ? 2 : 1) * a.Hkv;
-  const long long r = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (r >= (long long)a.T * heads) return;
-  const int t = (int)(r / heads), h = (int)(r % heads), lane = threadIdx.x & 31;
-  const int kind = h < a.Hq ? 0 : h < a.Hq + a.Hkv ? 1 : 2;
-  const int hh = kind == 0 ? h : (h - a.Hq) % a.Hkv;
-  const T* x = kind == 0 ? (const T*)a.q + t * a.sq + hh * D
-                         : kind == 1 ? (const T*)a.k + t * a.sk + hh * D : (const T*)a.v + t * a.sv + hh * D;
-  T* y;
-  if (kind == 0) {
-    y = (T*)a.qo + ((size_t)t * a.Hq + hh) * D;
+constexpr int kRopeThreads = 128;
+constexpr int kRopeFly = 4;  // rows in flight per lane group
+constexpr int kRopeWarpsPerSm = 32;
+
+// A row (one head of one token) is taken by D / 16 lanes with two 16-byte pieces each, chosen so
+// that a lane holds both elements of its eight pairs: no exchange but the norm's sum.  A warp takes
+// a work item: `chunk` of a token's rows (q heads, then k, then v), 32 / (D / 16) of them side by
+// side; its lanes' sines and cosines are computed once per item.
+//
+// The angle of pair j at position p, in turns, is the low 64 bits of p * turns[j]: whole turns fall
+// off the top of the integer, so a far position costs no precision.  Its top 32 bits, rounded, are
+// the half turns that sincospif takes.
+//
+// HBM-bound where there are many tokens: every row is read and written once.
+template <bool BF, int D>
+__global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a, int* err) {
+  constexpr int GL = D / 16, RPW = 32 / GL;
+  const long long item = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  if (item >= (long long)a.T * a.chunks) return;
+  const int t = (int)(item / a.chunks), h0 = (int)(item % a.chunks) * a.chunk, h1 = min(a.heads, h0 + a.chunk);
+  const int lane = threadIdx.x & 31, g = lane / GL, i = lane % GL;
+  const unsigned group = (GL == 8 ? 0xffu : 0xfu) << (g * GL);
+  // this lane's pieces (of 8 elements) and whether they are rotated
+  int c0, c1;
+  bool r0, r1;
+  if (a.layout == IG_ROPE_HALF) {
+    const int hc = a.rot / 16;
+    r0 = r1 = i < hc;
+    c0 = r0 ? i : 2 * i;  // 2 hc + 2 (i - hc)
+    c1 = r0 ? i + hc : 2 * i + 1;
   } else {
-    T* o = (T*)(kind == 1 ? a.ko : a.vo);
-    if (a.page) {
-      const int s = a.slot[t];
-      if (s < 0) return;
-      if (s / a.page >= a.n_pages) {
-        if (lane == 0) raise_error(err, IG_DEVERR_INDEX);
-        return;
+    c0 = i;
+    c1 = i + GL;
+    r0 = c0 * 8 < a.rot;
+    r1 = c1 * 8 < a.rot;
+  }
+  // where the token's key and value go; the row of head hk is hk * step further
+  size_t row = (size_t)t * a.Hkv, step = 1;
+  bool put = true;
+  if (a.page && h1 > a.Hq) {
+    const int sl = a.slot[t], at = sl / a.page;
+    if (sl < 0 || at >= a.n_pages) {
+      put = false;
+      if (sl >= 0 && lane == 0) raise_error(err, IG_DEVERR_INDEX);
+    } else {
+      row = (size_t)at * a.Hkv * a.page + sl % a.page;
+      step = a.page;
+    }
+  }
+  float cs[8], sn[8];
+  if (r0 && h0 < a.Hq + a.Hkv) {
+    const uint64_t p = (uint64_t)(int64_t)a.pos[t];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int j = a.layout == IG_ROPE_HALF ? 8 * i + x : 4 * (x < 4 ? c0 : c1) + (x & 3);
+      // (a second piece that is not rotated has no frequencies)
+      const uint64_t at = a.layout == IG_ROPE_HALF || x < 4 || r1 ? p * __ldg(a.turns + j) : 0;
+      sincospif((float)(int32_t)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn[x], &cs[x]);
+      sn[x] *= a.rscale;
+      cs[x] *= a.rscale;
+    }
+  }
+  for (int hb = h0 + g; hb - g < h1; hb += RPW * kRopeFly) {
+    uint4 raw[kRopeFly][2];
+#pragma unroll
+    for (int x = 0; x < kRopeFly; ++x) {
+      const int h = hb + x * RPW;
+      if (h < h1) {
+        const uint16_t* src = h < a.Hq ? a.q + t * a.sq + (int64_t)h * D
+                              : h < a.Hq + a.Hkv ? a.k + t * a.sk + (int64_t)(h - a.Hq) * D
+                                                 : a.v + t * a.sv + (int64_t)(h - a.Hq - a.Hkv) * D;
+        raw[x][0] = ld_once(src + c0 * 8);
+        raw[x][1] = ld_once(src + c1 * 8);
       }
-      y = o + (((size_t)(s / a.page) * a.Hkv + hh) * a.page + s % a.page) * D;
-    } else {
-      y = o + ((size_t)t * a.Hkv + hh) * D;
     }
-  }
-  if (kind == 2) {
-    for (int i = lane; i < D; i += 32) y[i] = x[i];
-    return;
-  }
-  const T* w = (const T*)(kind == 0 ? a.wq : a.wk);
-  float v[D / 32];
-  float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {  // pairs j = lane + 32 i of the rotated part, then the rest
-    const int j = lane + 32 * i;
-    int e0, e1;
-    if (j < a.rot / 2) {
-      e0 = a.layout == IG_ROPE_HALF ? j : 2 * j;
-      e1 = a.layout == IG_ROPE_HALF ? j + a.rot / 2 : 2 * j + 1;
-    } else {
-      e0 = 2 * j;
-      e1 = 2 * j + 1;
-    }
-    v[2 * i] = to_f(x[e0]);
-    v[2 * i + 1] = to_f(x[e1]);
-    ss += v[2 * i] * v[2 * i] + v[2 * i + 1] * v[2 * i + 1];
-  }
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float rn = w ? 1.f / sqrtf(ss / D + a.eps) : 1.f;
+    for (int x = 0; x < kRopeFly; ++x) {
+      const int h = hb + x * RPW;
+      if (h >= h1) continue;
+      if (h < a.Hq + a.Hkv) {
+        const uint16_t* w = h < a.Hq ? a.wq : a.wk;
+        float e[8], f[8];
+        unpack8<BF>(raw[x][0], e);
+        unpack8<BF>(raw[x][1], f);
+        if (w) {
+          float ss = 0.f, w0[8], w1[8];
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const int j = lane + 32 * i;
-    const bool turn = j < a.rot / 2;
-    const int e0 = turn && a.layout == IG_ROPE_HALF ? j : 2 * j;
-    const int e1 = turn && a.layout == IG_ROPE_HALF ? j + a.rot / 2 : 2 * j + 1;
-    float p = v[2 * i], n = v[2 * i + 1];
-    if (w) {
-      p *= rn * to_f(w[e0]);
-      n *= rn * to_f(w[e1]);
+          for (int y = 0; y < 8; ++y) ss = fmaf(e[y], e[y], fmaf(f[y], f[y], ss));
+#pragma unroll
+          for (int o = GL / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
+          const float rn = rsqrtf(ss * (1.f / D) + a.eps);
+          unpack8<BF>(__ldg(reinterpret_cast<const uint4*>(w) + c0), w0);
+          unpack8<BF>(__ldg(reinterpret_cast<const uint4*>(w) + c1), w1);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            e[y] *= rn * w0[y];
+            f[y] *= rn * w1[y];
+          }
+        }
+        if (a.layout == IG_ROPE_HALF) {
+          if (r0)
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const float u = e[y] * cs[y] - f[y] * sn[y];
+              f[y] = e[y] * sn[y] + f[y] * cs[y];
+              e[y] = u;
+            }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if (r0) {
+              const float u = e[2 * y] * cs[y] - e[2 * y + 1] * sn[y];
+              e[2 * y + 1] = e[2 * y] * sn[y] + e[2 * y + 1] * cs[y];
+              e[2 * y] = u;
+            }
+            if (r1) {
+              const float u = f[2 * y] * cs[4 + y] - f[2 * y + 1] * sn[4 + y];
+              f[2 * y + 1] = f[2 * y] * sn[4 + y] + f[2 * y + 1] * cs[4 + y];
+              f[2 * y] = u;
+            }
+          }
+        }
+        raw[x][0] = pack8<BF>(e);
+        raw[x][1] = pack8<BF>(f);
+      }
+      uint16_t* dst;
+      if (h < a.Hq) {
+        dst = a.qo + ((size_t)t * a.Hq + h) * D;
+      } else {
+        if (!put) continue;
+        const bool isk = h < a.Hq + a.Hkv;
+        dst = (isk ? a.ko : a.vo) + (row + step * (isk ? h - a.Hq : h - a.Hq - a.Hkv)) * D;
+      }
+      *reinterpret_cast<uint4*>(dst + c0 * 8) = raw[x][0];
+      *reinterpret_cast<uint4*>(dst + c1 * 8) = raw[x][1];
     }
-    if (turn) {
-      // the angle in turns is the low 64 bits of position * turns; its top 32 bits, rounded, in
-      // half turns
-      const uint64_t at = (uint64_t)(int64_t)a.pos[t] * a.turns[j];
-      float sn, cs;
-      sincospif((float)(int32_t)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn, &cs);
-      sn *= a.rscale;
-      cs *= a.rscale;
-      const float u = p * cs - n * sn;
-      n = p * sn + n * cs;
-      p = u;
-    }
-    y[e0] = from_f<T>(p);
-    y[e1] = from_f<T>(n);
   }
 }
 
-template <typename T, int D>
-ig_status launch_rope(cudaStream_t st, const RopeArgs& a) {
-  const long long rows = (long long)a.T * (a.Hq + (a.vo ? 2 : 1) * a.Hkv);
-  k_qk_norm_rope<T, D><<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a, error_word());
+template <bool BF, int D>
+ig_status launch_rope(cudaStream_t st, RopeArgs a) {
+  constexpr int RPW = 32 / (D / 16);
+  a.heads = a.Hq + (a.vo ? 2 : 1) * a.Hkv;
+  // A work item is as many rows as keep kRopeWarpsPerSm warps per SM busy, from one step of a warp
+  // up to the whole token: few tokens spread over the SMs, many share each angle among its rows.
+  const long long rows = (long long)a.T * a.heads, want = (long long)sm_count(st) * kRopeWarpsPerSm;
+  const long long per = (rows + want - 1) / want;
+  a.chunk = (int)(per < a.heads ? per : a.heads);
+  a.chunk = (a.chunk + RPW - 1) / RPW * RPW;
+  a.chunks = (a.heads + a.chunk - 1) / a.chunk;
+  const long long items = (long long)a.T * a.chunks, ctas = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  k_qk_norm_rope<BF, D><<<(unsigned)ctas, kRopeThreads, 0, st>>>(a, error_word());
   IG_CHECK_LAUNCH("norm and rotation launch");
   return IG_OK;
 }
@@ -216,8 +310,8 @@ extern "C" ig_status ig_qk_norm_rope(void* stream, int dtype, int T, int Hq, int
                  !overlap(q_out, qo, v_out, ko) && !overlap(k_out, ko, v_out, ko),
              "outputs must not overlap the inputs or each other");
   const RopeArgs a{q, k, v, q_weight, k_weight, q_stride, k_stride, v_stride, positions, slot, turns, q_out, k_out,
-                   v_out, T, Hq, Hkv, rot, layout, page, n_pages, eps, rot_scale};
+                   v_out, T, Hq, Hkv, rot, layout, page, n_pages, eps, rot_scale, 0, 0, 0};
   cudaStream_t s = as_stream(stream);
-  if (dtype == IG_F16) return d == 128 ? launch_rope<__half, 128>(s, a) : launch_rope<__half, 64>(s, a);
-  return d == 128 ? launch_rope<__nv_bfloat16, 128>(s, a) : launch_rope<__nv_bfloat16, 64>(s, a);
+  if (dtype == IG_F16) return d == 128 ? launch_rope<false, 128>(s, a) : launch_rope<false, 64>(s, a);
+  return d == 128 ? launch_rope<true, 128>(s, a) : launch_rope<true, 64>(s, a);
 }
