@@ -58,7 +58,7 @@ struct RopeArgs {
 };
 
 constexpr int kRopeThreads = 128;
-constexpr int kRopeFly = 4;  // rows in flight per lane group
+constexpr int kRopeFly = 2;  // rows per batch of a lane group; two batches in flight
 constexpr int kRopeWarpsPerSm = 32;
 
 // A row (one head of one token) is taken by D / 16 lanes with two 16-byte pieces each, chosen so
@@ -70,9 +70,13 @@ constexpr int kRopeWarpsPerSm = 32;
 // off the top of the integer, so a far position costs no precision.  Its top 32 bits, rounded, are
 // the half turns that sincospif takes.
 //
-// HBM-bound where there are many tokens: every row is read and written once.
+// HBM-bound where there are many tokens: every row is read and written once.  Measured (4 x 3968
+// tokens of 32 + 64 heads of 128 fp16 into pages, 780 MB): 126 us, 6.2 TB/s, 0.91 of the copy rate; 4097
+// tokens of 40 + 16 normed bf16 heads (117 MB): 22.9 us, 5.1 TB/s; one launch alone 2.6 us.  The next
+// batch of rows is loaded before the last is worked on (without: 29 us for the second), five CTAs
+// per SM (4: 25.2, 6: 24.1, 8 with one row per batch: 23.3 us).
 template <bool BF, int D>
-__global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a, int* err) {
+__global__ void __launch_bounds__(kRopeThreads, 5) k_qk_norm_rope(const RopeArgs a, int* err) {
   constexpr int GL = D / 16, RPW = 32 / GL;
   const long long item = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
   if (item >= (long long)a.T * a.chunks) return;
@@ -106,21 +110,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a,
       step = a.page;
     }
   }
-  float cs[8], sn[8];
-  if (r0 && h0 < a.Hq + a.Hkv) {
-    const uint64_t p = (uint64_t)(int64_t)a.pos[t];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const int j = a.layout == IG_ROPE_HALF ? 8 * i + x : 4 * (x < 4 ? c0 : c1) + (x & 3);
-      // (a second piece that is not rotated has no frequencies)
-      const uint64_t at = a.layout == IG_ROPE_HALF || x < 4 || r1 ? p * __ldg(a.turns + j) : 0;
-      sincospif((float)(int32_t)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn[x], &cs[x]);
-      sn[x] *= a.rscale;
-      cs[x] *= a.rscale;
-    }
-  }
-  for (int hb = h0 + g; hb - g < h1; hb += RPW * kRopeFly) {
-    uint4 raw[kRopeFly][2];
+  auto load = [&](int hb, uint4 (&raw)[kRopeFly][2]) {
 #pragma unroll
     for (int x = 0; x < kRopeFly; ++x) {
       const int h = hb + x * RPW;
@@ -132,6 +122,25 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a,
         raw[x][1] = ld_once(src + c1 * 8);
       }
     }
+  };
+  uint4 raw[kRopeFly][2], next[kRopeFly][2];
+  load(h0 + g, raw);
+  // (the angles while the first rows are on their way)
+  float cs[8], sn[8];
+  if (r0 && h0 < a.Hq + a.Hkv) {
+    const uint64_t p = (uint64_t)(int64_t)a.pos[t];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int j = a.layout == IG_ROPE_HALF ? 8 * i + x : 4 * (x < 4 ? c0 : c1) + (x & 3);
+      if (a.layout == IG_ROPE_PAIRS && x >= 4 && !r1) continue;
+      const uint64_t at = p * __ldg(a.turns + j);
+      sincospif((float)(int32_t)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn[x], &cs[x]);
+      sn[x] *= a.rscale;
+      cs[x] *= a.rscale;
+    }
+  }
+  for (int hb = h0 + g; hb - g < h1; hb += RPW * kRopeFly) {
+    load(hb + RPW * kRopeFly, next);
 #pragma unroll
     for (int x = 0; x < kRopeFly; ++x) {
       const int h = hb + x * RPW;
@@ -193,6 +202,11 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeArgs a,
       *reinterpret_cast<uint4*>(dst + c0 * 8) = raw[x][0];
       *reinterpret_cast<uint4*>(dst + c1 * 8) = raw[x][1];
     }
+#pragma unroll
+    for (int x = 0; x < kRopeFly; ++x) {
+      raw[x][0] = next[x][0];
+      raw[x][1] = next[x][1];
+    }
   }
 }
 
@@ -200,12 +214,13 @@ template <bool BF, int D>
 ig_status launch_rope(cudaStream_t st, RopeArgs a) {
   constexpr int RPW = 32 / (D / 16);
   a.heads = a.Hq + (a.vo ? 2 : 1) * a.Hkv;
-  // A work item is as many rows as keep kRopeWarpsPerSm warps per SM busy, from one step of a warp
-  // up to the whole token: few tokens spread over the SMs, many share each angle among its rows.
+  // A work item is as many rows as leave kRopeWarpsPerSm items per SM, from one step of a warp up to
+  // the whole token: few tokens spread over the SMs, many share each angle among their rows.  (64 items
+  // per SM: 23.9 -> 25.0 us at 4097 tokens.)
   const long long rows = (long long)a.T * a.heads, want = (long long)sm_count(st) * kRopeWarpsPerSm;
   const long long per = (rows + want - 1) / want;
-  a.chunk = (int)(per < a.heads ? per : a.heads);
-  a.chunk = (a.chunk + RPW - 1) / RPW * RPW;
+  a.chunks = per < a.heads ? (int)((a.heads + per - 1) / per) : 1;
+  a.chunk = ((a.heads + a.chunks - 1) / a.chunks + RPW - 1) / RPW * RPW;
   a.chunks = (a.heads + a.chunk - 1) / a.chunk;
   const long long items = (long long)a.T * a.chunks, ctas = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   k_qk_norm_rope<BF, D><<<(unsigned)ctas, kRopeThreads, 0, st>>>(a, error_word());
