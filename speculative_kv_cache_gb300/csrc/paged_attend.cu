@@ -28,7 +28,7 @@
 //
 // A CTA is one producer warp and three or four consumer warps.  The producer walks the tiles, looks the
 // pages up one tile ahead, and moves each tile with TMA (a page's rows of one head are contiguous;
-// boxes of 64 columns, 128-byte swizzle) into a ring of stages; a stage is consumed by one warp (or,
+// boxes of 64-column halves, 128-byte swizzle) into a ring of stages; a stage is consumed by one warp (or,
 // for more than 16 queries, by as many warps as it takes, each with its own queries), the stages in
 // turn.  A warp folds its tiles into its own (m, l, o); the warps join where a head ends.
 #include <cuda_bf16.h>
@@ -58,7 +58,8 @@ __host__ __device__ constexpr int pa_slots(int NQ, int WQ) { return pa_turns(WQ)
 // Where the work is: everything the kernels need beside the pointers.
 struct PaShape {
   int B, Hq, Hkv, G, QT;   // G query heads per key head, in QT groups of the unit's rows
-  int page, n_pages, max_pages, box;  // box: rows of a TMA box, a power of two that divides page
+  int page, n_pages, max_pages;
+  int box, tt;             // rows of a TMA box (a multiple of 8 that divides page); tokens of a tile
   float scale2;            // scale * log2(e)
   int by_unit;             // info is indexed by unit (units <= CTAs) or by CTA
 };
@@ -141,10 +142,9 @@ __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile
 }
 
 // The tiles of a CTA's share, in order, head by head; all lanes of a warp walk together.
-template <int TT>
 struct PaWalk {
   const int32_t* L_valid;
-  int B, per_seq, max_len;  // heads (times query groups) of a sequence; the table's length
+  int B, per_seq, max_len, tt;  // heads (times query groups) of a sequence; the table's length; a tile
   int b, off, nt, L, left;  // sequence, tile in its work, tiles of a head, its length; tiles left
   int base, len_here, len_next;
 
@@ -155,7 +155,7 @@ struct PaWalk {
   __device__ void enter(int seq) {
     b = seq;
     L = __shfl_sync(0xffffffffu, len_here, seq - base);
-    nt = (L + TT - 1) / TT;
+    nt = (L + tt - 1) / tt;
   }
   __device__ void start(int seq, int offset, int tiles) {
     left = tiles;
@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     const uint16_t* __restrict__ q, const int32_t* __restrict__ table, const int32_t* __restrict__ L_valid,
     const PaShape s, float* __restrict__ out, float* __restrict__ lse, float* __restrict__ part,
     int2* __restrict__ info, int* err) {
-  constexpr int TT = pa_tokens<D>(), MT = TT / 16, NS = pa_stages(WQ), HALVES = D / 64;
+  constexpr int TT = pa_tokens<D>(), MT = TT / 16, NS = pa_stages(WQ);
   constexpr int RU = 8 * NQ * WQ;          // query rows of a unit
   constexpr int TG = pa_turns(WQ);         // warps that take stages in turn
   constexpr int kPaThreads = pa_threads(WQ), kPaWarps = TG * WQ, SLOTS = pa_slots(NQ, WQ);
   static_assert(NS % TG == 0, "a stage is always the same warps'");
   constexpr int PARTS = BF ? 3 : 2;        // 16-bit parts of a weight
-  constexpr uint32_t kHalfBytes = TT * 128, kKvBytes = kPaStageBytes / 2;
+  constexpr uint32_t kKvBytes = kPaStageBytes / 2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* ring = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                          ~static_cast<uintptr_t>(1023));
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       raise_error(err, IG_DEVERR_INDEX);
       L = L < 0 ? 0 : max_len;
     }
-    return (L + TT - 1) / TT * per_seq;
+    return (L + s.tt - 1) / s.tt * per_seq;
   };
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += tiles_of(b);
@@ -266,77 +266,108 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     }
   }
   __syncthreads();
-  PaWalk<TT> w;
+  PaWalk w;
   w.L_valid = L_valid;
   w.B = s.B;
   w.per_seq = per_seq;
   w.max_len = max_len;
+  w.tt = s.tt;
   w.b = w.off = w.L = w.left = 0;
   w.nt = 1;
   if (r1 > r0) w.start(sh.start_b, sh.start_off, r1 - r0);
 
   if (warp == kPaWarps) {
-    // ---- producer.  Lane i < boxes * 2 * HALVES moves one box: K or V, a half of the columns.
-    const int box = lane / (2 * HALVES), is_v = (lane / HALVES) & 1, half = lane % HALVES;
-    const int boxes = TT / s.box;
-    const int box_tokens = box * s.box;
-    auto page_of = [&](const PaWalk<TT>& at) -> int {  // the lane's page number, -1: nothing to move
-      const int t = at.tile() * TT + box_tokens;
-      if (at.left <= 0 || box >= boxes || t >= at.L) return -1;
-      const int g = __ldg(table + (size_t)at.b * s.max_pages + t / s.page);
-      return g;
+    // ---- producer.  The tiles of a head are taken in windows of 32 pages, a page number per lane;
+    // the next window's numbers are loaded while this one's tiles go out.  Of a tile, lane i moves
+    // box i / 2 of the keys (even i) or values.
+    const int boxes = s.tt / s.box, box_at = lane / 2 * s.box, is_v = lane & 1;
+    const int jump = s.tt / s.page, step = s.tt % s.page;  // a tile further: pages and rows
+    const uint32_t box_bytes = (uint32_t)s.box * D * 2;
+    // tiles from where `at` stands that 32 pages cover, and the lane's page number
+    auto window = [&](const PaWalk& at, int& first, int& id) -> int {
+      const int tile = at.tile();
+      first = (int)((long long)tile * s.tt / s.page);
+      const long long covered = ((long long)first + 32) * s.page / s.tt - tile;
+      const bool in = (long long)(first + lane) * s.page < at.L;
+      id = in ? __ldg(table + (size_t)at.b * s.max_pages + first + lane) : -1;
+      const int run = at.run();
+      return covered < run ? (int)covered : run;
     };
-    uint32_t it = 0;
-    int g = page_of(w);
-    while (w.left > 0) {
-      const int tile = w.tile(), hk = w.unit() / s.QT, n = min(TT, w.L - tile * TT);
-      const bool want = box < boxes && box_tokens < n;
-      const int t = tile * TT + box_tokens;
-      const int mine_g = g;
-      w.advance(1);
-      g = page_of(w);  // the next tile's pages, while this one's stage is waited for
-      const bool ok = want && mine_g >= 0 && mine_g < s.n_pages;
-      if (want && !ok) raise_error(err, IG_DEVERR_INDEX);
-      const uint32_t st = it % NS, r = it / NS;
-      const bool freed = r == 0 || pa_wait(&sh.empty[st], (r - 1) & 1, &sh.abort, (uint32_t)kDefaultWaitIters);
-      if (!__all_sync(0xffffffffu, freed)) {  // one verdict for the warp
+    uint32_t st = 0, round = 0, it = 0;
+    int first = 0, ids = -1, n = w.left > 0 ? window(w, first, ids) : 0;
+    bool going = true;
+    while (n > 0 && going) {
+      const int tile = w.tile(), hk = w.unit() / s.QT, L = w.L;
+      w.advance(n);
+      int first2 = 0, ids2 = -1;
+      const int n2 = w.left > 0 ? window(w, first2, ids2) : 0;
+      int tokens = L - tile * s.tt;                  // from this tile on
+      int pg = (tile * s.tt + box_at) / s.page;      // this lane's page and row in it
+      int row = (tile * s.tt + box_at) - pg * s.page;
+      pg -= first;
+      for (int i = 0; i < n; ++i) {
+        const int g = __shfl_sync(0xffffffffu, ids, pg & 31);
+        const bool want = lane < 2 * boxes && box_at < tokens;
+        const bool ok = want && g >= 0 && g < s.n_pages;
+        const unsigned moving = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, want && !ok);
+        const bool freed = round == 0 || pa_wait(&sh.empty[st], (round - 1) & 1, &sh.abort, (uint32_t)kDefaultWaitIters);
+        if (!__all_sync(0xffffffffu, freed)) {  // one verdict for the warp
+          if (lane == 0) {
+            sh.abort = 1;
+            raise_error(err, IG_DEVERR_TIMEOUT);
+          }
+          going = false;
+          break;
+        }
         if (lane == 0) {
-          sh.abort = 1;
-          raise_error(err, IG_DEVERR_TIMEOUT);
+          const int live = min(tokens, s.tt);
+          unsigned long long v = live >= 64 ? ~0ull : (1ull << live) - 1;
+          if (bad) {
+            raise_error(err, IG_DEVERR_INDEX);
+            for (unsigned m = bad & 0x55555555u; m; m &= m - 1)
+              v &= ~((s.box >= 64 ? ~0ull : (1ull << s.box) - 1) << ((__ffs(m) - 1) / 2 * s.box));
+          }
+          sh.valid[st] = v;
+          mbar_arrive_expect_tx(&sh.full[st], (uint32_t)__popc(moving) * box_bytes);
         }
-        break;
-      }
-      const unsigned moving = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, want && !ok);
-      if (lane == 0) {
-        unsigned long long v = n >= 64 ? ~0ull : (1ull << n) - 1;
-        for (unsigned m = bad; m; m &= m - 1) {
-          const int bt = (__ffs(m) - 1) / (2 * HALVES) * s.box;
-          v &= ~(((s.box >= 64 ? 0ull : 1ull << s.box) - 1) << bt);
+        __syncwarp();
+        if (ok)
+          tma_load_3d(ring + st * kPaStageBytes + is_v * kKvBytes + box_at * (D * 2), is_v ? &map_v : &map_k, 0,
+                      (g * s.Hkv + hk) * s.page + row, 0, &sh.full[st]);
+        ++it;
+        if (++st == NS) {
+          st = 0;
+          ++round;
         }
-        sh.valid[st] = v;
-        mbar_arrive_expect_tx(&sh.full[st], (uint32_t)__popc(moving) * s.box * 128);
+        tokens -= s.tt;
+        pg += jump;
+        row += step;
+        if (row >= s.page) {
+          row -= s.page;
+          ++pg;
+        }
       }
-      __syncwarp();
-      if (ok) {
-        const int row = (mine_g * s.Hkv + hk) * s.page + t % s.page;
-        tma_load_2d(ring + st * kPaStageBytes + is_v * kKvBytes + half * kHalfBytes + box_tokens * 128,
-                    is_v ? &map_v : &map_k, half * 64, row, &sh.full[st]);
-      }
-      ++it;
+      n = n2;
+      first = first2;
+      ids = ids2;
     }
     __syncwarp();
     if (*(volatile int*)&sh.abort)  // let the copies already issued land before the CTA leaves
-      for (uint32_t st = 0; st < NS && st < it; ++st)
-        mbar_wait_bounded(&sh.full[st], ((it - 1 - st) / NS) & 1, 1u << 16);
+      for (uint32_t x = 0; x < NS && x < it; ++x) mbar_wait_bounded(&sh.full[x], ((it - 1 - x) / NS) & 1, 1u << 16);
   } else {
     // ---- consumers: warp = tg + TG * wq takes stages tg, tg + TG, ... for query rows wq
     const int tg = warp % TG, wq = warp / TG;
     const int gl = lane >> 2, tl = lane & 3;  // fragment row and column pair
     const uint32_t limit = wait_limit(err);
     // ldmatrix rows of this lane: keys (16 tokens x 16 columns), values transposed
-    const uint32_t k_row = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128, k_chunk = lane >> 4;
-    const uint32_t v_row = ((lane & 7) + (lane >> 4) * 8) * 128, v_chunk = (lane >> 3) & 1;
-    const uint32_t swz = lane & 7;
+    const uint32_t k_chunk = lane >> 4, v_chunk = (lane >> 3) & 1, swz = lane & 7, half_bytes = s.box * 128;
+    uint32_t k_row[MT], v_row[MT];  // where a box after the other puts them; rows past the tile: any
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      auto at = [&](int r) -> uint32_t { return r < s.tt ? r / s.box * (s.box * D * 2) + r % s.box * 128 : (r & 7) * 128; };
+      k_row[i] = at(i * 16 + (lane & 7) + ((lane >> 3) & 1) * 8);
+      v_row[i] = at(i * 16 + (lane & 7) + (lane >> 4) * 8);
+    }
     uint32_t it = 0;  // tile of this CTA
     bool cut_one = false;
     while (w.left > 0) {
@@ -383,7 +414,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             uint32_t a[4];
-            ldsm4(a, kb + (ks / 4) * kHalfBytes + i * 2048 + k_row + ((((ks % 4) * 2 + k_chunk) ^ swz) << 4));
+            ldsm4(a, kb + (ks / 4) * half_bytes + k_row[i] + ((((ks % 4) * 2 + k_chunk) ^ swz) << 4));
 #pragma unroll
             for (int j = 0; j < NQ; ++j) mma16816<BF>(z[i][j], a, qf[ks][j][0], qf[ks][j][1]);
           }
@@ -461,7 +492,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             uint32_t a[4];
-            ldsm4_t(a, vb + (dt / 4) * kHalfBytes + i * 2048 + v_row + ((((dt % 4) * 2 + v_chunk) ^ swz) << 4));
+            ldsm4_t(a, vb + (dt / 4) * half_bytes + v_row[i] + ((((dt % 4) * 2 + v_chunk) ^ swz) << 4));
             if (!whole) {  // rows that do not count may hold anything: zero times NaN is NaN
               const unsigned v0 = (unsigned)(valid >> (i * 16 + tl * 2)) & 3u, v1 = (unsigned)(valid >> (i * 16 + 8 + tl * 2)) & 3u;
               const uint32_t k0 = (v0 & 1 ? 0xffffu : 0u) | (v0 & 2 ? 0xffff0000u : 0u);
@@ -715,14 +746,15 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
                        const int32_t* table, const int32_t* L, float* out, float* lse, void* ws) {
   constexpr int RU = 8 * NQ * WQ, TT = pa_tokens<D>();
   s.QT = (s.G + RU - 1) / RU;
-  s.box = TT;
-  while (s.page % s.box) s.box >>= 1;
-  const long long most = (long long)s.B * ((s.max_pages * s.page + TT - 1) / TT) * s.Hkv * s.QT;
+  s.box = TT < s.page ? TT : s.page;
+  while (s.page % s.box) s.box -= 8;
+  s.tt = TT / s.box * s.box;
+  const long long most = (long long)s.B * ((s.max_pages * s.page + s.tt - 1) / s.tt) * s.Hkv * s.QT;
   IG_REQUIRE(most < (1ll << 31), "B*max_pages*page*Hkv is too large: %lld tiles", most);
   const int rows = s.n_pages * s.Hkv * s.page;
   CUtensorMap mk, mv;
-  ig_status r = make_map(&mk, K, rows, D, s.box);
-  if (r == IG_OK) r = make_map(&mv, V, rows, D, s.box);
+  ig_status r = make_map_halves(&mk, K, rows, D, s.box);
+  if (r == IG_OK) r = make_map_halves(&mv, V, rows, D, s.box);
   if (r != IG_OK) return r;
   constexpr size_t smem = 1024 + (size_t)pa_stages(WQ) * kPaStageBytes + sizeof(PaShared<D, NQ, WQ>);
   cudaError_t e = cudaFuncSetAttribute(k_paged_attend<BF, D, NQ, WQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -12,6 +12,10 @@ namespace ig {
 // swizzle atom) x box_rows rows, 128B swizzle, zero fill out of bounds.
 ig_status make_map(CUtensorMap* m, const void* base, int rows, int cols, int box_rows);
 
+// The same tensor (of 16-bit elements, cols 64 or 128) with its 64-column halves as a third dimension:
+// a box is all columns of box_rows rows, one half after the other, each 128B-swizzled.
+ig_status make_map_halves(CUtensorMap* m, const void* base, int rows, int cols, int box_rows);
+
 // Shared-memory matrix descriptor of a K-major, 128B-swizzled tile whose 8-row groups are
 // 1024 bytes apart: start address >> 4 (bits 0-13), leading offset 16 B (unused for swizzled
 // K-major tiles), stride offset 1024 B (bits 32-45), descriptor version 1 (bit 46), layout
@@ -31,6 +35,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
           smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
       : "memory");
 }
 
