@@ -59,7 +59,7 @@ __host__ __device__ constexpr int pa_slots(int NQ, int WQ) { return pa_turns(WQ)
 struct PaShape {
   int B, Hq, Hkv, G, QT;   // G query heads per key head, in QT groups of the unit's rows
   int page, n_pages, max_pages;
-  int box, tt;             // rows of a TMA box (a multiple of 8 that divides page); tokens of a tile
+  int box;                 // rows of a TMA box, a power of two that divides page
   float scale2;            // scale * log2(e)
   int by_unit;             // info is indexed by unit (units <= CTAs) or by CTA
 };
@@ -142,9 +142,10 @@ __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile
 }
 
 // The tiles of a CTA's share, in order, head by head; all lanes of a warp walk together.
+template <int TT>
 struct PaWalk {
   const int32_t* L_valid;
-  int B, per_seq, max_len, tt;  // heads (times query groups) of a sequence; the table's length; a tile
+  int B, per_seq, max_len;  // heads (times query groups) of a sequence; the table's length
   int b, off, nt, L, left;  // sequence, tile in its work, tiles of a head, its length; tiles left
   int base, len_here, len_next;
 
@@ -155,7 +156,7 @@ struct PaWalk {
   __device__ void enter(int seq) {
     b = seq;
     L = __shfl_sync(0xffffffffu, len_here, seq - base);
-    nt = (L + tt - 1) / tt;
+    nt = (L + TT - 1) / TT;
   }
   __device__ void start(int seq, int offset, int tiles) {
     left = tiles;
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       raise_error(err, IG_DEVERR_INDEX);
       L = L < 0 ? 0 : max_len;
     }
-    return (L + s.tt - 1) / s.tt * per_seq;
+    return (L + TT - 1) / TT * per_seq;
   };
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += tiles_of(b);
@@ -266,12 +267,11 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     }
   }
   __syncthreads();
-  PaWalk w;
+  PaWalk<TT> w;
   w.L_valid = L_valid;
   w.B = s.B;
   w.per_seq = per_seq;
   w.max_len = max_len;
-  w.tt = s.tt;
   w.b = w.off = w.L = w.left = 0;
   w.nt = 1;
   if (r1 > r0) w.start(sh.start_b, sh.start_off, r1 - r0);
@@ -280,14 +280,14 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     // ---- producer.  The tiles of a head are taken in windows of 32 pages, a page number per lane;
     // the next window's numbers are loaded while this one's tiles go out.  Of a tile, lane i moves
     // box i / 2 of the keys (even i) or values.
-    const int boxes = s.tt / s.box, box_at = lane / 2 * s.box, is_v = lane & 1;
-    const int jump = s.tt / s.page, step = s.tt % s.page;  // a tile further: pages and rows
+    const int boxes = TT / s.box, box_at = lane / 2 * s.box, is_v = lane & 1;
+    const int jump = TT / s.page, step = TT % s.page;  // a tile further: pages and rows
     const uint32_t box_bytes = (uint32_t)s.box * D * 2;
     // tiles from where `at` stands that 32 pages cover, and the lane's page number
-    auto window = [&](const PaWalk& at, int& first, int& id) -> int {
+    auto window = [&](const PaWalk<TT>& at, int& first, int& id) -> int {
       const int tile = at.tile();
-      first = (int)((long long)tile * s.tt / s.page);
-      const long long covered = ((long long)first + 32) * s.page / s.tt - tile;
+      first = (int)((long long)tile * TT / s.page);
+      const long long covered = ((long long)first + 32) * s.page / TT - tile;
       const bool in = (long long)(first + lane) * s.page < at.L;
       id = in ? __ldg(table + (size_t)at.b * s.max_pages + first + lane) : -1;
       const int run = at.run();
@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       w.advance(n);
       int first2 = 0, ids2 = -1;
       const int n2 = w.left > 0 ? window(w, first2, ids2) : 0;
-      int tokens = L - tile * s.tt;                  // from this tile on
-      int pg = (tile * s.tt + box_at) / s.page;      // this lane's page and row in it
-      int row = (tile * s.tt + box_at) - pg * s.page;
+      int tokens = L - tile * TT;                  // from this tile on
+      int pg = (tile * TT + box_at) / s.page;      // this lane's page and row in it
+      int row = (tile * TT + box_at) - pg * s.page;
       pg -= first;
       for (int i = 0; i < n; ++i) {
         const int g = __shfl_sync(0xffffffffu, ids, pg & 31);
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
           break;
         }
         if (lane == 0) {
-          const int live = min(tokens, s.tt);
+          const int live = min(tokens, TT);
           unsigned long long v = live >= 64 ? ~0ull : (1ull << live) - 1;
           if (bad) {
             raise_error(err, IG_DEVERR_INDEX);
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
           st = 0;
           ++round;
         }
-        tokens -= s.tt;
+        tokens -= TT;
         pg += jump;
         row += step;
         if (row >= s.page) {
@@ -361,10 +361,10 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     const uint32_t limit = wait_limit(err);
     // ldmatrix rows of this lane: keys (16 tokens x 16 columns), values transposed
     const uint32_t k_chunk = lane >> 4, v_chunk = (lane >> 3) & 1, swz = lane & 7, half_bytes = s.box * 128;
-    uint32_t k_row[MT], v_row[MT];  // where a box after the other puts them; rows past the tile: any
+    uint32_t k_row[MT], v_row[MT];  // where one box after the other puts them
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      auto at = [&](int r) -> uint32_t { return r < s.tt ? r / s.box * (s.box * D * 2) + r % s.box * 128 : (r & 7) * 128; };
+      auto at = [&](int r) -> uint32_t { return r / s.box * (s.box * D * 2) + r % s.box * 128; };
       k_row[i] = at(i * 16 + (lane & 7) + ((lane >> 3) & 1) * 8);
       v_row[i] = at(i * 16 + (lane & 7) + (lane >> 4) * 8);
     }
@@ -746,10 +746,9 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
                        const int32_t* table, const int32_t* L, float* out, float* lse, void* ws) {
   constexpr int RU = 8 * NQ * WQ, TT = pa_tokens<D>();
   s.QT = (s.G + RU - 1) / RU;
-  s.box = TT < s.page ? TT : s.page;
-  while (s.page % s.box) s.box -= 8;
-  s.tt = TT / s.box * s.box;
-  const long long most = (long long)s.B * ((s.max_pages * s.page + s.tt - 1) / s.tt) * s.Hkv * s.QT;
+  s.box = TT;
+  while (s.page % s.box) s.box >>= 1;
+  const long long most = (long long)s.B * ((s.max_pages * s.page + TT - 1) / TT) * s.Hkv * s.QT;
   IG_REQUIRE(most < (1ll << 31), "B*max_pages*page*Hkv is too large: %lld tiles", most);
   const int rows = s.n_pages * s.Hkv * s.page;
   CUtensorMap mk, mv;
