@@ -50,7 +50,7 @@ __host__ __device__ constexpr int pa_tokens() { return kPaStageBytes / (4 * D); 
 // warps that take stages in turn, and stages: a multiple of them, so that a stage is always the
 // same warps' (a warp that skipped a phase of a stage's barrier could not tell the phases' parity)
 __host__ __device__ constexpr int pa_turns(int WQ) { return WQ == 1 ? 3 : WQ == 2 ? 2 : 1; }
-__host__ __device__ constexpr int pa_stages(int WQ) { return WQ == 2 ? 4 : 6; }  // two CTAs per SM
+__host__ __device__ constexpr int pa_stages(int WQ) { return WQ == 1 ? 6 : WQ == 2 ? 4 : 5; }  // two CTAs per SM
 __host__ __device__ constexpr int pa_threads(int WQ) { return (pa_turns(WQ) * WQ + 1) * 32; }
 // joining warps' outputs held at once, per group of queries
 __host__ __device__ constexpr int pa_slots(int NQ, int WQ) { return pa_turns(WQ) == 1 ? 0 : NQ == 1 ? 2 : 1; }
@@ -67,7 +67,10 @@ struct PaShape {
 // shared memory behind the ring
 template <int D, int NQ, int WQ>
 struct PaShared {
-  float merge[pa_slots(NQ, WQ) ? pa_slots(NQ, WQ) * WQ : 1][D / 16 * NQ * 4][32];  // a lane's registers apart
+  // joining warps' outputs, a lane's registers apart
+  float merge[pa_slots(NQ, WQ) ? pa_slots(NQ, WQ) * WQ : 1][pa_slots(NQ, WQ) ? D / 16 * NQ * 4 : 1][32];
+  // the warps' queries, where they would not fit the registers (rows 16 bytes apart in the banks)
+  uint4 q[WQ > 1 ? WQ * pa_turns(WQ) : 1][WQ > 1 ? NQ * 8 : 1][WQ > 1 ? D / 8 + 1 : 1];
   float m[pa_turns(WQ) * WQ][NQ * 8], l[pa_turns(WQ) * WQ][NQ * 8];
   unsigned long long valid[pa_stages(WQ)];  // tokens of the stage that count
   uint64_t full[pa_stages(WQ)], empty[pa_stages(WQ)];
@@ -200,6 +203,8 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   constexpr int RU = 8 * NQ * WQ;          // query rows of a unit
   constexpr int TG = pa_turns(WQ);         // warps that take stages in turn
   constexpr int kPaThreads = pa_threads(WQ), kPaWarps = TG * WQ, SLOTS = pa_slots(NQ, WQ);
+  constexpr bool QS = WQ > 1;              // queries in shared memory
+  static_assert(!QS || NQ == 2, "ldmatrix takes the queries 16 at a time");
   static_assert(NS % TG == 0, "a stage is always the same warps'");
   constexpr int PARTS = BF ? 3 : 2;        // 16-bit parts of a weight
   constexpr uint32_t kKvBytes = kPaStageBytes / 2;
@@ -368,6 +373,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       k_row[i] = at(i * 16 + (lane & 7) + ((lane >> 3) & 1) * 8);
       v_row[i] = at(i * 16 + (lane & 7) + (lane >> 4) * 8);
     }
+    const uint32_t q_row = QS ? smem_addr(&sh.q[warp][(lane & 7) + (lane >> 4) * 8][(lane >> 3) & 1]) : 0u;
     uint32_t it = 0;  // tile of this CTA
     bool cut_one = false;
     while (w.left > 0) {
@@ -375,16 +381,26 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       const int tile0 = w.tile(), nt = w.nt, run = w.run();
       const int qrow = qt * RU + wq * 8 * NQ;  // of this warp, within the key head's G
       const uint16_t* qp = q + ((size_t)b * s.Hq + (size_t)hk * s.G + qrow) * D;
-      uint32_t qf[D / 16][NQ][2];
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-          const bool in = qrow + j * 8 + gl < s.G;
-          const uint16_t* p = qp + (size_t)(j * 8 + gl) * D + ks * 16 + tl * 2;
-          qf[ks][j][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
-          qf[ks][j][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(p + 8)) : 0u;
+      uint32_t qf[QS ? 1 : D / 16][NQ][2];
+      if constexpr (QS) {
+        __syncwarp();
+        for (int i = lane; i < NQ * 8 * (D / 8); i += 32) {
+          const int r = i / (D / 8), c = i % (D / 8);
+          sh.q[warp][r][c] = qrow + r < s.G ? __ldg(reinterpret_cast<const uint4*>(qp + (size_t)r * D) + c)
+                                            : make_uint4(0, 0, 0, 0);
         }
+        __syncwarp();
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int j = 0; j < NQ; ++j) {
+            const bool in = qrow + j * 8 + gl < s.G;
+            const uint16_t* p = qp + (size_t)(j * 8 + gl) * D + ks * 16 + tl * 2;
+            qf[ks][j][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
+            qf[ks][j][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(p + 8)) : 0u;
+          }
+      }
       float m[NQ][2], l[NQ][2], o[D / 16][NQ][4];
 #pragma unroll
       for (int j = 0; j < NQ; ++j) {
@@ -410,14 +426,25 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
 #pragma unroll
           for (int j = 0; j < NQ; ++j) z[i][j][0] = z[i][j][1] = z[i][j][2] = z[i][j][3] = 0.f;
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
+        for (int ks = 0; ks < D / 16; ++ks) {
+          uint32_t b[4];
+          if constexpr (QS) {
+            ldsm4(b, q_row + ks * 32);
+          } else {
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+              b[2 * j] = qf[ks][j][0];
+              b[2 * j + 1] = qf[ks][j][1];
+            }
+          }
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             uint32_t a[4];
             ldsm4(a, kb + (ks / 4) * half_bytes + k_row[i] + ((((ks % 4) * 2 + k_chunk) ^ swz) << 4));
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) mma16816<BF>(z[i][j], a, qf[ks][j][0], qf[ks][j][1]);
+            for (int j = 0; j < NQ; ++j) mma16816<BF>(z[i][j], a, b[2 * j], b[2 * j + 1]);
           }
+        }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
