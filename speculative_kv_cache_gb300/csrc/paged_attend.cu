@@ -43,12 +43,12 @@ namespace {
 constexpr int kPaCtasPerSm = 2;
 constexpr int kMaxPaCtas = 320;                   // upper bound of the grid (sizes the workspace)
 constexpr int kPaStageBytes = 16384;              // keys and values of one tile
+constexpr int kPaSolo = 2;                        // tiles of a head that one warp takes alone
 constexpr int kPaPartHead = 4;                    // a partial: [max, sum, -, -, output[D]]
 
 template <int D>
 __host__ __device__ constexpr int pa_tokens() { return kPaStageBytes / (4 * D); }  // tokens of a tile: 32 or 64
-// warps that take stages in turn, and stages: a multiple of them, so that a stage is always the
-// same warps' (a warp that skipped a phase of a stage's barrier could not tell the phases' parity)
+// warps that take stages in turn, and stages
 __host__ __device__ constexpr int pa_turns(int WQ) { return WQ == 1 ? 3 : WQ == 2 ? 2 : 1; }
 __host__ __device__ constexpr int pa_stages(int WQ) { return WQ == 1 ? 6 : WQ == 2 ? 4 : 5; }  // two CTAs per SM
 __host__ __device__ constexpr int pa_threads(int WQ) { return (pa_turns(WQ) * WQ + 1) * 32; }
@@ -73,6 +73,7 @@ struct PaShared {
   uint4 q[WQ > 1 ? WQ * pa_turns(WQ) : 1][WQ > 1 ? NQ * 8 : 1][WQ > 1 ? D / 8 + 1 : 1];
   float m[pa_turns(WQ) * WQ][NQ * 8], l[pa_turns(WQ) * WQ][NQ * 8];
   unsigned long long valid[pa_stages(WQ)];  // tokens of the stage that count
+  uint32_t tile[pa_stages(WQ)];             // the tile (of the CTA's) it is for
   uint64_t full[pa_stages(WQ)], empty[pa_stages(WQ)];
   int scan[pa_threads(WQ) / 32];
   int start_b, start_off, total;
@@ -144,6 +145,16 @@ __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile
   return false;
 }
 
+// The same for tile x of a stage's barrier.  A stage's phases go to different warps, and a warp that has
+// not followed them all cannot tell them by their parity; so the producer writes the tile's number
+// once the phase before is over.
+__device__ __forceinline__ bool pa_wait_tile(const volatile uint32_t* tile, uint32_t x, uint64_t* bar, uint32_t parity,
+                                             volatile int* abort, uint32_t limit) {
+  for (uint32_t i = 0; i < limit && !*abort; ++i)
+    if (*tile == x && mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+
 // The tiles of a CTA's share, in order, head by head; all lanes of a warp walk together.
 template <int TT>
 struct PaWalk {
@@ -205,7 +216,6 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   constexpr int kPaThreads = pa_threads(WQ), kPaWarps = TG * WQ, SLOTS = pa_slots(NQ, WQ);
   constexpr bool QS = WQ > 1;              // queries in shared memory
   static_assert(!QS || NQ == 2, "ldmatrix takes the queries 16 at a time");
-  static_assert(NS % TG == 0, "a stage is always the same warps'");
   constexpr int PARTS = BF ? 3 : 2;        // 16-bit parts of a weight
   constexpr uint32_t kKvBytes = kPaStageBytes / 2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -221,6 +231,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], WQ);
+      sh.tile[i] = ~0u;
     }
     sh.abort = 0;
     fence_mbar_init();
@@ -333,6 +344,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
               v &= ~((s.box >= 64 ? ~0ull : (1ull << s.box) - 1) << ((__ffs(m) - 1) / 2 * s.box));
           }
           sh.valid[st] = v;
+          *(volatile uint32_t*)&sh.tile[st] = it;
           mbar_arrive_expect_tx(&sh.full[st], (uint32_t)__popc(moving) * box_bytes);
         }
         __syncwarp();
@@ -375,10 +387,20 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     }
     const uint32_t q_row = QS ? smem_addr(&sh.q[warp][(lane & 7) + (lane >> 4) * 8][(lane >> 3) & 1]) : 0u;
     uint32_t it = 0;  // tile of this CTA
-    bool cut_one = false;
-    while (w.left > 0) {
+    bool cut = false;
+    for (uint32_t seg = 0; w.left > 0; ++seg) {
       const int u_in = w.unit(), hk = u_in / s.QT, qt = u_in % s.QT, b = w.b;
       const int tile0 = w.tile(), nt = w.nt, run = w.run();
+      const bool done = tile0 == 0 && run == nt;  // the whole head is here
+      cut = tile0 == 0 && !done;                  // it goes on in later CTAs
+      w.advance(run);
+      // a few tiles are one warp's own (warps then work on different heads and need not meet)
+      const bool solo = TG > 1 && run <= kPaSolo;
+      const int owner = solo ? seg % TG : 0;
+      if (solo && tg != owner) {
+        it += run;
+        continue;
+      }
       const int qrow = qt * RU + wq * 8 * NQ;  // of this warp, within the key head's G
       const uint16_t* qp = q + ((size_t)b * s.Hq + (size_t)hk * s.G + qrow) * D;
       uint32_t qf[QS ? 1 : D / 16][NQ][2];
@@ -410,9 +432,9 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
         for (int i = 0; i < D / 16; ++i) o[i][j][0] = o[i][j][1] = o[i][j][2] = o[i][j][3] = 0.f;
       }
       // this warp's stages of the run
-      for (uint32_t x = it + (tg + TG - it % TG) % TG; x < it + run; x += TG) {
+      for (uint32_t x = solo ? it : it + (tg + TG - it % TG) % TG; x < it + run; x += solo ? 1 : TG) {
         const uint32_t st = x % NS;
-        if (!pa_wait(&sh.full[st], (x / NS) & 1, &sh.abort, limit)) {
+        if (!pa_wait_tile(&sh.tile[st], x, &sh.full[st], (x / NS) & 1, &sh.abort, limit)) {
           if (lane == 0 && !atomicExch(&sh.abort, 1)) raise_error(err, IG_DEVERR_TIMEOUT);
           // the walk goes on without waiting, so that every warp meets the others' barriers
         }
@@ -551,7 +573,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int sh2 = 4; sh2 < 32; sh2 <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], sh2);
-      if constexpr (TG > 1) {
+      if (TG > 1 && !solo) {
         if (gl == 0)
 #pragma unroll
           for (int j = 0; j < NQ; ++j)
@@ -604,9 +626,8 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
           if (from + SLOTS < TG) consumer_sync<kPaWarps * 32>();
         }
       }
-      const bool done = tile0 == 0 && run == nt;  // the whole head was here
       const int unit = b * per_seq + u_in;
-      if (tg == 0) {
+      if (tg == owner) {
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -638,24 +659,19 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
           }
       }
       // what the second kernel joins: a head that begins here and goes on in later CTAs
-      if (threadIdx.x == 0) {
-        const bool cut = tile0 == 0 && !done;
-        if (cut || (s.by_unit && done)) {
-          int last = cta;  // the CTA that holds the head's last tile
-          if (cut) {
-            const long long end = (long long)r1 - run + nt - 1;  // a cut head is this CTA's last
-            last = (int)(end * ctas / total);
-            while (last + 1 < ctas && (long long)total * (last + 1) / ctas <= end) ++last;
-            while ((long long)total * last / ctas > end) --last;
-          }
-          if (s.by_unit) info[unit] = make_int2(cut ? cta : -1, last);
-          else info[cta] = make_int2(unit, last);
-          cut_one = true;
+      if (tg == owner && wq == 0 && lane == 0 && (cut || (s.by_unit && done))) {
+        int last = cta;  // the CTA that holds the head's last tile
+        if (cut) {
+          const long long end = (long long)r1 - run + nt - 1;  // a cut head is this CTA's last
+          last = (int)(end * ctas / total);
+          while (last + 1 < ctas && (long long)total * (last + 1) / ctas <= end) ++last;
+          while ((long long)total * last / ctas > end) --last;
         }
+        if (s.by_unit) info[unit] = make_int2(cut ? cta : -1, last);
+        else info[cta] = make_int2(unit, last);
       }
-      w.advance(run);
     }
-    if (threadIdx.x == 0 && !s.by_unit && !cut_one) info[cta] = make_int2(-1, 0);
+    if (threadIdx.x == 0 && !s.by_unit && !cut) info[cta] = make_int2(-1, 0);
     // sequences without a token
     for (int b = cta; b < s.B; b += gridDim.x) {
       if (__ldg(L_valid + b) > 0) continue;
