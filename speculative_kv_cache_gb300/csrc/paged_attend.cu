@@ -43,7 +43,11 @@ namespace {
 constexpr int kPaCtasPerSm = 2;
 constexpr int kMaxPaCtas = 320;                   // upper bound of the grid (sizes the workspace)
 constexpr int kPaStageBytes = 16384;              // keys and values of one tile
-constexpr int kPaSolo = 2;                        // tiles of a head that one warp takes alone
+// Tiles of a head that one warp takes alone, where its CTA has other heads for the other warps (149 x 11
+// heads of 106 to 212 tokens: 42.3 us at 2, 39.7 at 4, 38.2 at 8, where 167 x 6 heads of 397 lose 10 %).
+constexpr int kPaSolo = 4;
+// Tiles of the longest head up to which heads are not cut, when every head has a CTA of its own
+constexpr int kPaWhole = 6;
 constexpr int kPaPartHead = 4;                    // a partial: [max, sum, -, -, output[D]]
 
 template <int D>
@@ -62,6 +66,7 @@ struct PaShape {
   int box;                 // rows of a TMA box, a power of two that divides page
   float scale2;            // scale * log2(e)
   int by_unit;             // info is indexed by unit (units <= CTAs) or by CTA
+  int whole;               // the shares are in heads, not tiles: no head is cut
 };
 
 // shared memory behind the ring
@@ -160,7 +165,8 @@ template <int TT>
 struct PaWalk {
   const int32_t* L_valid;
   int B, per_seq, max_len;  // heads (times query groups) of a sequence; the table's length
-  int b, off, nt, L, left;  // sequence, tile in its work, tiles of a head, its length; tiles left
+  int whole;                // shares of whole heads
+  int b, off, nt, L, left;  // sequence, tile in its work, tiles of a head, its length; tiles (heads) left
   int base, len_here, len_next;
 
   __device__ int bounded(int i) const {
@@ -174,20 +180,20 @@ struct PaWalk {
   }
   __device__ void start(int seq, int offset, int tiles) {
     left = tiles;
-    off = offset;
     base = seq;
     const int lane = threadIdx.x & 31;
     len_here = bounded(base + lane);
     len_next = bounded(base + 32 + lane);
     enter(seq);
+    off = whole ? offset * nt : offset;
   }
   // the head that the walk stands in
   __device__ int unit() const { return off / nt; }
   __device__ int tile() const { return off % nt; }
-  __device__ int run() const { return min(nt - off % nt, left); }
-  __device__ void advance(int n) {
-    left -= n;
+  __device__ int run() const { return whole ? nt - off % nt : min(nt - off % nt, left); }
+  __device__ void advance(int n) {  // n <= run()
     off += n;
+    left -= whole ? (off % nt == 0 ? 1 : 0) : n;
     if (left <= 0 || off < nt * per_seq) return;
     off = 0;
     const int lane = threadIdx.x & 31;
@@ -245,7 +251,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       raise_error(err, IG_DEVERR_INDEX);
       L = L < 0 ? 0 : max_len;
     }
-    return (L + TT - 1) / TT * per_seq;
+    return (s.whole ? min(L, 1) : (L + TT - 1) / TT) * per_seq;
   };
   int mine = 0;
   for (int b = b0; b < b1; ++b) mine += tiles_of(b);
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     before += w < warp ? sh.scan[w] : 0;
     total += sh.scan[w];
   }
-  // with fewer tiles than CTAs the first `ctas` get one each
+  // in tiles, or in heads; with fewer than CTAs the first `ctas` get one each
   const int ctas = min((int)gridDim.x, total), cta = blockIdx.x;
   int r0 = 0, r1 = 0;
   if (cta < ctas) {
@@ -288,6 +294,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   w.B = s.B;
   w.per_seq = per_seq;
   w.max_len = max_len;
+  w.whole = s.whole;
   w.b = w.off = w.L = w.left = 0;
   w.nt = 1;
   if (r1 > r0) w.start(sh.start_b, sh.start_off, r1 - r0);
@@ -391,11 +398,11 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     for (uint32_t seg = 0; w.left > 0; ++seg) {
       const int u_in = w.unit(), hk = u_in / s.QT, qt = u_in % s.QT, b = w.b;
       const int tile0 = w.tile(), nt = w.nt, run = w.run();
-      const bool done = tile0 == 0 && run == nt;  // the whole head is here
+      const bool done = tile0 == 0 && run == nt;  // all of the head is here
       cut = tile0 == 0 && !done;                  // it goes on in later CTAs
       w.advance(run);
       // a few tiles are one warp's own (warps then work on different heads and need not meet)
-      const bool solo = TG > 1 && run <= kPaSolo;
+      const bool solo = TG > 1 && run <= kPaSolo && (seg > 0 || w.left > 0);
       const int owner = solo ? seg % TG : 0;
       if (solo && tg != owner) {
         it += run;
@@ -442,11 +449,15 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
         const uint32_t kb = smem_addr(ring + st * kPaStageBytes), vb = kb + kKvBytes;
         const unsigned long long valid = sh.valid[st];
         const bool whole = valid == (TT == 64 ? ~0ull : (1ull << TT) - 1);
-        float z[MT][NQ][4];
+        // (a product depends on the one before it in its accumulator: at least four accumulators in turn)
+        constexpr int ZC = MT * NQ >= 4 ? 1 : 2;
+        float zc[ZC][MT][NQ][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int c = 0; c < ZC; ++c)
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) z[i][j][0] = z[i][j][1] = z[i][j][2] = z[i][j][3] = 0.f;
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) zc[c][i][j][0] = zc[c][i][j][1] = zc[c][i][j][2] = zc[c][i][j][3] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           uint32_t b[4];
@@ -464,15 +475,16 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
             uint32_t a[4];
             ldsm4(a, kb + (ks / 4) * half_bytes + k_row[i] + ((((ks % 4) * 2 + k_chunk) ^ swz) << 4));
 #pragma unroll
-            for (int j = 0; j < NQ; ++j) mma16816<BF>(z[i][j], a, b[2 * j], b[2 * j + 1]);
+            for (int j = 0; j < NQ; ++j) mma16816<BF>(zc[ks % ZC][i][j], a, b[2 * j], b[2 * j + 1]);
           }
         }
+        float z[MT][NQ][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int j = 0; j < NQ; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[i][j][e] *= s.scale2;
+            for (int e = 0; e < 4; ++e) z[i][j][e] = (ZC == 2 ? zc[0][i][j][e] + zc[ZC - 1][i][j][e] : zc[0][i][j][e]) * s.scale2;
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < MT; ++i)
@@ -533,33 +545,48 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
               for (int pp = 0; pp < PARTS; ++pp) p[pp][i][j][hh] = transpose8(split2<BF>(x0, x1));
             }
         }
+        // DG column tiles side by side, for the same reason
+        constexpr int DG = 4 / NQ;
 #pragma unroll
-        for (int dt = 0; dt < D / 16; ++dt) {
-          float acc[NQ][4];
+        for (int d0 = 0; d0 < D / 16; d0 += DG) {
+          float acc[DG][NQ][4];
 #pragma unroll
-          for (int j = 0; j < NQ; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+          for (int x = 0; x < DG; ++x)
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) acc[x][j][0] = acc[x][j][1] = acc[x][j][2] = acc[x][j][3] = 0.f;
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            uint32_t a[4];
-            ldsm4_t(a, vb + (dt / 4) * half_bytes + v_row[i] + ((((dt % 4) * 2 + v_chunk) ^ swz) << 4));
+            uint32_t a[DG][4];
+#pragma unroll
+            for (int x = 0; x < DG; ++x) {
+              const int dt = d0 + x;
+              ldsm4_t(a[x], vb + (dt / 4) * half_bytes + v_row[i] + ((((dt % 4) * 2 + v_chunk) ^ swz) << 4));
+            }
             if (!whole) {  // rows that do not count may hold anything: zero times NaN is NaN
               const unsigned v0 = (unsigned)(valid >> (i * 16 + tl * 2)) & 3u, v1 = (unsigned)(valid >> (i * 16 + 8 + tl * 2)) & 3u;
               const uint32_t k0 = (v0 & 1 ? 0xffffu : 0u) | (v0 & 2 ? 0xffff0000u : 0u);
               const uint32_t k1 = (v1 & 1 ? 0xffffu : 0u) | (v1 & 2 ? 0xffff0000u : 0u);
-              a[0] &= k0;
-              a[1] &= k0;
-              a[2] &= k1;
-              a[3] &= k1;
+#pragma unroll
+              for (int x = 0; x < DG; ++x) {
+                a[x][0] &= k0;
+                a[x][1] &= k0;
+                a[x][2] &= k1;
+                a[x][3] &= k1;
+              }
             }
 #pragma unroll
             for (int pp = 0; pp < PARTS; ++pp)
 #pragma unroll
-              for (int j = 0; j < NQ; ++j) mma16816<BF>(acc[j], a, p[pp][i][j][0], p[pp][i][j][1]);
+              for (int x = 0; x < DG; ++x)
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) mma16816<BF>(acc[x][j], a[x], p[pp][i][j][0], p[pp][i][j][1]);
           }
 #pragma unroll
-          for (int j = 0; j < NQ; ++j)
+          for (int x = 0; x < DG; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[dt][j][e] = fmaf(o[dt][j][e], corr[j][e & 1], acc[j][e]);
+            for (int j = 0; j < NQ; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[d0 + x][j][e] = fmaf(o[d0 + x][j][e], corr[j][e & 1], acc[x][j][e]);
         }
         __syncwarp();
         if (lane == 0)
@@ -807,12 +834,15 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
   if (grid > most) grid = (int)most;
   const long long units = (long long)s.B * s.Hkv * s.QT;
   s.by_unit = units <= grid ? 1 : 0;
+  // Short heads with a CTA each are not cut: the join costs 2 us, a tile 0.8 us (4 heads of 256 tokens:
+  // 7.4 us cut and joined).
+  s.whole = s.by_unit && most <= units * kPaWhole ? 1 : 0;
   float* part = static_cast<float*>(ws);
   int2* info = reinterpret_cast<int2*>(static_cast<char*>(ws) + pa_part_bytes(s.G, D));
   k_paged_attend<BF, D, NQ, WQ><<<grid, pa_threads(WQ), smem, st>>>(mk, mv, q, table, L, s, out, lse, part, info,
                                                                error_word());
   IG_CHECK_LAUNCH("paged attention launch");
-  if (grid == 1) return IG_OK;  // nothing was cut
+  if (grid == 1 || s.whole) return IG_OK;  // nothing was cut
   // a row's partials are many only when there are few units: then a row gets a whole block
   const int rows_used = s.G < RU ? s.G : RU, list = s.by_unit ? (int)units : grid;
   const float bits = BF ? 0.f : 15.f;
