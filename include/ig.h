@@ -66,7 +66,7 @@ int ig_version(void);
 ig_status ig_check(void* stream);
 
 /* Iteration limit of the score kernels' bounded waits for their staged copies (k2_scores,
- * k23_score_select) on the current device: a wait that runs out records IG_DEVERR_TIMEOUT,
+ * k23_score_select), and of the paged attention's (k_paged_attend), on the current device: a wait that runs out records IG_DEVERR_TIMEOUT,
  * the CTA then waits (with the fixed default limit) for its copies in flight to land and
  * leaves without scoring, and the next ig_check returns IG_ERR_TIMEOUT.  max_iters < 0
  * restores the default (2^22 probes, far more than a copy needs); 0 makes the first wait give

@@ -140,16 +140,20 @@ def header_functions() -> list[str]:
     return sorted(set(re.findall(r"\b(ig_[a-z_0-9]+)\s*\(", txt)))
 
 
+# torch's current stream without a Stream object (2 us less per call); None where torch lacks it
+_raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", None)
+
+
 def _p(x):
     """Address of a buffer argument (tensor, ndarray, int, or None)."""
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
     if torch is not None and isinstance(x, torch.Tensor):
         if not x.is_contiguous():
             raise ValueError("tensor arguments must be contiguous")
         return x.data_ptr()
+    if isinstance(x, int):
+        return x
     if isinstance(x, np.ndarray):
         if not x.flags["C_CONTIGUOUS"]:
             raise ValueError("array arguments must be C-contiguous")
@@ -157,19 +161,44 @@ def _p(x):
     raise TypeError(f"unsupported buffer argument {type(x)}")
 
 
-def _rows(x, stride):
-    """Address of a buffer of rows ``stride`` elements apart: as _p, and also a tensor whose first
-    dimension has that stride and whose others are dense (a slice of a fused projection)."""
-    if torch is not None and isinstance(x, torch.Tensor) and not x.is_contiguous():
-        if x.numel() and not (x[0].is_contiguous() and (x.shape[0] == 1 or x.stride(0) == stride)):
-            raise ValueError(f"tensor rows must be dense and {stride} elements apart")
+def _here():
+    """The current GPU, where a call runs; None before torch uses one."""
+    return torch.cuda.current_device() if torch is not None and torch.cuda.is_initialized() else None
+
+
+def _q(x, here):
+    """As _p, and refuses a tensor of another GPU than ``here``."""
+    if torch is not None and isinstance(x, torch.Tensor):
+        if not x.is_contiguous():
+            raise ValueError("tensor arguments must be contiguous")
+        if here is not None and x.get_device() not in (here, -1):
+            raise ValueError(f"a tensor is on cuda:{x.get_device()}, the current device is cuda:{here}")
         return x.data_ptr()
     return _p(x)
+
+
+def _rows(x, stride, here=None):
+    """Address of a buffer of rows ``stride`` elements apart: as _q, and also a tensor whose first
+    dimension has that stride and whose others are dense (a slice of a fused projection)."""
+    if torch is None or not isinstance(x, torch.Tensor) or x.is_contiguous():
+        return _q(x, here)
+    shape, strides = x.shape, x.stride()
+    ok, dense = strides[0] == stride or shape[0] == 1, 1
+    for i in range(len(strides) - 1, 0, -1):
+        ok = ok and (strides[i] == dense or shape[i] == 1)
+        dense *= shape[i]
+    if not ok:
+        raise ValueError(f"tensor rows must be dense and {stride} elements apart")
+    if here is not None and x.get_device() not in (here, -1):
+        raise ValueError(f"a tensor is on cuda:{x.get_device()}, the current device is cuda:{here}")
+    return x.data_ptr()
 
 
 def _s(stream):
     """A cudaStream_t from a torch stream, an int handle, or None (torch's current stream)."""
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         if torch is not None and torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
@@ -443,9 +472,10 @@ def ig_paged_attend_workspace_bytes(B, Hq, Hkv, d) -> int:
 
 def ig_paged_attend(stream, dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scale, q, K, V, page_table, L_valid, out,
                     lse, workspace, workspace_bytes):
-    _ok(_lib.ig_paged_attend(_s(stream), dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scale, _p(q), _p(K), _p(V),
-                             _p(page_table), _p(L_valid), _p(out), _p(lse), _p(workspace), workspace_bytes),
-        "ig_paged_attend")
+    h = _here()
+    _ok(_lib.ig_paged_attend(_s(stream), dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scale, _q(q, h), _q(K, h),
+                             _q(V, h), _q(page_table, h), _q(L_valid, h), _q(out, h), _q(lse, h), _q(workspace, h),
+                             workspace_bytes), "ig_paged_attend")
 
 
 def ig_rope_turns(rot, theta, scaling, factor, context, p0, p1, turns) -> float:
@@ -457,19 +487,20 @@ def ig_rope_turns(rot, theta, scaling, factor, context, p0, p1, turns) -> float:
 
 def ig_qk_norm_rope(stream, dtype, T, Hq, Hkv, d, rot, layout, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight,
                     eps, positions, turns, rot_scale, q_out, page, n_pages, slot, k_out, v_out):
-    _ok(_lib.ig_qk_norm_rope(_s(stream), dtype, T, Hq, Hkv, d, rot, layout, _rows(q, q_stride), q_stride,
-                             _rows(k, k_stride), k_stride, _rows(v, v_stride), v_stride, _p(q_weight), _p(k_weight), eps,
-                             _p(positions), _p(turns), rot_scale, _p(q_out), page, n_pages, _p(slot), _p(k_out),
-                             _p(v_out)), "ig_qk_norm_rope")
+    h = _here()
+    _ok(_lib.ig_qk_norm_rope(_s(stream), dtype, T, Hq, Hkv, d, rot, layout, _rows(q, q_stride, h), q_stride,
+                             _rows(k, k_stride, h), k_stride, _rows(v, v_stride, h), v_stride, _q(q_weight, h),
+                             _q(k_weight, h), eps, _q(positions, h), _q(turns, h), rot_scale, _q(q_out, h), page, n_pages,
+                             _q(slot, h), _q(k_out, h), _q(v_out, h)), "ig_qk_norm_rope")
 
 
 def ig_page_copy(stream, layers, n_pages, Hkv, page, d, K, V, n, moves):
     """K, V: lists of every layer's device pages."""
     if len(K) != layers or len(V) != layers:
         raise ValueError("one K and one V per layer")
-    K, V = _ptr_array(K), _ptr_array(V)
-    _ok(_lib.ig_page_copy(_s(stream), layers, n_pages, Hkv, page, d, C.cast(K, _vp), C.cast(V, _vp), n, _p(moves)),
-        "ig_page_copy")
+    h, arr = _here(), _vp * layers
+    K, V = arr(*[_q(x, h) for x in K]), arr(*[_q(x, h) for x in V])
+    _ok(_lib.ig_page_copy(_s(stream), layers, n_pages, Hkv, page, d, K, V, n, _q(moves, h)), "ig_page_copy")
 
 
 def ig_pages_create(n_pages, page, seqs, max_pages) -> int:
@@ -576,8 +607,7 @@ _sig("ig_decoder_graph_launch", _i, _vp, _vp)
 
 
 def _ptr_array(items):
-    arr = (_vp * len(items))(*[_p(t) for t in items])
-    return arr
+    return (_vp * len(items))(*[_p(t) for t in items])
 
 
 def ig_decoder_workspace_bytes(cfg: DecoderConfig) -> int:

@@ -311,6 +311,40 @@ def test_attend_parts_join_by_their_lse(ig):
     assert torch.allclose(torch.logaddexp(parts[0][1].double(), parts[1][1].double()), lse.double(), rtol=0, atol=1e-4)
 
 
+def test_attend_waits_that_run_out_are_reported(ig):
+    """A wait limit of 0 makes every wait for a tile give up at once: the call ends by itself, ig_check
+    names the timeout, and the next call is right again."""
+    c = make_attend(13, "f16", [3000, 5], 8, 2, 128, 16)
+    want = attend(ig, c)
+    ig.ig_check()
+    ig.ig_set_wait_limit(0)
+    try:
+        attend(ig, c)
+        with pytest.raises(ig.IGError) as e:
+            ig.ig_check()
+        assert e.value.status == ig.IG_ERR_TIMEOUT
+    finally:
+        ig.ig_set_wait_limit(-1)
+    got = attend(ig, c)
+    ig.ig_check()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_tensors_of_another_device_are_refused(ig, monkeypatch):
+    c = make_attend(14, "f16", [5], 1, 1, 64, 8)
+    args = make_rope(ig, 1, "f16", 1, 1, 1, 64, 0, 0, False, 0)
+    n = ig.ig_launch_count()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)  # as on a machine with two
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        attend(ig, c, ws=ws, stream=0)
+    with pytest.raises(ValueError):
+        rope(ig, args, stream=0)
+    with pytest.raises(ValueError):
+        ig.ig_page_copy(0, 1, c["n"], 1, 8, 64, [c["K"]], [c["V"]], 0, None)
+    assert ig.ig_launch_count() == n
+
+
 # ---------------------------------------------------------------------------------------
 # norm and rotation
 # ---------------------------------------------------------------------------------------
