@@ -179,11 +179,14 @@ struct PaWalk {
     nt = (L + TT - 1) / TT;
   }
   __device__ void start(int seq, int offset, int tiles) {
-    left = tiles;
-    base = seq;
     const int lane = threadIdx.x & 31;
+    base = seq;
     len_here = bounded(base + lane);
     len_next = bounded(base + 32 + lane);
+    start_here(seq, offset, tiles);
+  }
+  __device__ void start_here(int seq, int offset, int tiles) {  // with the lengths in hand
+    left = tiles;
     enter(seq);
     off = whole ? offset * nt : offset;
   }
@@ -243,31 +246,42 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     fence_mbar_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  const int per = (s.B + kPaThreads - 1) / kPaThreads;
-  const int b0 = min(s.B, (int)threadIdx.x * per), b1 = min(s.B, b0 + per);
-  auto tiles_of = [&](int b) -> int {
+  pdl_wait();
+  auto length = [&](int b) -> int {
     int L = __ldg(L_valid + b);
     if (L < 0 || L > max_len) {
       raise_error(err, IG_DEVERR_INDEX);
       L = L < 0 ? 0 : max_len;
     }
-    return (s.whole ? min(L, 1) : (L + TT - 1) / TT) * per_seq;
+    return L;
   };
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+  auto tiles_of = [&](int L) -> int { return (s.whole ? min(L, 1) : (L + TT - 1) / TT) * per_seq; };
+  // the sums before each thread's sequences: a sequence per lane of every warp, or, for more than 32,
+  // a run of sequences per thread
+  const bool few = s.B <= 32;
+  const int per = few ? 1 : (s.B + kPaThreads - 1) / kPaThreads;
+  const int b0 = min(s.B, (few ? lane : (int)threadIdx.x) * per), b1 = min(s.B, b0 + per);
+  int mine = 0, len = 0;
+  for (int b = b0; b < b1; ++b) {
+    len = length(b);
+    mine += tiles_of(len);
+  }
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) sh.scan[warp] = incl;
-  __syncthreads();
-  int before = incl - mine, total = 0;
+  int before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
+  if (!few) {
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < kPaThreads / 32; ++w) {
-    before += w < warp ? sh.scan[w] : 0;
-    total += sh.scan[w];
+    for (int w = 0; w < kPaThreads / 32; ++w) {
+      before += w < warp ? sh.scan[w] : 0;
+      total += sh.scan[w];
+    }
   }
   // in tiles, or in heads; with fewer than CTAs the first `ctas` get one each
   const int ctas = min((int)gridDim.x, total), cta = blockIdx.x;
@@ -275,20 +289,8 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   if (cta < ctas) {
     r0 = (int)((long long)total * cta / ctas);
     r1 = (int)((long long)total * (cta + 1) / ctas);
-    if (r0 >= before && r0 < before + mine) {  // in this thread's sequences
-      int at = before;
-      for (int b = b0; b < b1; ++b) {
-        const int n = tiles_of(b);
-        if (r0 < at + n) {
-          sh.start_b = b;
-          sh.start_off = r0 - at;
-          break;
-        }
-        at += n;
-      }
-    }
   }
-  __syncthreads();
+  const bool here = r1 > r0 && r0 >= before && r0 < before + mine;  // it starts in this thread's sequences
   PaWalk<TT> w;
   w.L_valid = L_valid;
   w.B = s.B;
@@ -297,7 +299,32 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   w.whole = s.whole;
   w.b = w.off = w.L = w.left = 0;
   w.nt = 1;
-  if (r1 > r0) w.start(sh.start_b, sh.start_off, r1 - r0);
+  if (few) {
+    const unsigned at = __ballot_sync(0xffffffffu, here);
+    w.base = 0;
+    w.len_here = len;
+    w.len_next = 0;
+    if (at) {
+      const int seq = __ffs(at) - 1;
+      w.start_here(seq, r0 - __shfl_sync(0xffffffffu, before, seq), r1 - r0);
+    }
+    __syncthreads();  // the barriers are set up
+  } else {
+    if (here) {
+      int at = before;
+      for (int b = b0; b < b1; ++b) {
+        const int n = tiles_of(length(b));
+        if (r0 < at + n) {
+          sh.start_b = b;
+          sh.start_off = r0 - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    __syncthreads();
+    if (r1 > r0) w.start(sh.start_b, sh.start_off, r1 - r0);
+  }
 
   if (warp == kPaWarps) {
     // ---- producer.  The tiles of a head are taken in windows of 32 pages, a page number per lane;
@@ -723,6 +750,7 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const float* __res
                                                              float* __restrict__ out, float* __restrict__ lse) {
   constexpr int VEC = D / 32, WPR = kPjWarps / RB;
   __shared__ float sm[kPjWarps], sl[kPjWarps], so[kPjWarps][D];
+  pdl_trigger();
   pdl_wait();
   const int2 e = info[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -839,8 +867,10 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
   s.whole = s.by_unit && most <= units * kPaWhole ? 1 : 0;
   float* part = static_cast<float*>(ws);
   int2* info = reinterpret_cast<int2*>(static_cast<char*>(ws) + pa_part_bytes(s.G, D));
-  k_paged_attend<BF, D, NQ, WQ><<<grid, pa_threads(WQ), smem, st>>>(mk, mv, q, table, L, s, out, lse, part, info,
-                                                               error_word());
+  // a programmatic dependent launch: its CTAs set up while the kernel before it in the stream drains
+  e = launch_pdl(k_paged_attend<BF, D, NQ, WQ>, dim3(grid), dim3(pa_threads(WQ)), smem, st, mk, mv, q, table, L, s, out,
+                 lse, part, info, error_word());
+  if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   IG_CHECK_LAUNCH("paged attention launch");
   if (grid == 1 || s.whole) return IG_OK;  // nothing was cut
   // a row's partials are many only when there are few units: then a row gets a whole block

@@ -78,6 +78,8 @@ constexpr int kRopeWarpsPerSm = 32;
 template <bool BF, int D>
 __global__ void __launch_bounds__(kRopeThreads, 5) k_qk_norm_rope(const RopeArgs a, int* err) {
   constexpr int GL = D / 16, RPW = 32 / GL;
+  pdl_trigger();  // the attention that reads the pages may set up meanwhile
+  pdl_wait();
   const long long item = (long long)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
   if (item >= (long long)a.T * a.chunks) return;
   const int t = (int)(item / a.chunks), h0 = (int)(item % a.chunks) * a.chunk, h1 = min(a.heads, h0 + a.chunk);
@@ -223,7 +225,8 @@ ig_status launch_rope(cudaStream_t st, RopeArgs a) {
   a.chunk = ((a.heads + a.chunks - 1) / a.chunks + RPW - 1) / RPW * RPW;
   a.chunks = (a.heads + a.chunk - 1) / a.chunk;
   const long long items = (long long)a.T * a.chunks, ctas = (items + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  k_qk_norm_rope<BF, D><<<(unsigned)ctas, kRopeThreads, 0, st>>>(a, error_word());
+  const cudaError_t e = launch_pdl(k_qk_norm_rope<BF, D>, dim3((unsigned)ctas), dim3(kRopeThreads), 0, st, a, error_word());
+  if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
   IG_CHECK_LAUNCH("norm and rotation launch");
   return IG_OK;
 }
