@@ -763,38 +763,57 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const float* __res
 #pragma unroll
   for (int i = 0; i < VEC; ++i) o[i] = 0.f;
   if (live) {
-    // U partials' loads in flight
-    constexpr int U = 4;
-    for (int j0 = warp % WPR; j0 < n; j0 += WPR * U) {
-      float pm[U], pl[U], po[U][VEC];
+    // this warp's partials are w0, w0 + WPR, ...: 32 maxima and sums at a time (one per lane), outputs U at
+    // a time, the first U on their way before the maxima are there
+    constexpr int U = 8;
+    const int w0 = warp % WPR, mine = (n - w0 + WPR - 1) / WPR;
+    auto at = [&](int i) -> const float* {
+      const int j = w0 + i * WPR;
+      return part + ((size_t)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * RU + row) * (D + kPaPartHead);
+    };
+    auto load = [&](int i0, float (&v)[U][VEC]) {
 #pragma unroll
       for (int x = 0; x < U; ++x) {
-        const int j = j0 + x * WPR;
-        pm[x] = -INFINITY;
-        pl[x] = 0.f;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) po[x][i] = 0.f;
-        if (j < n) {
-          const float* p = part + ((size_t)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * RU + row) * (D + kPaPartHead);
-          const float2 h = *reinterpret_cast<const float2*>(p);
-          pm[x] = h.x;
-          pl[x] = h.y;
-#pragma unroll
-          for (int i = 0; i < VEC; i += 2) {
-            const float2 y = *reinterpret_cast<const float2*>(p + kPaPartHead + lane * VEC + i);
-            po[x][i] = y.x;
-            po[x][i + 1] = y.y;
+        if (i0 + x < mine) {
+          const float* p = at(i0 + x) + kPaPartHead + lane * VEC;
+          if constexpr (VEC == 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p);
+            v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
+          } else {
+            const float2 y = *reinterpret_cast<const float2*>(p);
+            v[x][0] = y.x, v[x][1] = y.y;
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[x][i] = 0.f;
         }
       }
+    };
+    float v[U][VEC];
+    for (int b0 = 0; b0 < mine; b0 += 32) {
+      load(b0, v);
+      const float2 h = b0 + lane < mine ? *reinterpret_cast<const float2*>(at(b0 + lane)) : make_float2(-INFINITY, 0.f);
+      float mx = h.x;
 #pragma unroll
-      for (int x = 0; x < U; ++x) {
-        const float mn = fmaxf(m, pm[x]), m0 = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2(m - m0), g = ex2(pm[x] - m0);
-        l = l * f + pl[x] * g;
+      for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mn = fmaxf(m, mx), m0 = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - m0), g = ex2(h.x - m0);
+      float sum = h.y * g;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = o[i] * f + po[x][i] * g;
-        m = mn;
+      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l = l * f + sum;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] *= f;
+      m = mn;
+      for (int i0 = 0; i0 < 32 && b0 + i0 < mine; i0 += U) {
+        if (i0) load(b0 + i0, v);
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          const float gx = __shfl_sync(0xffffffffu, g, i0 + x);
+          // (a partial past the end has weight 0 and values 0)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) o[i] = fmaf(v[x][i], gx, o[i]);
+        }
       }
     }
   }
