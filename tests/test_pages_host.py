@@ -238,7 +238,7 @@ def test_no_tokens_and_no_moves_do_nothing(ig):
 
 @pytest.mark.parametrize("bad", [dict(layers=0), dict(layers=129), dict(n_pages=0), dict(Hkv=0), dict(page=12), dict(page=0),
                                  dict(d=60), dict(d=0), dict(n=-1), dict(K=0), dict(V=8), dict(moves=None), dict(moves=2),
-                                 dict(n_pages=1 << 28)])
+                                 dict(n_pages=1 << 28), dict(n_pages=1, page=1 << 23, d=512)])
 def test_page_copy_refusals(ig, bad):
     a = dict(layers=2, n_pages=4, Hkv=2, page=16, d=64, K=1 << 20, V=2 << 20, n=1, moves=4)
     a.update(bad)
