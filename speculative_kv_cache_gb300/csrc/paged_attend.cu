@@ -8,16 +8,19 @@
 //
 // What bounds it.  Every key and value is read once from HBM and used by G queries: 4 d G flop for
 // 4 d bytes.  From G = 8 on that is more than the fp32 units do at HBM speed, so the products run
-// on the tensor cores (mma.sync: with at most 64 queries there is no 128-row tile for tcgen05 to
-// fill, and the copies, not the products, set the time).  Tokens are the 16 rows of an MMA, queries
-// its 8 columns: S^T = K Q^T, then O^T = V^T P^T, which costs no padding at G = 8 and at G = 1 leaves
-// the tensor cores far from full.
+// on the tensor cores.  Tokens are the 16 rows of an MMA (mma.sync), queries its 8 columns: S^T = K Q^T,
+// then O^T = V^T P^T, which costs no padding at G = 8 and at G = 1 leaves the tensor cores far from
+// full (13 % busy at G = 5).  Not tcgen05: its M = 128 holds at most 64 queries twice, an MMA of it takes
+// the same 72 cycles at N = 64 as at N = 128, and a tile's two dependent batches wait 500 more; such a
+// kernel took 27 us where this takes 24 to 26 (16 sequences of 4099 tokens, G = 56) and was ahead only
+// in very long caches (34 against 43 us at 4 x 32768, G = 64), which the host cannot see coming.
 //
 // Precision.  K, V, q enter as they are.  A weight in fp16 or bf16 alone would cost 2^-11 or 2^-8, so
 // it is split into 16-bit parts that are multiplied in turn: two for fp16 (scaled by 2^15 so that
 // the second part of a small weight stays normal; 22 bits), three for bf16 (24 bits).  Sums over the
-// tokens of one tile run in the tensor cores, which truncate; those over tiles in fp32 adds that
-// round to nearest, so that long sequences collect no bias.
+// tokens of one tile run in the tensor cores, whose adds need not round to nearest; those over tiles in
+// fp32 adds that do, so that long sequences collect no bias.  (2-norm error against 64 bits 3e-7 to 6e-7,
+// plain fp32 torch operations 2e-7 to 1.2e-6.)
 //
 // Work split.  The tokens of every (sequence, key head) are cut into tiles of 16 KB of keys and values,
 // and CTA c of G takes tiles [R c / G, R (c+1) / G) of all R, in sequence and head order: equal shares
@@ -26,11 +29,21 @@
 // and the head it ends with), joined in order by a second kernel, a programmatic dependent launch.
 // No atomics: the result does not depend on timing.
 //
-// A CTA is one producer warp and three or four consumer warps.  The producer walks the tiles, looks the
-// pages up one tile ahead, and moves each tile with TMA (a page's rows of one head are contiguous;
-// boxes of 64-column halves, 128-byte swizzle) into a ring of stages; a stage is consumed by one warp (or,
-// for more than 16 queries, by as many warps as it takes, each with its own queries), the stages in
-// turn.  A warp folds its tiles into its own (m, l, o); the warps join where a head ends.
+// A CTA is one producer warp and three or four consumer warps, two CTAs to an SM.  The producer walks the
+// tiles, looks the pages up a window of 32 ahead, and moves each tile with TMA (a page's rows of one head
+// are contiguous; a box is their two 64-column halves, 128-byte swizzle) into a ring of stages; a stage is
+// consumed by one warp (or, for more than 16 queries, by as many warps as it takes, each with its own
+// queries), the stages in turn.  A warp folds its tiles into its own (m, l, o); the warps join where a
+// head ends.
+//
+// Measured (device time, HBM copy rate 6.79 TB/s): 64 sequences of 0 to 8192 tokens, 8 key heads of 128, 1.08
+// GB: 164 us, 6.5 TB/s, 0.96 of the copy rate; one of 131071 tokens, 537 MB: 85.5 us, 0.92; 8 of 2000
+// tokens, 32 key heads, 260 MB: 47 us, 0.81 (a launch costs 7 us beside its bytes: launch 2, first loads 2,
+// tail 1, join 2); 4 heads of 256 tokens: 5.7 us.  16 of 4050 tokens, 56 heads on one key head, 33 MB: 28 us,
+// bound by the products (three parts of bf16 weights) of one or two warps per scheduler.  What the steps
+// gave: page numbers in windows instead of per tile 190 -> 165 us and 58 -> 47 us (one producer warp had
+// set the pace); four products side by side instead of one accumulator after the other 1550 -> 1150 cycles
+// a tile; heads of a few tiles to one warp each 22.5 -> 13.9 us (104 x 17 heads of 3 tokens).
 #include <cuda_bf16.h>
 #include <math.h>
 
