@@ -38,8 +38,8 @@
 //
 // Measured (device time, HBM copy rate 6.79 TB/s): 64 sequences of 0 to 8192 tokens, 8 key heads of 128, 1.08
 // GB: 164 us, 6.5 TB/s, 0.96 of the copy rate; one of 131071 tokens, 537 MB: 85.5 us, 0.92; 8 of 2000
-// tokens, 32 key heads, 260 MB: 47 us, 0.81 (a launch costs 7 us beside its bytes: launch 2, first loads 2,
-// tail 1, join 2); 4 heads of 256 tokens: 5.7 us.  16 of 4050 tokens, 56 heads on one key head, 33 MB: 28 us,
+// tokens, 32 key heads, 260 MB: 43 us, 0.89 (47 us where its 256 heads were cut); a launch costs 5 us beside
+// its bytes (launch 2, first loads 2, tail 1) and the join 3; 4 heads of 256 tokens: 5.8 us.  16 of 4050 tokens, 56 heads on one key head, 33 MB: 28 us,
 // bound by the products (three parts of bf16 weights) of one or two warps per scheduler.  What the steps
 // gave: page numbers in windows instead of per tile 190 -> 165 us and 58 -> 47 us (one producer warp had
 // set the pace); four products side by side instead of one accumulator after the other 1550 -> 1150 cycles
@@ -59,8 +59,11 @@ constexpr int kPaStageBytes = 16384;              // keys and values of one tile
 // Tiles of a head that one warp takes alone, where its CTA has other heads for the other warps (149 x 11
 // heads of 106 to 212 tokens: 42.3 us at 2, 39.7 at 4, 38.2 at 8, where 167 x 6 heads of 397 lose 10 %).
 constexpr int kPaSolo = 4;
-// Tiles of the longest head up to which heads are not cut, when every head has a CTA of its own
+// Heads that could have a CTA each are not cut where the longest has at most kPaWhole tiles (the join costs
+// 2 us, a tile 0.8 us: 4 heads of 256 tokens take 7.4 us cut, 6.2 us whole), or where there are enough of
+// them to keep HBM busy (one per SM) and the longest is at most kPaEven tiles above the mean.
 constexpr int kPaWhole = 6;
+constexpr int kPaEven = 3;
 constexpr int kPaPartHead = 4;                    // a partial: [max, sum, -, -, output[D]]
 
 template <int D>
@@ -79,7 +82,6 @@ struct PaShape {
   int box;                 // rows of a TMA box, a power of two that divides page
   float scale2;            // scale * log2(e)
   int by_unit;             // info is indexed by unit (units <= CTAs) or by CTA
-  int whole;               // the shares are in heads, not tiles: no head is cut
 };
 
 // shared memory behind the ring
@@ -93,8 +95,8 @@ struct PaShared {
   unsigned long long valid[pa_stages(WQ)];  // tokens of the stage that count
   uint32_t tile[pa_stages(WQ)];             // the tile (of the CTA's) it is for
   uint64_t full[pa_stages(WQ)], empty[pa_stages(WQ)];
-  int scan[pa_threads(WQ) / 32];
-  int start_b, start_off, total;
+  int scan[pa_threads(WQ) / 32][3];
+  int start_b, start_off;
   int abort;
 };
 
@@ -268,35 +270,55 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     }
     return L;
   };
-  auto tiles_of = [&](int L) -> int { return (s.whole ? min(L, 1) : (L + TT - 1) / TT) * per_seq; };
-  // the sums before each thread's sequences: a sequence per lane of every warp, or, for more than 32,
-  // a run of sequences per thread
+  // the sums before each thread's sequences (of tiles, and of sequences that have any): a sequence per lane
+  // of every warp, or, for more than 32, a run of sequences per thread
   const bool few = s.B <= 32;
   const int per = few ? 1 : (s.B + kPaThreads - 1) / kPaThreads;
   const int b0 = min(s.B, (few ? lane : (int)threadIdx.x) * per), b1 = min(s.B, b0 + per);
-  int mine = 0, len = 0;
+  int tiles = 0, used = 0, longest = 0, len = 0;
   for (int b = b0; b < b1; ++b) {
     len = length(b);
-    mine += tiles_of(len);
+    const int n = (len + TT - 1) / TT;
+    tiles += n;
+    used += n > 0;
+    longest = max(longest, n);
   }
-  int incl = mine;
+  int tiles_in = tiles, used_in = used;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int y = __shfl_up_sync(0xffffffffu, tiles_in, o), y2 = __shfl_up_sync(0xffffffffu, used_in, o);
+    if (lane >= o) {
+      tiles_in += y;
+      used_in += y2;
+    }
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
   }
-  int before = incl - mine, total = __shfl_sync(0xffffffffu, incl, 31);
+  int tiles_before = tiles_in - tiles, used_before = used_in - used;
+  int all_tiles = __shfl_sync(0xffffffffu, tiles_in, 31), all_used = __shfl_sync(0xffffffffu, used_in, 31);
   if (!few) {
-    if (lane == 31) sh.scan[warp] = incl;
+    if (lane == 31) {
+      sh.scan[warp][0] = tiles_in;
+      sh.scan[warp][1] = used_in;
+      sh.scan[warp][2] = longest;
+    }
     __syncthreads();
-    total = 0;
+    all_tiles = all_used = 0;
 #pragma unroll
     for (int w = 0; w < kPaThreads / 32; ++w) {
-      before += w < warp ? sh.scan[w] : 0;
-      total += sh.scan[w];
+      tiles_before += w < warp ? sh.scan[w][0] : 0;
+      used_before += w < warp ? sh.scan[w][1] : 0;
+      all_tiles += sh.scan[w][0];
+      all_used += sh.scan[w][1];
+      longest = max(longest, sh.scan[w][2]);
     }
   }
-  // in tiles, or in heads; with fewer than CTAs the first `ctas` get one each
+  // heads are cut, and shares counted in tiles; or not, and shares counted in heads
+  const bool uncut = s.by_unit && (longest <= kPaWhole || (2 * all_used * per_seq >= (int)gridDim.x &&
+                                                           (long long)longest * all_used <= all_tiles + kPaEven * all_used));
+  auto share_of = [&](int L) -> int { return (uncut ? min(L, 1) : (L + TT - 1) / TT) * per_seq; };
+  const int before = (uncut ? used_before : tiles_before) * per_seq, mine = (uncut ? used : tiles) * per_seq;
+  const int total = (uncut ? all_used : all_tiles) * per_seq;
+  // with fewer shares than CTAs the first `ctas` get one each
   const int ctas = min((int)gridDim.x, total), cta = blockIdx.x;
   int r0 = 0, r1 = 0;
   if (cta < ctas) {
@@ -309,7 +331,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   w.B = s.B;
   w.per_seq = per_seq;
   w.max_len = max_len;
-  w.whole = s.whole;
+  w.whole = uncut;
   w.b = w.off = w.L = w.left = 0;
   w.nt = 1;
   if (few) {
@@ -326,7 +348,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     if (here) {
       int at = before;
       for (int b = b0; b < b1; ++b) {
-        const int n = tiles_of(length(b));
+        const int n = share_of(length(b));
         if (r0 < at + n) {
           sh.start_b = b;
           sh.start_off = r0 - at;
@@ -754,9 +776,9 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
 }
 
 // Joins the partials of the heads that were cut: block (x, y) takes unit x (or the head that CTA x
-// began) and rows y * RB ... of it; a row's partials are spread over the 8 / RB warps it has, taken
+// began) and rows y * RB ... of it; a row's partials are spread over the 4 / RB warps it has, taken
 // in order, and the warps join in order.
-constexpr int kPjWarps = 8;
+constexpr int kPjWarps = 4;  // (8: the blocks do not fit beside the attention's: 1 us more)
 template <int D, int RB>
 __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const float* __restrict__ part, const int2* __restrict__ info,
                                                              const PaShape s, int RU, float scale_bits,
@@ -894,9 +916,6 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
   if (grid > most) grid = (int)most;
   const long long units = (long long)s.B * s.Hkv * s.QT;
   s.by_unit = units <= grid ? 1 : 0;
-  // Short heads with a CTA each are not cut: the join costs 2 us, a tile 0.8 us (4 heads of 256 tokens:
-  // 7.4 us cut and joined).
-  s.whole = s.by_unit && most <= units * kPaWhole ? 1 : 0;
   float* part = static_cast<float*>(ws);
   int2* info = reinterpret_cast<int2*>(static_cast<char*>(ws) + pa_part_bytes(s.G, D));
   // a programmatic dependent launch: its CTAs set up while the kernel before it in the stream drains
@@ -904,7 +923,7 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
                  lse, part, info, error_word());
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   IG_CHECK_LAUNCH("paged attention launch");
-  if (grid == 1 || s.whole) return IG_OK;  // nothing was cut
+  if (grid == 1 || (s.by_unit && most <= units * kPaWhole)) return IG_OK;  // nothing can have been cut
   // a row's partials are many only when there are few units: then a row gets a whole block
   const int rows_used = s.G < RU ? s.G : RU, list = s.by_unit ? (int)units : grid;
   const float bits = BF ? 0.f : 15.f;
