@@ -165,6 +165,19 @@ def test_attend_splits_over_length_and_batch(ig, B, Hq, Hkv, d, page, dt, hi):
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("B,Hkv,lo,hi", [(24, 8, 700, 720), (40, 5, 1, 190), (25, 8, 500, 700), (160, 1, 640, 660),
+                                         (33, 9, 900, 990)])
+@pytest.mark.parametrize("group,dt", [(1, "f16"), (5, "bf16"), (20, "f16")])
+def test_attend_heads_with_a_cta_each(ig, B, Hkv, lo, hi, group, dt):
+    """As many heads as CTAs or fewer: not cut where they are short or near even, cut otherwise; the first
+    sequences are empty."""
+    lengths = [0, 0] + [lo + (b * 37) % (hi - lo + 1) for b in range(B - 2)]
+    c = make_attend(B + hi, dt, lengths, Hkv * group, Hkv, 64, 32)
+    out, lse = attend(ig, c)
+    ig.ig_check()
+    check_attend(c, out, lse)
+
+
 def test_attend_without_lse_and_with_a_negative_scale(ig):
     c = make_attend(3, "f16", [100, 33], 4, 4, 64, 16)
     c["scale"] = -0.3
