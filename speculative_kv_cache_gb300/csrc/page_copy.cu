@@ -19,7 +19,8 @@ __global__ void __launch_bounds__(kCopyThreads) k_page_copy(const CopyLayers P, 
                                                            const int32_t* __restrict__ moves, int* err) {
   pdl_trigger();
   pdl_wait();
-  const int src = moves[3 * blockIdx.x], dst = moves[3 * blockIdx.x + 1], rows = moves[3 * blockIdx.x + 2];
+  const int32_t* mv = moves + 3 * (size_t)blockIdx.x;
+  const int src = __ldca(mv), dst = __ldca(mv + 1), rows = __ldca(mv + 2);
   if (src < 0) return;
   if (src >= n_pages || dst < 0 || dst >= n_pages || rows < 0 || rows > page) {
     if (threadIdx.x == 0) raise_error(err, IG_DEVERR_INDEX);

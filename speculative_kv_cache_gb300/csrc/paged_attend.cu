@@ -12,8 +12,8 @@
 // then O^T = V^T P^T, which costs no padding at G = 8 and at G = 1 leaves the tensor cores far from
 // full (13 % busy at G = 5).  Not tcgen05: its M = 128 holds at most 64 queries twice, an MMA of it takes
 // the same 72 cycles at N = 64 as at N = 128, and a tile's two dependent batches wait 500 more; such a
-// kernel took 27 us where this takes 24 to 26 (16 sequences of 4099 tokens, G = 56) and was ahead only
-// in very long caches (34 against 43 us at 4 x 32768, G = 64), which the host cannot see coming.
+// kernel took 27 us where this takes 23 to 25 (16 sequences of 4099 tokens, G = 56) and was ahead only
+// in very long caches (34 against 40 us at 4 x 32768, G = 64), which the host cannot see coming.
 //
 // Precision.  K, V, q enter as they are.  A weight in fp16 or bf16 alone would cost 2^-11 or 2^-8, so
 // it is split into 16-bit parts that are multiplied in turn: two for fp16 (scaled by 2^15 so that
@@ -37,9 +37,9 @@
 // head ends.
 //
 // Measured (device time, HBM copy rate 6.79 TB/s): 64 sequences of 0 to 8192 tokens, 8 key heads of 128, 1.08
-// GB: 164 us, 6.5 TB/s, 0.96 of the copy rate; one of 131071 tokens, 537 MB: 85.5 us, 0.92; 8 of 2000
+// GB: 164 us, 6.5 TB/s, 0.96 of the copy rate; one of 131071 tokens, 537 MB: 83.7 us, 0.95; 8 of 2000
 // tokens, 32 key heads, 260 MB: 43 us, 0.89 (47 us where its 256 heads were cut); a launch costs 5 us beside
-// its bytes (launch 2, first loads 2, tail 1) and the join 3; 4 heads of 256 tokens: 5.8 us.  16 of 4050 tokens, 56 heads on one key head, 33 MB: 28 us,
+// its bytes (launch 2, first loads 2, tail 1) and the join 3; 4 heads of 256 tokens: 5.8 us.  16 of 4050 tokens, 56 heads on one key head, 33 MB: 27 us,
 // bound by the products (three parts of bf16 weights) of one or two warps per scheduler.  What the steps
 // gave: page numbers in windows instead of per tile 190 -> 165 us and 58 -> 47 us (one producer warp had
 // set the pace); four products side by side instead of one accumulator after the other 1550 -> 1150 cycles
@@ -175,6 +175,9 @@ __device__ __forceinline__ bool pa_wait_tile(const volatile uint32_t* tile, uint
   return false;
 }
 
+// (The kernels here start before the ones before them have ended, so what those write is read by plain
+// (ld.ca) loads, not by the read-only path, which asks for data that stay as they are for a kernel's whole life.)
+//
 // The tiles of a CTA's share, in order, head by head; all lanes of a warp walk together.
 template <int TT>
 struct PaWalk {
@@ -185,7 +188,7 @@ struct PaWalk {
   int base, len_here, len_next;
 
   __device__ int bounded(int i) const {
-    const int v = i < B ? __ldg(L_valid + i) : 0;
+    const int v = i < B ? __ldca(L_valid + i) : 0;
     return v < 0 ? 0 : v > max_len ? max_len : v;
   }
   __device__ void enter(int seq) {
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   }
   pdl_wait();
   auto length = [&](int b) -> int {
-    int L = __ldg(L_valid + b);
+    int L = __ldca(L_valid + b);
     if (L < 0 || L > max_len) {
       raise_error(err, IG_DEVERR_INDEX);
       L = L < 0 ? 0 : max_len;
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       first = (int)((long long)tile * TT / s.page);
       const long long covered = ((long long)first + 32) * s.page / TT - tile;
       const bool in = (long long)(first + lane) * s.page < at.L;
-      id = in ? __ldg(table + (size_t)at.b * s.max_pages + first + lane) : -1;
+      id = in ? __ldca(table + (size_t)at.b * s.max_pages + first + lane) : -1;
       const int run = at.run();
       return covered < run ? (int)covered : run;
     };
@@ -474,12 +477,15 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       const uint16_t* qp = q + ((size_t)b * s.Hq + (size_t)hk * s.G + qrow) * D;
       uint32_t qf[QS ? 1 : D / 16][NQ][2];
       if constexpr (QS) {
-        __syncwarp();
-        for (int i = lane; i < NQ * 8 * (D / 8); i += 32) {
-          const int r = i / (D / 8), c = i % (D / 8);
-          sh.q[warp][r][c] = qrow + r < s.G ? __ldg(reinterpret_cast<const uint4*>(qp + (size_t)r * D) + c)
-                                            : make_uint4(0, 0, 0, 0);
+        uint4 v[NQ * D / 32];  // all on their way before the first is put down
+#pragma unroll
+        for (int i = 0; i < NQ * D / 32; ++i) {
+          const int r = (i * 32 + lane) / (D / 8), c = (i * 32 + lane) % (D / 8);
+          v[i] = qrow + r < s.G ? __ldca(reinterpret_cast<const uint4*>(qp + (size_t)r * D) + c) : make_uint4(0, 0, 0, 0);
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NQ * D / 32; ++i) sh.q[warp][(i * 32 + lane) / (D / 8)][(i * 32 + lane) % (D / 8)] = v[i];
         __syncwarp();
       } else {
 #pragma unroll
@@ -488,8 +494,8 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
           for (int j = 0; j < NQ; ++j) {
             const bool in = qrow + j * 8 + gl < s.G;
             const uint16_t* p = qp + (size_t)(j * 8 + gl) * D + ks * 16 + tl * 2;
-            qf[ks][j][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(p)) : 0u;
-            qf[ks][j][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(p + 8)) : 0u;
+            qf[ks][j][0] = in ? __ldca(reinterpret_cast<const uint32_t*>(p)) : 0u;
+            qf[ks][j][1] = in ? __ldca(reinterpret_cast<const uint32_t*>(p + 8)) : 0u;
           }
       }
       float m[NQ][2], l[NQ][2], o[D / 16][NQ][4];
@@ -763,7 +769,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     if (threadIdx.x == 0 && !s.by_unit && !cut) info[cta] = make_int2(-1, 0);
     // sequences without a token
     for (int b = cta; b < s.B; b += gridDim.x) {
-      if (__ldg(L_valid + b) > 0) continue;
+      if (__ldca(L_valid + b) > 0) continue;
       for (int i = threadIdx.x; i < s.Hq * D / 4; i += kPaWarps * 32)
         reinterpret_cast<float4*>(out + (size_t)b * s.Hq * D)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (lse)
@@ -776,18 +782,18 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
 }
 
 // Joins the partials of the heads that were cut: block (x, y) takes unit x (or the head that CTA x
-// began) and rows y * RB ... of it; a row's partials are spread over the 4 / RB warps it has, taken
-// in order, and the warps join in order.
-constexpr int kPjWarps = 4;  // (8: the blocks do not fit beside the attention's: 1 us more)
-template <int D, int RB>
-__global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const float* __restrict__ part, const int2* __restrict__ info,
+// began) and rows y * RB ... of it, WPR warps a row; a warp takes every WPR-th partial in order, and the
+// warps join in order.  A warp a row where a head has few partials (blocks of four warps, which fit beside
+// the attention's: 1 us less than eight); with about 16 or more, four warps, with 64 or more, sixteen.
+template <int D, int WPR, int RB>
+__global__ void __launch_bounds__(WPR * RB * 32) k_paged_join(const float* __restrict__ part, const int2* __restrict__ info,
                                                              const PaShape s, int RU, float scale_bits,
                                                              float* __restrict__ out, float* __restrict__ lse) {
-  constexpr int VEC = D / 32, WPR = kPjWarps / RB;
-  __shared__ float sm[kPjWarps], sl[kPjWarps], so[kPjWarps][D];
+  constexpr int VEC = D / 32;
+  __shared__ float sm[WPR * RB], sl[WPR * RB], so[WPR * RB][WPR > 1 ? D : 1];
   pdl_trigger();
   pdl_wait();
-  const int2 e = info[blockIdx.x];
+  const int2 e = __ldca(info + blockIdx.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (e.x < 0) return;
   const int unit = s.by_unit ? (int)blockIdx.x : e.x, c0 = s.by_unit ? e.x : (int)blockIdx.x;
@@ -812,10 +818,10 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const float* __res
         if (i0 + x < mine) {
           const float* p = at(i0 + x) + kPaPartHead + lane * VEC;
           if constexpr (VEC == 4) {
-            const float4 y = *reinterpret_cast<const float4*>(p);
+            const float4 y = __ldca(reinterpret_cast<const float4*>(p));
             v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
           } else {
-            const float2 y = *reinterpret_cast<const float2*>(p);
+            const float2 y = __ldca(reinterpret_cast<const float2*>(p));
             v[x][0] = y.x, v[x][1] = y.y;
           }
         } else {
@@ -827,7 +833,7 @@ __global__ void __launch_bounds__(kPjWarps * 32) k_paged_join(const float* __res
     float v[U][VEC];
     for (int b0 = 0; b0 < mine; b0 += 32) {
       load(b0, v);
-      const float2 h = b0 + lane < mine ? *reinterpret_cast<const float2*>(at(b0 + lane)) : make_float2(-INFINITY, 0.f);
+      const float2 h = b0 + lane < mine ? __ldca(reinterpret_cast<const float2*>(at(b0 + lane))) : make_float2(-INFINITY, 0.f);
       float mx = h.x;
 #pragma unroll
       for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -924,17 +930,18 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
   if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
   IG_CHECK_LAUNCH("paged attention launch");
   if (grid == 1 || (s.by_unit && most <= units * kPaWhole)) return IG_OK;  // nothing can have been cut
-  // a row's partials are many only when there are few units: then a row gets a whole block
   const int rows_used = s.G < RU ? s.G : RU, list = s.by_unit ? (int)units : grid;
   const float bits = BF ? 0.f : 15.f;
   const float* cpart = part;
   const int2* cinfo = info;
-  if (grid >= 16 * units)
-    e = launch_pdl(k_paged_join<D, 1>, dim3(list, rows_used), dim3(kPjWarps * 32), 0, st, cpart, cinfo, s, RU, bits, out,
-                   lse);
-  else
-    e = launch_pdl(k_paged_join<D, kPjWarps>, dim3(list, (rows_used + kPjWarps - 1) / kPjWarps), dim3(kPjWarps * 32), 0,
-                   st, cpart, cinfo, s, RU, bits, out, lse);
+  const long long partials = grid / units;  // of a head, about
+#define IG_PJ(WPR, RB)                                                                                            \
+  e = launch_pdl(k_paged_join<D, WPR, RB>, dim3(list, (rows_used + RB - 1) / RB), dim3(WPR * RB * 32), 0, st, cpart, \
+                 cinfo, s, RU, bits, out, lse)
+  if (partials >= 64) IG_PJ(16, 1);
+  else if (partials >= 16) IG_PJ(4, 1);
+  else IG_PJ(1, 4);
+#undef IG_PJ
   if (e != cudaSuccess) return cuda_fail(e, "paged attention join launch");
   IG_CHECK_LAUNCH("paged attention join launch");
   return IG_OK;
@@ -971,10 +978,10 @@ extern "C" ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int
   IG_REQUIRE(d == 64 || d == 128, "d must be 64 or 128 (got %d)", d);
   IG_REQUIRE(page > 0 && page % 8 == 0, "page must be a positive multiple of 8 (got %d)", page);
   IG_REQUIRE(n_pages > 0 && max_pages > 0, "n_pages and max_pages must be positive");
-  IG_REQUIRE((long long)B * Hq < (1ll << 31), "B*Hq must stay below 2^31");
+  IG_REQUIRE(Hq <= 65536 && (long long)B * Hq < (1ll << 31), "Hq at most 65536, B*Hq below 2^31");
   IG_REQUIRE((long long)max_pages * page < (1ll << 30), "max_pages*page must stay below 2^30");
   IG_REQUIRE((double)n_pages * Hkv * page < 2147483648.0, "n_pages*Hkv*page must stay below 2^31 rows");
-  IG_REQUIRE(isfinite(scale), "scale must be finite");
+  IG_REQUIRE(isfinite(scale) && fabsf(scale) < 1e38f, "scale must be finite (and below 1e38)");
   IG_REQUIRE(q && K && V && page_table && L_valid && out, "null pointer argument");
   IG_REQUIRE(aligned(q, 16) && aligned(K, 16) && aligned(V, 16), "q, K, V must be 16-byte aligned");
   IG_REQUIRE(aligned(out, 16), "out must be 16-byte aligned");

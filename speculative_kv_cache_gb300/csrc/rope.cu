@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kRopeThreads, 5) k_qk_norm_rope(const RopeArgs
   size_t row = (size_t)t * a.Hkv, step = 1;
   bool put = true;
   if (a.page && h1 > a.Hq) {
-    const int sl = a.slot[t], at = sl / a.page;
+    const int sl = __ldca(a.slot + t), at = sl / a.page;
     if (sl < 0 || at >= a.n_pages) {
       put = false;
       if (sl >= 0 && lane == 0) raise_error(err, IG_DEVERR_INDEX);
@@ -130,12 +130,12 @@ __global__ void __launch_bounds__(kRopeThreads, 5) k_qk_norm_rope(const RopeArgs
   // (the angles while the first rows are on their way)
   float cs[8], sn[8];
   if (r0 && h0 < a.Hq + a.Hkv) {
-    const uint64_t p = (uint64_t)(int64_t)a.pos[t];
+    const uint64_t p = (uint64_t)(int64_t)__ldca(a.pos + t);
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
       const int j = a.layout == IG_ROPE_HALF ? 8 * i + x : 4 * (x < 4 ? c0 : c1) + (x & 3);
       if (a.layout == IG_ROPE_PAIRS && x >= 4 && !r1) continue;
-      const uint64_t at = p * __ldg(a.turns + j);
+      const uint64_t at = p * __ldca(reinterpret_cast<const unsigned long long*>(a.turns) + j);
       sincospif((float)(int32_t)((at + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn[x], &cs[x]);
       sn[x] *= a.rscale;
       cs[x] *= a.rscale;
@@ -159,8 +159,8 @@ __global__ void __launch_bounds__(kRopeThreads, 5) k_qk_norm_rope(const RopeArgs
 #pragma unroll
           for (int o = GL / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
           const float rn = rsqrtf(ss * (1.f / D) + a.eps);
-          unpack8<BF>(__ldg(reinterpret_cast<const uint4*>(w) + c0), w0);
-          unpack8<BF>(__ldg(reinterpret_cast<const uint4*>(w) + c1), w1);
+          unpack8<BF>(__ldca(reinterpret_cast<const uint4*>(w) + c0), w0);
+          unpack8<BF>(__ldca(reinterpret_cast<const uint4*>(w) + c1), w1);
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
             e[y] *= rn * w0[y];

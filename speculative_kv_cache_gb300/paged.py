@@ -56,7 +56,13 @@ class PagedCache:
     def _run_moves(self, moves):
         if len(moves):
             m = torch.from_numpy(np.ascontiguousarray(moves, dtype=np.int32)).to(self.dev)
-            ig.ig_page_copy(None, self.layers, self.n_pages, self.Hkv, self.page, self.d, self.K, self.V, len(moves), m)
+            for l in range(0, self.layers, 128):
+                K, V = self.K[l:l + 128], self.V[l:l + 128]
+                ig.ig_page_copy(None, len(K), self.n_pages, self.Hkv, self.page, self.d, K, V, len(moves), m)
+
+    def _check(self, name, x, *shape, dtype=None):
+        if x is not None and (x.numel() != math.prod(shape) or x.shape[0] != shape[0] or x.dtype != (dtype or self.dtype)):
+            raise ValueError(f"{name} must be {list(shape)} of {dtype or self.dtype}, got {list(x.shape)} of {x.dtype}")
 
     def extend(self, new):
         """Room for ``new[sequence]`` more tokens of each named sequence; returns device int32 slots
@@ -117,6 +123,14 @@ class PagedCache:
         into ``layer``'s pages; returns the new q.  q, k and v may be slices of one projection
         [T, heads * d] (the first dimension's stride is taken as it is)."""
         T = q.shape[0]
+        self._check("q", q, T, self.Hq, self.d)
+        self._check("k", k, T, self.Hkv, self.d)
+        self._check("v", v, T, self.Hkv, self.d)
+        self._check("slots", slots, T, dtype=torch.int32)
+        self._check("positions", positions, T, dtype=torch.int32)
+        self._check("q_weight", q_weight, self.d)
+        self._check("k_weight", k_weight, self.d)
+        self._check("q_out", q_out, T, self.Hq, self.d)
         if q_out is None:
             q_out = torch.empty((T, self.Hq, self.d), dtype=self.dtype, device=self.dev)
         # a lone row's stride may be anything: it is never used
@@ -129,6 +143,9 @@ class PagedCache:
     def attend(self, layer, q, out=None, lse=None):
         """Attention of one token per sequence, q [seqs, Hq, d], over all its tokens: fp32
         [seqs, Hq, d], zero for empty sequences."""
+        self._check("q", q, self.seqs, self.Hq, self.d)
+        self._check("out", out, self.seqs, self.Hq, self.d, dtype=torch.float32)
+        self._check("lse", lse, self.seqs, self.Hq, dtype=torch.float32)
         if out is None:
             out = torch.empty((self.seqs, self.Hq, self.d), dtype=torch.float32, device=self.dev)
         ig.ig_paged_attend(None, self.dt, self.seqs, self.Hq, self.Hkv, self.d, self.page, self.n_pages, self.max_pages,

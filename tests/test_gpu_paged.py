@@ -16,6 +16,9 @@ Tolerances.  u = 2^-23 bounds one fp32 operation, truncation included.
 * copies: equal.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -290,6 +293,39 @@ def test_attend_on_another_stream_and_replayed(ig):
         check_attend(c, out, lse)
     ig.ig_check()
     assert torch.equal(out, want[0])
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    """No call outside a graph before: every operator captured, then replayed."""
+    code = """
+import math, sys
+sys.path.insert(0, "tests")
+import torch
+from speculative_kv_cache_gb300 import ig
+import test_gpu_paged as t
+c = t.make_attend(1, "f16", [300, 0, 17], 8, 2, 128, 16)
+r = t.make_rope(ig, 2, "bf16", 5, 4, 2, 64, 64, 0, True, 8)
+K, V = torch.randn(4, 2, 8, 64, device="cuda").half(), torch.randn(4, 2, 8, 64, device="cuda").half()
+moves = t.i32([[0, 1, 8]])
+out = torch.zeros(3, 8, 128, device="cuda")
+lse = torch.zeros(3, 8, device="cuda")
+ws = torch.empty(ig.ig_paged_attend_workspace_bytes(3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    t.attend(ig, c, out, lse, ws)
+    t.rope(ig, r)
+    ig.ig_page_copy(None, 1, 4, 2, 8, 64, [K], [V], 1, moves)
+g.replay()
+torch.cuda.synchronize()
+ig.ig_check()
+t.check_attend(c, out, lse)
+t.check_rope(r, r["q"], r["k"], r["v"], r["qo"])
+assert torch.equal(K[0], K[1]) and torch.equal(V[0], V[1])
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-3000:]
 
 
 def test_attend_two_calls_at_once(ig):
@@ -677,6 +713,10 @@ def test_cache_of_forked_requests(ig, dt, d, rot, layout, page):
         assert int(cache.table.max()) == used - 1
         step({0: 1, 2: 2, 3: 1})
         before = cache.free_pages(), cache.L.tolist()
+        with pytest.raises(ValueError):
+            cache.attend(0, torch.zeros(seqs, Hq, d, device=DEV))  # fp32
+        with pytest.raises(ValueError):
+            cache.write(0, *[torch.zeros(2, n, d, dtype=DT[dt], device=DEV) for n in (Hq, Hkv, Hkv)], i32([0]), i32([0, 0]))
         with pytest.raises(ig.IGError) as e:
             cache.extend({2: 1, 1: 25 * page})
         assert e.value.status == ig.IG_ERR_CAPACITY and cache.L.tolist() == before[1]

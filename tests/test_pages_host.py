@@ -183,7 +183,7 @@ def _attend(ig, **k):
 
 @pytest.mark.parametrize("bad", [dict(dtype=2), dict(dtype=-1), dict(B=0), dict(Hq=0), dict(Hkv=0), dict(Hq=3), dict(d=96),
                                  dict(page=12), dict(page=0), dict(page=-8), dict(n_pages=0), dict(max_pages=0),
-                                 dict(scale=float("nan")), dict(scale=float("inf")), dict(q=None), dict(K=None),
+                                 dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=2e38), dict(Hq=1 << 17), dict(q=None), dict(K=None),
                                  dict(V=None), dict(page_table=None), dict(L_valid=None), dict(out=None), dict(q=264),
                                  dict(K=520), dict(V=770), dict(out=1540), dict(page_table=1026), dict(lse=2),
                                  dict(workspace=(1 << 20) + 16), dict(n_pages=1 << 28), dict(max_pages=1 << 27),
