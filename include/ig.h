@@ -440,7 +440,8 @@ ig_status ig_append_kv(void* stream, ig_pool* pool, int layer, int B, int H, int
  *   lse         dev fp32 [B][Hq] out, or NULL
  *   workspace   dev, >= ig_paged_attend_workspace_bytes(B, Hq, Hkv, d) bytes, 256-byte aligned;
  *               arbitrary content, not shared by calls that may run at the same time
- * dtype: IG_F16 or IG_BF16 (q, K and V).  d must be 64 or 128; scale finite. */
+ * dtype: IG_F16 or IG_BF16 (q, K and V).  d must be 64 or 128; |scale| < 1e38; Hq <= 65536, B * Hq < 2^31,
+ * max_pages * page < 2^30, n_pages * Hkv * page < 2^31, and fewer than 2^31 tiles of 16 KB in full tables. */
 size_t ig_paged_attend_workspace_bytes(int B, int Hq, int Hkv, int d);
 ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page,
                           int n_pages, int max_pages, float scale, const uint16_t* q,
@@ -497,7 +498,8 @@ ig_status ig_rope_turns(int rot, double theta, int scaling, double factor, int c
  *               may have the same slot (which one's pieces stay is not defined).
  *   page = 0:   k_out, v_out are dense [T][Hkv][d] (n_pages = 0, slot NULL); v and v_out may both be
  *               NULL
- * d must be 64 or 128; rot 0 or a multiple of 16 up to d; T >= 0. */
+ * d must be 64 or 128; rot 0 or a multiple of 16 up to d; T >= 0 (0: nothing is done), T * (Hq + 2 Hkv) and
+ * n_pages * Hkv * page < 2^31. */
 #define IG_ROPE_HALF 0
 #define IG_ROPE_PAIRS 1
 ig_status ig_qk_norm_rope(void* stream, int dtype, int T, int Hq, int Hkv, int d, int rot, int layout,
@@ -513,7 +515,8 @@ ig_status ig_qk_norm_rope(void* stream, int dtype, int T, int Hq, int Hkv, int d
  *   moves   dev int32 [n][3]: src, dst, rows (0 <= rows <= page).  src < 0: the move is skipped.
  *           A page or row count out of range sets IG_DEVERR_INDEX and the move is skipped.
  *           The moves run in no order: a dst may appear once, and as no other move's src.
- * At most 128 layers per call; d a multiple of 8; n >= 0. */
+ * At most 128 layers per call; d a multiple of 8; n >= 0 (0: nothing is done); n_pages * Hkv * page < 2^31 and a
+ * page below 16 GB. */
 ig_status ig_page_copy(void* stream, int layers, int n_pages, int Hkv, int page, int d,
                        uint16_t* const* K, uint16_t* const* V, int n, const int32_t* moves);
 
