@@ -324,9 +324,12 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
   // with fewer shares than CTAs the first `ctas` get one each
   const int ctas = min((int)gridDim.x, total), cta = blockIdx.x;
   int r0 = 0, r1 = 0;
+  // CTA c's first share, total c / ctas, without a 64-bit division
+  const unsigned each = ctas ? (unsigned)total / ctas : 0, rest = ctas ? (unsigned)total % ctas : 0;
+  auto first_of = [&](unsigned c) -> int { return (int)(each * c + rest * c / (unsigned)ctas); };
   if (cta < ctas) {
-    r0 = (int)((long long)total * cta / ctas);
-    r1 = (int)((long long)total * (cta + 1) / ctas);
+    r0 = first_of(cta);
+    r1 = first_of(cta + 1);
   }
   const bool here = r1 > r0 && r0 >= before && r0 < before + mine;  // it starts in this thread's sequences
   PaWalk<TT> w;
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     // tiles from where `at` stands that 32 pages cover, and the lane's page number
     auto window = [&](const PaWalk<TT>& at, int& first, int& id) -> int {
       const int tile = at.tile();
-      first = (int)((long long)tile * TT / s.page);
+      first = tile * TT / s.page;
       const long long covered = ((long long)first + 32) * s.page / TT - tile;
       const bool in = (long long)(first + lane) * s.page < at.L;
       id = in ? __ldca(table + (size_t)at.b * s.max_pages + first + lane) : -1;
@@ -757,10 +760,10 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       if (tg == owner && wq == 0 && lane == 0 && (cut || (s.by_unit && done))) {
         int last = cta;  // the CTA that holds the head's last tile
         if (cut) {
-          const long long end = (long long)r1 - run + nt - 1;  // a cut head is this CTA's last
-          last = (int)(end * ctas / total);
-          while (last + 1 < ctas && (long long)total * (last + 1) / ctas <= end) ++last;
-          while ((long long)total * last / ctas > end) --last;
+          const int end = r1 - run + nt - 1;  // its last tile: a cut head is this CTA's last
+          last = min(ctas - 1, (int)((float)end * ((float)ctas / (float)total)));  // within 1
+          while (last + 1 < ctas && first_of(last + 1) <= end) ++last;
+          while (first_of(last) > end) --last;
         }
         if (s.by_unit) info[unit] = make_int2(cut ? cta : -1, last);
         else info[cta] = make_int2(unit, last);
