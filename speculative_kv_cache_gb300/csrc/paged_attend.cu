@@ -616,8 +616,9 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
               for (int pp = 0; pp < PARTS; ++pp) p[pp][i][j][hh] = transpose8(split2<BF>(x0, x1));
             }
         }
-        // DG column tiles side by side, for the same reason
-        constexpr int DG = 4 / NQ;
+        // DG column tiles side by side, for the same reason (four of 16 queries where registers allow: 27.2 ->
+        // 26 us for 64 x 2048 tokens, 16 heads)
+        constexpr int DG = WQ == 1 ? 4 : 2;
 #pragma unroll
         for (int d0 = 0; d0 < D / 16; d0 += DG) {
           float acc[DG][NQ][4];
