@@ -24,6 +24,8 @@ class PagedCache:
                  layout=ig.IG_ROPE_HALF, theta=10000.0, scaling=ig.IG_ROPE_PLAIN, factor=1.0, context=0, p0=0.0, p1=0.0,
                  eps=1e-6, device="cuda:0"):
         self.pages = None
+        if dtype not in _DTYPES:
+            raise ValueError(f"pages hold float16 or bfloat16, not {dtype}")
         self.layers, self.Hq, self.Hkv, self.d = layers, Hq, Hkv, d
         self.n_pages, self.seqs, self.max_pages, self.page = n_pages, seqs, max_pages, page
         self.dtype, self.dt = dtype, _DTYPES[dtype]

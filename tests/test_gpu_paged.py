@@ -181,6 +181,16 @@ def test_attend_heads_with_a_cta_each(ig, B, Hkv, lo, hi, group, dt):
     check_attend(c, out, lse)
 
 
+@pytest.mark.parametrize("B,live", [(3000, {0: 5000, 1200: 4001, 2999: 3333}), (700, {699: 20000}), (129, {3: 900, 128: 7}),
+                                    (33, {32: 1})])
+def test_attend_few_requests_in_many_slots(ig, B, live):
+    """A batch of mostly empty slots: a CTA's share may go on hundreds of sequences further."""
+    c = make_attend(B, "f16", [live.get(b, 0) for b in range(B)], 2, 1, 64, 296)
+    out, lse = attend(ig, c)
+    ig.ig_check()
+    check_attend(c, out, lse)
+
+
 def test_attend_without_lse_and_with_a_negative_scale(ig):
     c = make_attend(3, "f16", [100, 33], 4, 4, 64, 16)
     c["scale"] = -0.3
