@@ -158,10 +158,12 @@ __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
 }
 
-// A wait that gives up together with the CTA's other waits.
+// The producer's wait for a free stage; gives up together with the CTA's other waits.  A consumer that gave
+// up frees stages whose copies it did not wait for, but sets `abort` first: the flag is read again after
+// the wait, so that no such stage is filled while its copies are still in flight.
 __device__ __forceinline__ bool pa_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
   for (uint32_t i = 0; i < limit && !*abort; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return !*abort;
   return false;
 }
 
@@ -367,6 +369,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     if (r1 > r0) w.start(sh.start_b, sh.start_off, r1 - r0);
   }
 
+  uint32_t sent = 0;  // the producer's tiles
   if (warp == kPaWarps) {
     // ---- producer.  The tiles of a head are taken in windows of 32 pages, a page number per lane;
     // the next window's numbers are loaded while this one's tiles go out.  Of a tile, lane i moves
@@ -443,9 +446,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
       first = first2;
       ids = ids2;
     }
-    __syncwarp();
-    if (*(volatile int*)&sh.abort)  // let the copies already issued land before the CTA leaves
-      for (uint32_t x = 0; x < NS && x < it; ++x) mbar_wait_bounded(&sh.full[x], ((it - 1 - x) / NS) & 1, 1u << 16);
+    sent = it;
   } else {
     // ---- consumers: warp = tg + TG * wq takes stages tg, tg + TG, ... for query rows wq
     const int tg = warp % TG, wq = warp / TG;
@@ -783,6 +784,10 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     }
   }
   __syncthreads();
+  // Where a wait ran out, copies may be in flight that no consumer waited for: they land before the CTA leaves,
+  // and its shared memory is another's.  Only here, where every consumer is done, is it known whether one gave up.
+  if (warp == kPaWarps && *(volatile int*)&sh.abort)
+    for (uint32_t x = 0; x < NS && x < sent; ++x) mbar_wait_bounded(&sh.full[x], ((sent - 1 - x) / NS) & 1);
 }
 
 // Joins the partials of the heads that were cut: block (x, y) takes unit x (or the head that CTA x
