@@ -10,6 +10,7 @@ place, so a captured ``write`` + ``attend`` replays with what ``extend`` put the
 from __future__ import annotations
 
 import math
+import operator
 
 import numpy as np
 import torch
@@ -44,23 +45,41 @@ class PagedCache:
             self.turns = torch.from_numpy(turns).to(self.dev)
         self.table_host = np.full((seqs, max_pages), -1, dtype=np.int32)
         self.L_host = np.zeros(seqs, dtype=np.int32)
+        self._moves, self._stale = [], False  # page moves still to run; whether the device is behind the manager
         self.table = torch.full((seqs, max_pages), -1, dtype=torch.int32, device=self.dev)
         self.L = torch.zeros(seqs, dtype=torch.int32, device=self.dev)
         self.ws = torch.empty(ig.ig_paged_attend_workspace_bytes(seqs, Hq, Hkv, d), dtype=torch.uint8, device=self.dev)
 
     # ------------------------------------------------------------------ the sequences
-    def _upload(self):
-        """The manager's tables and lengths, copied to the device (ordered on the current stream)."""
+    def _sync(self):
+        """The device brought up to the manager: the moves that are due, then its tables and lengths
+        (ordered on the current stream).  Where that fails, it stays due for the next call."""
+        self._stale = True
         ig.ig_pages_table(self.pages, self.table_host, self.L_host)
-        self.table.copy_(torch.from_numpy(self.table_host))
-        self.L.copy_(torch.from_numpy(self.L_host))
-
-    def _run_moves(self, moves):
-        if len(moves):
-            m = torch.from_numpy(np.ascontiguousarray(moves, dtype=np.int32)).to(self.dev)
+        if len(self._moves):
+            m = torch.from_numpy(np.ascontiguousarray(self._moves, dtype=np.int32)).to(self.dev)
             for l in range(0, self.layers, 128):
                 K, V = self.K[l:l + 128], self.V[l:l + 128]
-                ig.ig_page_copy(None, len(K), self.n_pages, self.Hkv, self.page, self.d, K, V, len(moves), m)
+                ig.ig_page_copy(None, len(K), self.n_pages, self.Hkv, self.page, self.d, K, V, len(self._moves), m)
+        self._moves = []
+        self.table.copy_(torch.from_numpy(self.table_host))
+        self.L.copy_(torch.from_numpy(self.L_host))
+        self._stale = False
+
+    def _catch_up(self):
+        if self._stale:
+            self._sync()
+
+    def _counts(self, new):
+        """``new`` as pairs of whole numbers, all of them checked."""
+        out = {}
+        for seq, n in new.items():
+            seq, n = operator.index(seq), operator.index(n)
+            if not 0 <= seq < self.seqs or n < 0 or seq in out:
+                raise ValueError(f"{n} tokens for sequence {seq}: the count must not be negative, the sequence one of "
+                                 f"{self.seqs} and named once")
+            out[seq] = min(n, self.max_pages * self.page + 1)  # one more than a table holds is refused below
+        return out.items()
 
     def _check(self, name, x, *shape, dtype=None):
         if x is not None and (x.numel() != math.prod(shape) or x.shape[0] != shape[0] or x.dtype != (dtype or self.dtype)):
@@ -68,52 +87,57 @@ class PagedCache:
 
     def extend(self, new):
         """Room for ``new[sequence]`` more tokens of each named sequence; returns device int32 slots
-        and positions of the tokens, in that order.  Raises IGError (IG_ERR_CAPACITY) with nothing
-        changed when the pages or a table run out."""
-        slots, positions, moves, before = [], [], [], {}
-        failed = None
-        for seq, n in new.items():
-            s = np.empty(n, dtype=np.int32)
-            had = int(self.L_host[seq])
-            try:
+        and positions of the tokens, in that order.  Raises ValueError or TypeError for a sequence or
+        count that cannot be, and IGError (IG_ERR_CAPACITY) when the pages or a table run out, with
+        every sequence as it was; only a page of its own that a sequence already got for the one it
+        shared (copied on write) stays with it."""
+        want = self._counts(new)
+        self._catch_up()
+        slots, positions, before = [], [], []
+        try:
+            for seq, n in want:
+                s = np.empty(n, dtype=np.int32)
+                had = int(self.L_host[seq])
                 move = ig.ig_pages_extend(self.pages, seq, n, s)
-            except ig.IGError as e:
-                failed = e
-                break
-            before[seq] = had
-            slots.append(s)
-            positions.append(np.arange(had, had + n, dtype=np.int32))
-            if move is not None:
-                moves.append(move)
-        if failed is not None:  # a page of its own that a sequence got stays with it, filled
-            for seq, had in before.items():
+                before.append((seq, had))
+                if move is not None:
+                    self._moves.append(move)
+                slots.append(s)
+                positions.append(np.arange(had, had + n, dtype=np.int32))
+            self._sync()
+            cat = lambda x: torch.from_numpy(np.concatenate(x) if x else np.empty(0, np.int32)).to(self.dev)  # noqa: E731
+            return cat(slots), cat(positions)
+        except BaseException:
+            for seq, had in before:
                 ig.ig_pages_truncate(self.pages, seq, had)
-        self._run_moves(moves)
-        self._upload()
-        if failed is not None:
-            raise failed
-        cat = lambda x: torch.from_numpy(np.concatenate(x) if x else np.empty(0, np.int32)).to(self.dev)  # noqa: E731
-        return cat(slots), cat(positions)
+            try:
+                self._sync()
+            except Exception:  # the first error is the one to name; what is due stays due
+                pass
+            raise
 
     def fork(self, src, dst):
         """Sequence ``dst`` (empty) becomes a copy of ``src``, sharing its pages."""
+        self._catch_up()
         ig.ig_pages_fork(self.pages, src, dst)
-        self._upload()
+        self._sync()
 
     def truncate(self, seq, n):
         """Keeps the first ``n`` tokens of a sequence."""
+        self._catch_up()
         ig.ig_pages_truncate(self.pages, seq, n)
-        self._upload()
+        self._sync()
 
     def free(self, seq):
         self.truncate(seq, 0)
 
     def compact(self):
         """Moves the used pages to the lowest numbers; returns how many moved."""
+        self._catch_up()
         moves = np.empty((self.n_pages // 2 + 1, 3), dtype=np.int32)
         n = ig.ig_pages_compact(self.pages, moves, len(moves))
-        self._run_moves(moves[:n])
-        self._upload()
+        self._moves = moves[:n]
+        self._sync()
         return n
 
     def free_pages(self):

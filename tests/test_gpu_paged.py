@@ -758,3 +758,43 @@ def test_cache_of_forked_requests(ig, dt, d, rot, layout, page):
         step({1: page, 2: 1, 0: 1, 3: 1})
     finally:
         cache.close()
+
+
+@pytest.mark.parametrize("bad", [{0: 1, 7: 1}, {0: 1, 2: -1}, {0: 1, 2: 1.5}, {0: 1, 2: 200}])
+def test_cache_attends_right_after_a_refused_extension(ig, bad):
+    """A sequence forked inside a page, whose extension is refused together with another's."""
+    from speculative_kv_cache_gb300.paged import PagedCache
+
+    cache = PagedCache(layers=1, Hq=4, Hkv=2, d=64, n_pages=20, seqs=3, max_pages=6, page=8)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    seen = [[], [], []]
+
+    def step(new):
+        slots, pos = cache.extend(new)
+        T = len(slots)
+        k, v = (torch.randn(T, 2, 64, generator=g, device=DEV).half() for _ in range(2))
+        cache.write(0, torch.zeros(T, 4, 64, dtype=torch.float16, device=DEV), k, v, slots, pos)
+        for i, s in enumerate(s for s, n in new.items() for _ in range(n)):
+            seen[s].append((k[i], v[i]))
+
+    try:
+        step({0: 13})
+        cache.fork(0, 1)
+        seen[1] = list(seen[0])
+        with pytest.raises((ValueError, TypeError, ig.IGError)):
+            cache.extend(bad)
+        assert cache.L.tolist() == [13, 13, 0]
+        step({0: 1, 1: 2})
+        q = torch.randn(3, 4, 64, generator=g, device=DEV).half()
+        lse = torch.empty(3, 4, device=DEV)
+        out = cache.attend(0, q, lse=lse)
+        ig.ig_check()
+        K, V = (torch.zeros(3, 2, 16, 64, dtype=torch.float16, device=DEV) for _ in range(2))
+        for s in range(3):
+            for t, (k, v) in enumerate(seen[s]):
+                K[s, :, t], V[s, :, t] = k, v
+        check_attend(dict(Hq=4, Hkv=2, d=64, page=16, q=q, K=K, V=V, table=i32([[0], [1], [2]]), scale=cache.scale,
+                          lengths=[len(x) for x in seen]), out, lse)
+    finally:
+        cache.close()

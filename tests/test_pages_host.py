@@ -258,3 +258,103 @@ def test_strided_rows_are_checked(ig):
     for bad, stride in [(x[:, 64:128], 64), (x.t(), 4), (x[:, ::2], 512), (x.view(4, 8, 64)[:, ::2], 512)]:
         with pytest.raises(ValueError):
             ig._rows(bad, stride)
+
+
+class HostCache:
+    """A PagedCache on CPU tensors, its page copies by a plain loop, and the tokens its rows should hold."""
+
+    def __init__(self, ig, monkeypatch, **k):
+        torch = pytest.importorskip("torch")
+        from speculative_kv_cache_gb300.paged import PagedCache
+
+        def page_copy(stream, layers, n_pages, Hkv, page, d, K, V, n, moves):
+            if self.fail:
+                raise RuntimeError("no memory")
+            for a, b, r in moves.tolist():
+                for x in K + V:
+                    x[b, :, :r] = x[a, :, :r].clone()
+
+        self.fail = False
+        monkeypatch.setattr(ig, "ig_page_copy", page_copy)
+        monkeypatch.setattr(torch.cuda, "set_device", lambda d: None)
+        a = dict(layers=2, Hq=2, Hkv=2, d=64, n_pages=12, seqs=4, max_pages=5, page=8, device="cpu")
+        a.update(k)
+        self.cache = PagedCache(**a)
+        for x in self.cache.K + self.cache.V:
+            x.fill_(-1)
+        self.want, self.next = [[] for _ in range(self.cache.seqs)], 1
+
+    def put(self, new):
+        slots, positions = self.cache.extend(new)
+        at = 0
+        for seq, n in new.items():
+            for _ in range(n):
+                s, c = int(slots[at]), self.cache
+                assert int(positions[at]) == len(self.want[seq])
+                for x in c.K + c.V:
+                    x[s // c.page, :, s % c.page] = self.next
+                self.want[seq].append(self.next)
+                self.next += 1
+                at += 1
+        assert at == len(slots) == len(positions)
+
+    def check(self):
+        """Device tables, manager and rows agree."""
+        c = self.cache
+        t, n = np.empty((c.seqs, c.max_pages), np.int32), np.empty(c.seqs, np.int32)
+        import speculative_kv_cache_gb300.ig as ig
+
+        ig.ig_pages_table(c.pages, t, n)
+        assert np.array_equal(c.table.numpy(), t) and np.array_equal(c.L.numpy(), n)
+        assert n.tolist() == [len(w) for w in self.want]
+        assert c.free_pages() == c.n_pages - len(set(t[t >= 0].tolist()))
+        for s, w in enumerate(self.want):
+            for x in c.K + c.V:
+                rows = [x[t[s, i // c.page], :, i % c.page] for i in range(len(w))]
+                assert all(bool((r == v).all()) for r, v in zip(rows, w)), (s, w)
+
+
+@pytest.mark.parametrize("bad", [{0: 1, 7: 1}, {0: 1, -1: 1}, {0: 1, 2: -1}, {0: 1, 2: 1.5}, {0: 1, 2: None}, {0: 1, "2": 1},
+                                 {0: 1, 1: 1, 2: 10 ** 12}, {0: 1, 2: 41}, {0: 1, 2: 40, 3: 40}])
+def test_cache_refuses_an_extension_and_keeps_every_sequence(ig, monkeypatch, bad):
+    h = HostCache(ig, monkeypatch)
+    h.put({0: 13})
+    h.cache.fork(0, 1)
+    h.want[1] = list(h.want[0])
+    h.check()
+    with pytest.raises((ValueError, TypeError, ig.IGError)) as e:
+        h.cache.extend(bad)
+    assert not isinstance(e.value, ig.IGError) or e.value.status == ig.IG_ERR_CAPACITY
+    h.check()
+    h.put({0: 1, 1: 4, 3: 9})
+    h.check()
+    h.cache.compact()
+    h.check()
+
+
+def test_cache_finishes_later_what_the_device_could_not_do(ig, monkeypatch):
+    """Page moves that fail leave the sequences as they were, and run before anything else changes."""
+    h = HostCache(ig, monkeypatch)
+    h.put({0: 13, 2: 20})
+    h.cache.fork(0, 1)
+    h.want[1] = list(h.want[0])
+    h.fail = True
+    with pytest.raises(RuntimeError, match="no memory"):
+        h.cache.extend({0: 2, 2: 1})
+    for change in [lambda: h.cache.extend({1: 1}), lambda: h.cache.fork(0, 3), lambda: h.cache.free(2), h.cache.compact]:
+        with pytest.raises(RuntimeError, match="no memory"):
+            change()
+    h.fail = False
+    h.cache.truncate(2, 3)
+    h.want[2] = h.want[2][:3]
+    h.check()
+    h.put({0: 1, 1: 1, 2: 9})
+    h.check()
+    h.cache.free(1)
+    h.want[1] = []
+    h.fail = True
+    with pytest.raises(RuntimeError, match="no memory"):
+        h.cache.compact()
+    h.fail = False
+    h.put({0: 1, 3: 2})
+    h.check()
