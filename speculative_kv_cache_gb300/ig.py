@@ -161,19 +161,29 @@ def _p(x):
     raise TypeError(f"unsupported buffer argument {type(x)}")
 
 
+_NO_GPU = -2  # no tensor's device
+
+
 def _here():
-    """The current GPU, where a call runs; None before torch uses one."""
-    return torch.cuda.current_device() if torch is not None and torch.cuda.is_initialized() else None
+    """The current GPU, where a call runs; before torch uses one, a number that no tensor's device has."""
+    return torch.cuda.current_device() if torch is not None and torch.cuda.is_initialized() else _NO_GPU
+
+
+def _elsewhere(x, here):
+    at = "the CPU" if x.get_device() < 0 else f"cuda:{x.get_device()}"
+    return ValueError(f"a tensor is on {at}, the call runs on {'a GPU' if here == _NO_GPU else f'cuda:{here}'}")
 
 
 def _q(x, here):
-    """As _p, and refuses a tensor of another GPU than ``here``."""
+    """Address of a device buffer: as _p, but refuses what is on the CPU or on another GPU than ``here``."""
     if torch is not None and isinstance(x, torch.Tensor):
         if not x.is_contiguous():
             raise ValueError("tensor arguments must be contiguous")
-        if here is not None and x.get_device() not in (here, -1):
-            raise ValueError(f"a tensor is on cuda:{x.get_device()}, the current device is cuda:{here}")
+        if here is not None and x.get_device() != here:
+            raise _elsewhere(x, here)
         return x.data_ptr()
+    if isinstance(x, np.ndarray):
+        raise ValueError("an array is on the CPU, the call takes device buffers")
     return _p(x)
 
 
@@ -181,7 +191,7 @@ def _qs(items, here):
     """_q of every item of a list, in a few passes where they are plain tensors (64 of them: 21 -> 12 us)."""
     if torch is not None and set(map(type, items)) == {torch.Tensor}:
         T = torch.Tensor
-        if all(map(T.is_contiguous, items)) and (here is None or {here, -1}.issuperset(map(T.get_device, items))):
+        if all(map(T.is_contiguous, items)) and {here} == set(map(T.get_device, items)):
             return map(T.data_ptr, items)
     return [_q(x, here) for x in items]
 
@@ -198,8 +208,8 @@ def _rows(x, stride, here=None):
         dense *= shape[i]
     if not ok:
         raise ValueError(f"tensor rows must be dense and {stride} elements apart")
-    if here is not None and x.get_device() not in (here, -1):
-        raise ValueError(f"a tensor is on cuda:{x.get_device()}, the current device is cuda:{here}")
+    if here is not None and x.get_device() != here:
+        raise _elsewhere(x, here)
     return x.data_ptr()
 
 

@@ -358,3 +358,23 @@ def test_cache_finishes_later_what_the_device_could_not_do(ig, monkeypatch):
     h.fail = False
     h.put({0: 1, 3: 2})
     h.check()
+
+
+def test_buffers_on_the_cpu_are_refused(ig):
+    """Where a call takes device buffers, a host tensor or array in any place is refused by the binding."""
+    torch = pytest.importorskip("torch")
+    host = torch.zeros(4096, dtype=torch.int64)
+    n = ig.ig_launch_count()
+    for bad in (host, host.numpy()):
+        for name in ("q", "K", "V", "page_table", "L_valid", "out", "lse", "workspace"):
+            with pytest.raises(ValueError, match="CPU"):
+                _attend(ig, **{name: bad})
+        for name in ("q", "k", "v", "q_weight", "k_weight", "positions", "turns", "q_out", "slot", "k_out", "v_out"):
+            with pytest.raises(ValueError, match="CPU"):
+                _rope(ig, **{name: bad})
+        for K, V, moves in [([bad], [1 << 20], 4), ([1 << 20], [bad], 4), ([1 << 20], [1 << 20], bad), ([bad], [bad], 4)]:
+            with pytest.raises(ValueError, match="CPU"):
+                ig.ig_page_copy(0, 1, 4, 2, 16, 64, K, V, 1, moves)
+    with pytest.raises(ValueError, match="CPU"):
+        _rope(ig, q=host.view(64, 64)[:, :32], q_stride=64)
+    assert ig.ig_launch_count() == n
