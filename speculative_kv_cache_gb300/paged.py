@@ -4,11 +4,14 @@ It owns the pages of every layer, the host-side page manager (``ig_pages_*``) an
 of its tables, and runs a token's way through a layer: ``write`` (norm and rotation of q and k, the
 rows into their pages: ``ig_qk_norm_rope``) and ``attend`` (``ig_paged_attend``).  Sequences can be
 forked (pages shared until one writes), cut back, freed, and the pages packed (``ig_page_copy``).
-All device work is queued on torch's current stream.  The device tensors ``table`` and ``L`` stay in
-place, so a captured ``write`` + ``attend`` replays with what ``extend`` put there since.
+All device work is queued on the current stream of the cache's GPU, whichever GPU is the current one.  The
+device tensors ``table`` and ``L`` stay in place, so a captured ``write`` + ``attend`` replays with what
+``extend`` put there since.  A cache's calls share its tables and one workspace, so they run one after
+another: on one stream, or on streams that wait for each other.
 """
 from __future__ import annotations
 
+import functools
 import math
 import operator
 
@@ -18,6 +21,17 @@ import torch
 from . import ig
 
 _DTYPES = {torch.float16: ig.IG_F16, torch.bfloat16: ig.IG_BF16}
+
+
+def _on_its_gpu(method):
+    @functools.wraps(method)
+    def call(self, *args, **kwargs):
+        if torch.cuda.current_device() == self.dev.index:
+            return method(self, *args, **kwargs)
+        with torch.cuda.device(self.dev):
+            return method(self, *args, **kwargs)
+
+    return call
 
 
 class PagedCache:
@@ -85,6 +99,7 @@ class PagedCache:
         if x is not None and (x.numel() != math.prod(shape) or x.shape[0] != shape[0] or x.dtype != (dtype or self.dtype)):
             raise ValueError(f"{name} must be {list(shape)} of {dtype or self.dtype}, got {list(x.shape)} of {x.dtype}")
 
+    @_on_its_gpu
     def extend(self, new):
         """Room for ``new[sequence]`` more tokens of each named sequence; returns device int32 slots
         and positions of the tokens, in that order.  Raises ValueError or TypeError for a sequence or
@@ -116,12 +131,14 @@ class PagedCache:
                 pass
             raise
 
+    @_on_its_gpu
     def fork(self, src, dst):
         """Sequence ``dst`` (empty) becomes a copy of ``src``, sharing its pages."""
         self._catch_up()
         ig.ig_pages_fork(self.pages, src, dst)
         self._sync()
 
+    @_on_its_gpu
     def truncate(self, seq, n):
         """Keeps the first ``n`` tokens of a sequence."""
         self._catch_up()
@@ -131,6 +148,7 @@ class PagedCache:
     def free(self, seq):
         self.truncate(seq, 0)
 
+    @_on_its_gpu
     def compact(self):
         """Moves the used pages to the lowest numbers; returns how many moved."""
         self._catch_up()
@@ -144,6 +162,7 @@ class PagedCache:
         return ig.ig_pages_free_count(self.pages)
 
     # ------------------------------------------------------------------ a layer's step
+    @_on_its_gpu
     def write(self, layer, q, k, v, slots, positions, q_weight=None, k_weight=None, q_out=None):
         """Norms and rotates the tokens' q [T, Hq, d] and k [T, Hkv, d] and puts k and v [T, Hkv, d]
         into ``layer``'s pages; returns the new q.  q, k and v may be slices of one projection
@@ -166,6 +185,7 @@ class PagedCache:
                            self.n_pages, slots, self.K[layer], self.V[layer])
         return q_out
 
+    @_on_its_gpu
     def attend(self, layer, q, out=None, lse=None):
         """Attention of one token per sequence, q [seqs, Hq, d], over all its tokens: fp32
         [seqs, Hq, d], zero for empty sequences."""

@@ -277,6 +277,7 @@ class HostCache:
         self.fail = False
         monkeypatch.setattr(ig, "ig_page_copy", page_copy)
         monkeypatch.setattr(torch.cuda, "set_device", lambda d: None)
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: None)  # a CPU device's index
         a = dict(layers=2, Hq=2, Hkv=2, d=64, n_pages=12, seqs=4, max_pages=5, page=8, device="cpu")
         a.update(k)
         self.cache = PagedCache(**a)
@@ -378,3 +379,41 @@ def test_buffers_on_the_cpu_are_refused(ig):
     with pytest.raises(ValueError, match="CPU"):
         _rope(ig, q=host.view(64, 64)[:, :32], q_stride=64)
     assert ig.ig_launch_count() == n
+
+
+def test_cache_works_on_its_own_gpu(ig, monkeypatch):
+    """With another GPU as the current one (a stand-in), every call that does device work switches to the
+    cache's, and back."""
+    torch = pytest.importorskip("torch")
+    h = HostCache(ig, monkeypatch)
+    current, at = [1], []
+
+    class On:
+        def __init__(self, d):
+            self.to = d.index
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.to
+
+        def __exit__(self, *e):
+            current[0] = self.was
+
+    copies = ig.ig_page_copy
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", On)
+    monkeypatch.setattr(ig, "ig_page_copy", lambda *a: (at.append(current[0]), copies(*a)))
+    monkeypatch.setattr(ig, "ig_pages_table", lambda *a, f=ig.ig_pages_table: (at.append(current[0]), f(*a)))
+    monkeypatch.setattr(ig, "ig_qk_norm_rope", lambda *a: at.append(current[0]))
+    monkeypatch.setattr(ig, "ig_paged_attend", lambda *a: at.append(current[0]))
+    c, z = h.cache, lambda *s: torch.zeros(*s, dtype=torch.float16)  # noqa: E731
+    h.put({0: 13})
+    c.fork(0, 1)
+    h.want[1] = list(h.want[0])
+    h.put({0: 1})
+    c.write(0, z(2, 2, 64), z(2, 2, 64), z(2, 2, 64), *[torch.zeros(2, dtype=torch.int32)] * 2)
+    c.attend(0, z(4, 2, 64))
+    c.free(1)
+    h.want[1] = []
+    c.compact()
+    assert len(at) >= 9 and set(at) == {None} and current == [1]
+    h.check()
