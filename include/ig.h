@@ -467,7 +467,8 @@ ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int Hkv, int d
  *   context   the trained context length (YARN and BANDS; else ignored, as p0 and p1)
  *   turns     host uint64 [rot / 2] out;  rot_scale host fp32 out: the factor on the rotated part
  *             (1 but for YARN)
- * rot: a positive multiple of 2; theta > 0; factor >= 1 (ignored by PLAIN). */
+ * rot: a positive multiple of 2; theta > 0; factor >= 1 (ignored by PLAIN); the base and frequencies within
+ * a double's range. */
 #define IG_ROPE_PLAIN 0
 #define IG_ROPE_LINEAR 1
 #define IG_ROPE_BASE 2

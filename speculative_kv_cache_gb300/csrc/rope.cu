@@ -258,6 +258,8 @@ extern "C" ig_status ig_rope_turns(int rot, double theta, int scaling, double fa
   const double two_pi = 6.283185307179586476925286766559;
   double lo = 0.0, hi = 0.0;
   if (scaling == IG_ROPE_BASE) theta *= pow(factor, (double)rot / (rot - 2));
+  // (frequencies grow or shrink with j, so the first and last bound them)
+  IG_REQUIRE(isfinite(theta) && isfinite(pow(theta, -2.0 * (rot / 2 - 1) / rot)), "a frequency or the base overflows");
   if (scaling == IG_ROPE_YARN) {
     auto at = [&](double n) { return rot * log(context / (two_pi * n)) / (2.0 * log(theta)); };
     lo = fmax(floor(at(p0)), 0.0);

@@ -417,3 +417,13 @@ def test_cache_works_on_its_own_gpu(ig, monkeypatch):
     c.compact()
     assert len(at) >= 9 and set(at) == {None} and current == [1]
     h.check()
+
+
+@pytest.mark.parametrize("args", [(64, 5e-324, 0, 1.0, 0, 0.0, 0.0), (64, 1e-320, 1, 4.0, 0, 0.0, 0.0),
+                                  (4, 1e300, 2, 1e200, 0, 0.0, 0.0)])
+def test_rope_turns_refuse_what_overflows(ig, args):
+    turns = np.zeros(args[0] // 2, dtype=np.uint64)
+    with pytest.raises(ig.IGError) as e:
+        ig.ig_rope_turns(*args, turns)
+    assert e.value.status == ig.IG_ERR_INVALID and not turns.any()
+    ig.ig_rope_turns(64, 1e-300, 0, 1.0, 0, 0.0, 0.0, np.zeros(32, dtype=np.uint64))
