@@ -428,9 +428,10 @@ ig_status ig_append_kv(void* stream, ig_pool* pool, int layer, int B, int H, int
  *   z_t = scale * q . K_t,  o = sum_t w_t V_t,  w = softmax_t(z),  t < L_valid[b]
  *   lse = log(sum_t exp(z_t))        (natural logarithm; joins results over parts of a cache)
  * in one pass over K and V, products in fp16/bf16 with fp32 sums, softmax in fp32, the weights
- * in at least 22 bits.  L_valid[b] = 0 (or every z_t = -inf) gives o = 0 and lse = -inf.  What
- * the pages hold past a sequence's last token may be anything, NaN included; a NaN or infinity
- * in a row that is attended gives non-finite results for its heads.
+ * in at least 20 bits down to 2^-100 of the sequence's largest (smaller ones may count as zero).
+ * L_valid[b] = 0 (or every z_t = -inf) gives o = 0 and lse = -inf.  What the pages hold past a
+ * sequence's last token may be anything, NaN included; a NaN or infinity in a row that is attended
+ * gives non-finite results for its heads.
  *   q           dev [B][Hq][d] of `dtype`, 16-byte aligned
  *   page_table  dev int32 [B][max_pages]; entries past a sequence's last page are not used.  A
  *               page number outside [0, n_pages) sets IG_DEVERR_INDEX and its tokens are left out

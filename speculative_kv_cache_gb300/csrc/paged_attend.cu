@@ -16,8 +16,13 @@
 // in very long caches (34 against 40 us at 4 x 32768, G = 64), which the host cannot see coming.
 //
 // Precision.  K, V, q enter as they are.  A weight in fp16 or bf16 alone would cost 2^-11 or 2^-8, so
-// it is split into 16-bit parts that are multiplied in turn: two for fp16 (scaled by 2^15 so that
-// the second part of a small weight stays normal; 22 bits), three for bf16 (24 bits).  Sums over the
+// it is split into 16-bit parts that are multiplied in turn: two for fp16 (20 bits or more), three for bf16 (24 bits).
+// fp16 has few exponents: scaled by 2^15, two parts hold weights from 1 down to 2^-19.  Smaller ones must keep their
+// bits too, as a large weight's value may be zero (a sink).  So the reference that weights are taken against need
+// not be the largest logit: it follows a tile down, by a power of two, which fp32 sums stand (kPaHigh) and
+// the next tiles then have for nothing; and the few weights of a tile that spans more go token by token
+// in fp32.  Nothing else changes for tiles within the parts: 16 x 4050 tokens, 56 heads 23.1 -> 22.9 us, 64 x 2048
+// tokens, 20 heads 27.0 -> 28.4 us, 33 heads of 64 15.1 -> 16.3 us (registers).  Sums over the
 // tokens of one tile run in the tensor cores, whose adds need not round to nearest; those over tiles in
 // fp32 adds that do, so that long sequences collect no bias.  (2-norm error against 64 bits 3e-7 to 6e-7,
 // plain fp32 torch operations 2e-7 to 1.2e-6.)
@@ -64,6 +69,11 @@ constexpr int kPaSolo = 4;
 // them to keep HBM busy (one per SM) and the longest is at most kPaEven tiles above the mean.
 constexpr int kPaWhole = 6;
 constexpr int kPaEven = 3;
+// Powers of two of fp16 weights that two 16-bit parts cover: 22 bits of the upper 17, 20 of all.  (17 in all, so that
+// more tiles leave them: 16.3 -> 18.9 us for 16 x 4050 tokens, 33 heads of 64 on one key head.)
+constexpr int kPaBand = 19;
+constexpr float kPaLeast = -126.f;                // weights below 2^kPaLeast of the reference are zero, as ex2 has them
+constexpr int kPaHigh = 95;                       // weights and their sums, times 2^15, stay near or below 2^kPaHigh
 constexpr int kPaPartHead = 4;                    // a partial: [max, sum, -, -, output[D]]
 
 template <int D>
@@ -136,6 +146,14 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+__device__ __forceinline__ float lds_half(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return __half2float(__ushort_as_half(v));
+}
+
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
 
 // Two fp32 as a pair of 16-bit values (x in the low half), and what the rounding left of them.
 template <bool BF>
@@ -567,23 +585,46 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
               for (int j = 0; j < NQ; ++j) z[i][j][e] = in ? z[i][j][e] : -INFINITY;
             }
         }
-        // the running maximum; most tiles of a long sequence leave it as it is
-        float tm[NQ][2];
-        bool more = false;
+        // The running maximum; most tiles of a long sequence leave it as it is.  For fp16 it is a reference, that
+        // follows the tiles down too where their weights would fall below what the parts hold.
+        float tm[NQ][2], ym[NQ][2];
+        bool look = false;
 #pragma unroll
         for (int j = 0; j < NQ; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float x2 = fmaxf(z[0][j][e], z[0][j][e + 2]);
+            float x2 = fmaxf(z[0][j][e], z[0][j][e + 2]), y2 = fminf(z[0][j][e], z[0][j][e + 2]);
 #pragma unroll
-            for (int i = 1; i < MT; ++i) x2 = fmaxf(x2, fmaxf(z[i][j][e], z[i][j][e + 2]));
+            for (int i = 1; i < MT; ++i) {
+              x2 = fmaxf(x2, fmaxf(z[i][j][e], z[i][j][e + 2]));
+              y2 = fminf(y2, fminf(z[i][j][e], z[i][j][e + 2]));
+            }
             tm[j][e] = x2;
-            more |= x2 > m[j][e];
+            ym[j][e] = y2;
+            look |= x2 > m[j][e];
           }
+        if constexpr (!BF) {
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (!whole) {  // (of the tokens that count)
+                float y2 = INFINITY;
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                  const float v = z[i / 2][j][i % 2 * 2 + e];
+                  y2 = fminf(y2, v > -INFINITY ? v : INFINITY);
+                }
+                ym[j][e] = y2;
+              }
+              look |= ym[j][e] < m[j][e] - kPaBand;
+            }
+        }
         float corr[NQ][2];
 #pragma unroll
         for (int j = 0; j < NQ; ++j) corr[j][0] = corr[j][1] = 1.f;
-        if (__any_sync(0xffffffffu, more)) {
+        if (__any_sync(0xffffffffu, look)) {
+          bool low = false;
 #pragma unroll
           for (int j = 0; j < NQ; ++j)
 #pragma unroll
@@ -595,7 +636,123 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
               corr[j][e] = mn == -INFINITY ? 1.f : ex2(m[j][e] - mn);
               m[j][e] = mn;
               l[j][e] *= corr[j][e];
+              if constexpr (!BF) {
+                tm[j][e] = x2;
+                low |= ym[j][e] < mn - kPaBand;
+              }
             }
+          if constexpr (!BF) {
+            if (__any_sync(0xffffffffu, low)) {
+              bool far = false;
+#pragma unroll
+              for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float y2 = INFINITY, sum = l[j][e];  // the least logit whose weight is not zero
+#pragma unroll
+                  for (int i = 0; i < 2 * MT; ++i) {
+                    const float v = z[i / 2][j][i % 2 * 2 + e];
+                    y2 = fminf(y2, v - m[j][e] > kPaLeast ? v : INFINITY);
+                  }
+#pragma unroll
+                  for (int sh2 = 4; sh2 < 32; sh2 <<= 1) {
+                    y2 = fminf(y2, __shfl_xor_sync(0xffffffffu, y2, sh2));
+                    sum += __shfl_xor_sync(0xffffffffu, sum, sh2);
+                  }
+                  // The reference goes down by a power of two.  Where the column's logits fit the parts, they come to lie
+                  // in the middle; else it goes next to the largest, or, where more of them are in the lower half (a
+                  // sink's tile), so far that the least fits.
+                  const float span = tm[j][e] - y2, half = 0.5f * (tm[j][e] + y2);
+                  int upper = 0;
+#pragma unroll
+                  for (int i = 0; i < 2 * MT; ++i) {
+                    const float v = z[i / 2][j][i % 2 * 2 + e];
+                    upper += v > half ? 1 : v >= y2 ? -1 : 0;
+                  }
+#pragma unroll
+                  for (int sh2 = 4; sh2 < 32; sh2 <<= 1) upper += __shfl_xor_sync(0xffffffffu, upper, sh2);
+                  if (y2 < m[j][e] - kPaBand) {
+                    const float to = span < kPaBand - 1 ? fminf(half + 0.5f * kPaBand, y2 + (kPaBand - 1))
+                                     : upper >= 0       ? tm[j][e]
+                                                        : y2 + (kPaBand - 1);
+                    const float room = (float)(kPaHigh + min(-16, 127 - (__float_as_int(sum) >> 23)));
+                    const float down = fminf(floorf(m[j][e] - to), room);
+                    if (down > 0.f) {
+                      const float up = power_of_two((int)down);
+                      m[j][e] -= down;
+                      l[j][e] *= up;
+                      corr[j][e] *= up;
+                    }
+                    far |= y2 < m[j][e] - kPaBand || tm[j][e] > m[j][e];
+                  }
+                }
+              if (__any_sync(0xffffffffu, far)) {
+                // weights that stay outside the parts: token by token, in fp32, and then as zeros
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][j][e] *= corr[j][e & 1];
+#pragma unroll
+                for (int j = 0; j < NQ; ++j) corr[j][0] = corr[j][1] = 1.f;
+                auto outside = [&](float v, float r) { return (v < r - kPaBand || v > r) && v - r > kPaLeast; };
+                unsigned groups = 0;  // of eight tokens
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i)
+#pragma unroll
+                  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) groups |= outside(z[i / 2][j][i % 2 * 2 + e], m[j][e]) ? 1u << i : 0u;
+                for (groups = __reduce_or_sync(0xffffffffu, groups); groups; groups &= groups - 1) {
+                  const int r8 = __ffs(groups) - 1;
+                  float wt[NQ][2];
+                  bool some = false;
+#pragma unroll
+                  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                      float v = z[0][j][e];
+#pragma unroll
+                      for (int i = 1; i < 2 * MT; ++i) v = i == r8 ? z[i / 2][j][i % 2 * 2 + e] : v;
+                      const bool it_is = outside(v, m[j][e]);
+                      wt[j][e] = it_is ? ex2(v - m[j][e]) * 32768.f : 0.f;
+                      l[j][e] += wt[j][e];
+                      some |= it_is;
+                    }
+                  for (unsigned left = __ballot_sync(0xffffffffu, some); left;) {
+                    const int g = (__ffs(left) - 1) >> 2, r = r8 * 8 + g;
+                    left &= ~(15u << (4 * g));
+                    float wg[NQ][2];
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                      for (int e = 0; e < 2; ++e) wg[j][e] = __shfl_sync(0xffffffffu, wt[j][e], 4 * g + tl);
+                    const uint32_t row = vb + r / s.box * (s.box * D * 2) + r % s.box * 128 + gl * 2;
+#pragma unroll
+                    for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+                      for (int hh = 0; hh < 2; ++hh) {
+                        const float v = lds_half(row + (dt / 4) * half_bytes + ((((dt % 4) * 2 + hh) ^ g) << 4));
+#pragma unroll
+                        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                          for (int e = 0; e < 2; ++e) o[dt][j][2 * hh + e] = fmaf(wg[j][e], v, o[dt][j][2 * hh + e]);
+                      }
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const float v = z[i][j][e], r = m[j][e & 1];
+                      z[i][j][e] = v < r - kPaBand || (v > r && r > -INFINITY) ? -INFINITY : v;
+                    }
+              }
+            }
+          }
         }
         // the weights, as 16-bit parts in the layout of the second product's operand
         uint32_t p[PARTS][MT][NQ][2];
@@ -673,6 +830,27 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int sh2 = 4; sh2 < 32; sh2 <<= 1) l[j][e] += __shfl_xor_sync(0xffffffffu, l[j][e], sh2);
+      // A reference that followed the tiles down goes back to about the largest logit, so that other warps' and CTAs'
+      // are not so far above it that the factor between them is zero.  (2^20: more than a sum of weights
+      // of at most 1 usually is.)
+      if constexpr (!BF) {
+#pragma unroll
+        for (int j = 0; j < NQ; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int up = (__float_as_int(l[j][e]) >> 23) - 127 - 15;
+            if (up > 20 && up < kPaHigh) {
+              const float f = power_of_two(-up);
+              m[j][e] += (float)up;
+              l[j][e] *= f;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[i][j][e] *= f;
+                o[i][j][e + 2] *= f;
+              }
+            }
+          }
+      }
       if (TG > 1 && !solo) {
         if (gl == 0)
 #pragma unroll

@@ -220,6 +220,55 @@ def test_attend_large_logits_and_wide_weights(ig, dt):
     check_attend(c, out, lse)
 
 
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("group", [1, 4, 12, 20, 40])
+@pytest.mark.parametrize("gap", [9, 12, 16, 20, 25, 30, 60, 80])
+def test_attend_small_weights_beside_a_large_one_without_a_value(ig, dt, d, group, gap):
+    """One token of each sequence lies `gap` above the others and has a value of zero, so that the output
+    is the small weights'; in the second half of the sequences the others fall off by up to `gap` more
+    (up to 80 in all, which keeps every weight above 2^-126 of the largest)."""
+    lengths = [40, 333, 700, 40, 150, 700]
+    c = make_attend(gap + group + d, dt, lengths, 2 * group, 2, d, 16)
+    c["q"] *= 0.5
+    c["q"][..., 0] = 8.0
+    unit = math.sqrt(d) / 8.0  # of key component 0 per unit of logit
+    for b, n in enumerate(lengths):
+        t = torch.arange(n, device=DEV)
+        p, r = c["table"][b, t // 16].long(), t % 16
+        fall = unit * min(gap, 80 - gap) * (t * 7 % 32) / 32 * (b >= 3)
+        c["K"][p, :, r, 0] = -fall[:, None].expand(n, 2).to(DT[dt])
+        sink = [0, n - 1, n // 2][b % 3]
+        p, r = p[sink], r[sink]
+        c["K"][p, :, r] = 0
+        c["K"][p, :, r, 0] = unit * gap
+        c["V"][p, :, r] = 0
+    out, lse = attend(ig, c)
+    ig.ig_check()
+    check_attend(c, out, lse)
+    assert torch.all(out.abs().amax(-1) > 0)
+
+
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("f16", 128), ("bf16", 128)])
+@pytest.mark.parametrize("group,lengths", [(4, [3000]), (12, [700, 3000, 65]), (20, [3000, 300]), (40, [1000])])
+@pytest.mark.parametrize("gap,period", [(15, 40), (15, 600), (40, 96), (75, 50), (75, 1000)])
+def test_attend_logits_that_rise_and_fall(ig, dt, d, group, lengths, gap, period):
+    """Logits between 0 and -gap, up and down within a tile or over many, parts of a sequence in several
+    CTAs; the upper half's values are zero, so that the lower half's weights make the output."""
+    c = make_attend(gap + period + group, dt, lengths, group, 1, d, 8)
+    c["q"] *= 0.25
+    c["q"][..., 0] = 8.0
+    for b, n in enumerate(lengths):
+        t = torch.arange(n, device=DEV)
+        p, r = c["table"][b, t // 8].long(), t % 8
+        fall = gap * ((t + 17 * b) % period - period / 2).abs() / (period / 2)
+        c["K"][p, 0, r, 0] = (-fall * math.sqrt(d) / 8.0).to(DT[dt])
+        c["V"][p[fall < gap / 2], 0, r[fall < gap / 2]] = 0
+    out, lse = attend(ig, c)
+    ig.ig_check()
+    check_attend(c, out, lse)
+    assert torch.all(out.abs().amax(-1) > 0)
+
+
 def test_attend_logits_of_minus_infinity(ig):
     # every key of sequence 0, and all but one of sequence 1, gives -inf
     c = make_attend(6, "f16", [40, 40], 2, 1, 64, 8)
