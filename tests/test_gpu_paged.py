@@ -847,3 +847,69 @@ def test_cache_attends_right_after_a_refused_extension(ig, bad):
                           lengths=[len(x) for x in seen]), out, lse)
     finally:
         cache.close()
+
+
+def test_rotation_keeps_a_nan_key_in_its_row(ig):
+    c = make_rope(ig, 7, "f16", 6, 4, 3, 64, 64, 0, True, 8)
+    clean = [c["q"].clone(), c["k"].clone(), c["v"].clone()]
+    c["k"][2, 1, 5] = float("nan")
+    c["k"][4, 0, 9] = float("inf")
+    rope(ig, c)
+    ig.ig_check()
+    y, tol = rope64(c, clean[0], c["wq"])
+    assert torch.all((c["qo"].double() - y).abs() <= tol)
+    y, tol = rope64(c, clean[1], c["wk"])
+    at, row = c["slot"].long() // 8, c["slot"].long() % 8
+    K, V = c["ko"][at, :, row], c["vo"][at, :, row]
+    ok = torch.ones(6, 3, dtype=torch.bool, device=DEV)
+    ok[2, 1] = ok[4, 0] = False
+    assert torch.all((K.double() - y).abs()[ok] <= tol[ok])
+    assert torch.all(torch.isnan(K[2, 1])) and not torch.any(torch.isfinite(K[4, 0, 9:10]))
+    assert torch.equal(V, clean[2])
+    rest = torch.ones(c["n"], 8, dtype=torch.bool, device=DEV)
+    rest[at, row] = False
+    assert torch.all(c["ko"].transpose(1, 2)[rest] == 7.0) and torch.all(c["vo"].transpose(1, 2)[rest] == 7.0)
+
+
+@pytest.mark.parametrize("scaling,factor,context,p0,p1", [(1, 4.0, 0, 0.0, 0.0), (2, 8.0, 0, 0.0, 0.0),
+                                                          (3, 16.0, 4096, 32.0, 1.0), (4, 8.0, 8192, 1.0, 4.0)])
+def test_rotation_by_scaled_frequencies(ig, scaling, factor, context, p0, p1):
+    """What ig_rope_turns gives for each rule, through the kernel, against the rule's frequencies in doubles."""
+    from test_pages_host import _frequencies
+
+    c = make_rope(ig, 8, "f16", 50, 4, 2, 128, 128, 0, False, 0, top=60000)
+    turns = np.zeros(64, dtype=np.int64)
+    s = ig.ig_rope_turns(128, 10000.0, scaling, factor, context, p0, p1, turns)
+    c.update(turns=torch.from_numpy(turns).to(DEV), rscale=s)
+    rope(ig, c)
+    ig.ig_check()
+    f = torch.tensor(_frequencies(128, 10000.0, scaling, factor, context, p0, p1), dtype=torch.float64, device=DEV)
+    a = (c["pos"].double()[:, None] * f)[:, None]
+    for x, got in ((c["q"].double(), c["qo"]), (c["k"].double(), c["ko"])):
+        x0, x1 = x[..., :64], x[..., 64:]
+        y = s * torch.cat([x0 * a.cos() - x1 * a.sin(), x0 * a.sin() + x1 * a.cos()], -1)
+        size = (s * (x0.abs() + x1.abs())).repeat(1, 1, 2)
+        # as rope64's, and the reference's angle: up to 60000 radians in doubles, 2^-36
+        tol = torch.clamp(STEP["f16"] * y.abs(), min=2.0 ** -25) * (1 + 2.0 ** -8) + size * (2.0 ** -21 + 144 * U + 2.0 ** -36)
+        assert torch.all((got.double() - y).abs() <= tol), float(((got.double() - y).abs() / tol).max())
+
+
+def test_cache_keeps_its_free_pages_when_an_extension_does_not_fit(ig):
+    from speculative_kv_cache_gb300.paged import PagedCache
+
+    cache = PagedCache(layers=1, Hq=2, Hkv=2, d=64, n_pages=6, seqs=3, max_pages=6, page=8)
+    try:
+        cache.extend({0: 12, 1: 8})
+        for bad in ({0: 1, 2: 25}, {1: 9, 2: 17}, {2: 49}):
+            with pytest.raises(ig.IGError) as e:
+                cache.extend(bad)
+            assert e.value.status == ig.IG_ERR_CAPACITY
+            assert cache.free_pages() == 3 and cache.L.tolist() == [12, 8, 0]
+        cache.fork(0, 2)
+        with pytest.raises(ig.IGError):  # a page of its own stays with the sequence that parted
+            cache.extend({2: 1, 1: 25})
+        assert cache.free_pages() == 2 and cache.L.tolist() == [12, 8, 12]
+        t = cache.table.tolist()
+        assert t[0][0] == t[2][0] and t[0][1] != t[2][1]
+    finally:
+        cache.close()
