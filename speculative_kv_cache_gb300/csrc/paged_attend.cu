@@ -155,6 +155,13 @@ __device__ __forceinline__ float lds_half(uint32_t addr) {
 
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
 
+// m += by, and the factor 2^(m before - m after) that keeps sums right: what the addition rounds off (Knuth's two-sum) is in it.
+__device__ __forceinline__ float pa_move(float& m, int by) {
+  const float b = (float)by, s = m + b, c = s - m, lost = (m - (s - c)) + (b - c);
+  m = s;
+  return power_of_two(-by) * fmaf(lost, 0.6931471805599453f, 1.f);
+}
+
 // Two fp32 as a pair of 16-bit values (x in the low half), and what the rounding left of them.
 template <bool BF>
 __device__ __forceinline__ uint32_t split2(float& x, float& y) {
@@ -677,9 +684,8 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
                                                         : y2 + (kPaBand - 1);
                     const float room = (float)(kPaHigh + min(-16, 127 - (__float_as_int(sum) >> 23)));
                     const float down = fminf(floorf(m[j][e] - to), room);
-                    if (down > 0.f) {
-                      const float up = power_of_two((int)down);
-                      m[j][e] -= down;
+                    if (down > 0.f && fabsf(m[j][e]) < 0x1p22f) {  // (where a float still tells one power from the next)
+                      const float up = pa_move(m[j][e], -(int)down);
                       l[j][e] *= up;
                       corr[j][e] *= up;
                     }
@@ -840,8 +846,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
           for (int e = 0; e < 2; ++e) {
             const int up = (__float_as_int(l[j][e]) >> 23) - 127 - 15;
             if (up > 20 && up < kPaHigh) {
-              const float f = power_of_two(-up);
-              m[j][e] += (float)up;
+              const float f = pa_move(m[j][e], up);
               l[j][e] *= f;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
