@@ -66,9 +66,10 @@ int ig_version(void);
 ig_status ig_check(void* stream);
 
 /* Iteration limit of the score kernels' bounded waits for their staged copies (k2_scores,
- * k23_score_select), and of the paged attention's (k_paged_attend), on the current device: a wait that runs out records IG_DEVERR_TIMEOUT,
- * the CTA then waits (with the fixed default limit) for its copies in flight to land and
- * leaves without scoring, and the next ig_check returns IG_ERR_TIMEOUT.  max_iters < 0
+ * k23_score_select), and of the paged attention's (k_paged_attend), on the current device: a wait
+ * that runs out records IG_DEVERR_TIMEOUT, the CTA then waits (with the fixed default limit) for its
+ * copies in flight to land and leaves without scoring (the attention's output is then undefined),
+ * and the next ig_check returns IG_ERR_TIMEOUT.  max_iters < 0
  * restores the default (2^22 probes, far more than a copy needs); 0 makes the first wait give
  * up at once, which is how tests exercise the timeout path without faulting anything.
  * Synchronous (a 4-byte copy to the device); not for use during stream capture.  No
@@ -430,8 +431,9 @@ ig_status ig_append_kv(void* stream, ig_pool* pool, int layer, int B, int H, int
  * in one pass over K and V, products in fp16/bf16 with fp32 sums, softmax in fp32, the weights
  * in at least 20 bits down to 2^-100 of the sequence's largest (smaller ones may count as zero).
  * L_valid[b] = 0 (or every z_t = -inf) gives o = 0 and lse = -inf.  What the pages hold past a
- * sequence's last token may be anything, NaN included; a NaN or infinity in a row that is attended
- * gives non-finite results for its heads.
+ * sequence's last token may be anything, NaN included.  In rows that are attended, a logit of -inf
+ * has weight zero; a logit that is NaN or +inf, or a value that is not finite, gives non-finite
+ * results for its heads.
  *   q           dev [B][Hq][d] of `dtype`, 16-byte aligned
  *   page_table  dev int32 [B][max_pages]; entries past a sequence's last page are not used.  A
  *               page number outside [0, n_pages) sets IG_DEVERR_INDEX and its tokens are left out

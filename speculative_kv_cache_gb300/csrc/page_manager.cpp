@@ -24,7 +24,7 @@ ig_status fail(ig_status st, const char* fmt, ...);
 struct ig_pages {
   int n_pages = 0, page = 0, seqs = 0, max_pages = 0;
   std::vector<int32_t> refs;                  // sequences that use each page
-  std::vector<std::vector<int32_t>> table;    // pages of each sequence, room for max_pages reserved
+  std::vector<std::vector<int32_t>> table;    // pages of each sequence
   std::vector<int64_t> length;                // tokens of each sequence
   std::priority_queue<int32_t, std::vector<int32_t>, std::greater<int32_t>> free_pages;  // lowest first
 };

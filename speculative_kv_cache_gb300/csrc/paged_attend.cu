@@ -6,14 +6,14 @@
 // o = sum e^(z - m) V, and two parts join as m = max(m1, m2), l = sum l_i e^(m_i - m), o likewise.
 // Exponents are taken to base 2, with log2(e) folded into the scale.
 //
-// What bounds it.  Every key and value is read once from HBM and used by G queries: 4 d G flop for
-// 4 d bytes.  From G = 8 on that is more than the fp32 units do at HBM speed, so the products run
+// What bounds it.  Every key and value is read once from HBM and used by G queries (once per 64 queries where
+// G is larger): 4 d G flop for 4 d bytes.  From G = 8 on that is more than the fp32 units do at HBM speed, so the products run
 // on the tensor cores.  Tokens are the 16 rows of an MMA (mma.sync), queries its 8 columns: S^T = K Q^T,
 // then O^T = V^T P^T, which costs no padding at G = 8 and at G = 1 leaves the tensor cores far from
-// full (13 % busy at G = 5).  Not tcgen05: its M = 128 holds at most 64 queries twice, an MMA of it takes
-// the same 72 cycles at N = 64 as at N = 128, and a tile's two dependent batches wait 500 more; such a
-// kernel took 27 us where this takes 23 to 25 (16 sequences of 4099 tokens, G = 56) and was ahead only
-// in very long caches (34 against 40 us at 4 x 32768, G = 64), which the host cannot see coming.
+// full (13 % busy at G = 5).  A tcgen05 kernel with the queries as M (at most 64 of them, twice, in its M = 128;
+// 72 cycles an MMA whether N is 64 or 128, and 500 more of waits for a tile's two dependent batches) was about
+// equal: 26.5 to 27.5 us where this takes 23 (fp16) to 27 (bf16) (16 sequences of about 4050 tokens, G = 56), and
+// 34 where this takes 35 (fp16) to 40 (bf16) (4 x 32768 tokens, G = 64).  Tokens as M were not tried on tcgen05.
 //
 // Precision.  K, V, q enter as they are.  A weight in fp16 or bf16 alone would cost 2^-11 or 2^-8, so
 // it is split into 16-bit parts that are multiplied in turn: two for fp16 (20 bits or more), three for bf16 (24 bits).
@@ -21,8 +21,8 @@
 // bits too, as a large weight's value may be zero (a sink).  So the reference that weights are taken against need
 // not be the largest logit: it follows a tile down, by a power of two, which fp32 sums stand (kPaHigh) and
 // the next tiles then have for nothing; and the few weights of a tile that spans more go token by token
-// in fp32.  Nothing else changes for tiles within the parts: 16 x 4050 tokens, 56 heads 23.1 -> 22.9 us, 64 x 2048
-// tokens, 20 heads 27.0 -> 28.4 us, 33 heads of 64 15.1 -> 16.3 us (registers).  Sums over the
+// in fp32.  (It costs nothing at 16 x 4050 tokens, 56 heads, 23.1 us; 64 x 2048 tokens, 20 heads 27.7 -> 28.7
+// us; 16 x 4050 tokens, 33 heads of 64 15.1 -> 16.6 us.)  Sums over the
 // tokens of one tile run in the tensor cores, whose adds need not round to nearest; those over tiles in
 // fp32 adds that do, so that long sequences collect no bias.  (2-norm error against 64 bits 3e-7 to 6e-7,
 // plain fp32 torch operations 2e-7 to 1.2e-6.)
@@ -42,10 +42,12 @@
 // head ends.
 //
 // Measured (device time, HBM copy rate 6.79 TB/s): 64 sequences of 0 to 8192 tokens, 8 key heads of 128, 1.08
-// GB: 164 us, 6.5 TB/s, 0.96 of the copy rate; one of 131071 tokens, 537 MB: 83.7 us, 0.95; 8 of 2000
-// tokens, 32 key heads, 260 MB: 43 us, 0.89 (47 us where its 256 heads were cut); a launch costs 5 us beside
-// its bytes (launch 2, first loads 2, tail 1) and the join 3; 4 heads of 256 tokens: 5.8 us.  16 of 4050 tokens, 56 heads on one key head, 33 MB: 27 us,
-// bound by the products (three parts of bf16 weights) of one or two warps per scheduler.  What the steps
+// GB, bf16: 167 us, 6.4 TB/s, 0.95 of the copy rate; one of 131071 tokens, 537 MB, fp16: 85 us, 0.93; 8 of 2000
+// tokens, 32 key heads, 260 MB, fp16: 43.4 us, 0.88 (47 us where its 256 heads were cut); heads of 64, 64 of 4096
+// tokens, 32 heads on 8, 537 MB: 87 us, 0.91, either type; a launch costs 5 us beside its bytes (launch 2, first
+// loads 2, tail 1) and the join 3; 4 heads of 256 tokens: 6.0 us.  16 of 4050 tokens, 56 heads on one key head, 33
+// MB: 27 us in bf16, 23 in fp16, bound by the products (three and two parts of a weight) of one or two warps per
+// scheduler, as 64 of 2048 tokens with 16 heads on one key head, 67 MB: 26 us, floor 10.  What the steps
 // gave: page numbers in windows instead of per tile 190 -> 165 us and 58 -> 47 us (one producer warp had
 // set the pace); four products side by side instead of one accumulator after the other 1550 -> 1150 cycles
 // a tile; heads of a few tiles to one warp each 22.5 -> 13.9 us (104 x 17 heads of 3 tokens).
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
             }
         }
         // DG column tiles side by side, for the same reason (four of 16 queries where registers allow: 27.2 ->
-        // 26 us for 64 x 2048 tokens, 16 heads)
+        // 26 us for 64 x 2048 tokens, 16 heads, bf16)
         constexpr int DG = WQ == 1 ? 4 : 2;
 #pragma unroll
         for (int d0 = 0; d0 < D / 16; d0 += DG) {
@@ -975,8 +977,10 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
 
 // Joins the partials of the heads that were cut: block (x, y) takes unit x (or the head that CTA x
 // began) and rows y * RB ... of it, WPR warps a row; a warp takes every WPR-th partial in order, and the
-// warps join in order.  A warp a row where a head has few partials (blocks of four warps, which fit beside
-// the attention's: 1 us less than eight); with about 16 or more, four warps, with 64 or more, sixteen.
+// warps join in order.  A warp a row where a head would have few partials if every slot of the batch had
+// tokens (blocks of four warps, which fit beside the attention's: 1 us less than eight); with about 16 or more,
+// four warps, with 64 or more, sixteen.  (The host does not know the lengths: few long sequences in many
+// slots have more partials than that, joined by one warp a row.)
 template <int D, int WPR, int RB>
 __global__ void __launch_bounds__(WPR * RB * 32) k_paged_join(const float* __restrict__ part, const int2* __restrict__ info,
                                                              const PaShape s, int RU, float scale_bits,

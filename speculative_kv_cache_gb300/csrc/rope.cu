@@ -71,8 +71,8 @@ constexpr int kRopeWarpsPerSm = 32;
 // the half turns that sincospif takes.
 //
 // HBM-bound where there are many tokens: every row is read and written once.  Measured (4 x 3968
-// tokens of 32 + 64 heads of 128 fp16 into pages, 780 MB): 126 us, 6.2 TB/s, 0.91 of the copy rate; 4097
-// tokens of 40 + 16 normed bf16 heads (117 MB): 22.9 us, 5.1 TB/s; one launch alone 2.6 us.  The next
+// tokens of 32 + 64 heads of 128 fp16 into pages, 780 MB): 125 us, 6.2 TB/s, 0.92 of the copy rate; 4097
+// tokens of 40 + 16 normed bf16 heads (117 MB): 22.2 us, 5.3 TB/s; one launch alone 2.8 us.  The next
 // batch of rows is loaded before the last is worked on (without: 29 us for the second), five CTAs
 // per SM (4: 25.2, 6: 24.1, 8 with one row per batch: 23.3 us).
 template <bool BF, int D>

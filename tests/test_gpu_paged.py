@@ -913,3 +913,29 @@ def test_cache_keeps_its_free_pages_when_an_extension_does_not_fit(ig):
         assert t[0][0] == t[2][0] and t[0][1] != t[2][1]
     finally:
         cache.close()
+
+
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("group", [1, 12, 20, 56])
+def test_attend_non_finite_rows_stay_with_their_heads(ig, dt, d, group):
+    """A logit that is NaN or +inf makes its heads' results non-finite, a value that is not finite its
+    component, however small the weight; the other key head and the other sequences are right."""
+    c = make_attend(31 + group, dt, [100, 333, 64, 700], 2 * group, 2, d, 16)
+    c["q"][..., 0] = 1.0
+    at = lambda b, t: (c["table"][b, t // 16].item(), 0, t % 16)  # noqa: E731
+    c["K"][at(0, 70)] = float("nan")
+    c["K"][at(1, 5) + (0,)] = float("inf")
+    c["V"][at(2, 63) + (3,)] = float("-inf")
+    c["K"][at(2, 63) + (0,)] = -200 * math.sqrt(d)  # a weight of zero
+    out, lse = attend(ig, c)
+    ig.ig_check()
+    first = slice(0, group)
+    assert not torch.any(torch.isfinite(out[:2, first])) and not torch.any(torch.isfinite(lse[:2, first]))
+    assert not torch.any(torch.isfinite(out[2, first, 3])) and torch.all(torch.isfinite(lse[2, first]))
+    assert torch.all(torch.isfinite(torch.cat([out[2, first, :3], out[2, first, 4:]], -1)))
+    for b, keep in ((0, [1]), (1, [1]), (2, [1]), (3, [0, 1])):
+        for h in keep:
+            q = slice(h * group, (h + 1) * group)
+            one = dict(c, Hq=group, Hkv=1, q=c["q"][b:b + 1, q], K=c["K"][:, h:h + 1], V=c["V"][:, h:h + 1],
+                       table=c["table"][b:b + 1], lengths=c["lengths"][b:b + 1])
+            check_attend(one, out[b:b + 1, q], lse[b:b + 1, q])
