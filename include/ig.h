@@ -452,6 +452,121 @@ ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int Hkv, int d
                           const int32_t* L_valid, float* out, float* lse, void* workspace,
                           size_t workspace_bytes);
 
+/* Bounds of the keys of listed pages, which ig_page_select scores.  For page and rows (0 <= rows <= page) of entry i, per key
+ * head and channel c, over the page's first `rows` keys (over none: 0):
+ *   codes[page][h][0][c] = floor(min K_c / u), codes[page][h][1][c] = ceil(max K_c / u),  u = scales[page][h]
+ * with u the least power of two, from 2^-126 on, that keeps the codes within -127 .. 127.  Where a key is not finite,
+ * codes are 0 and u = +inf.  A page's bounds are made again once its keys have changed.
+ *   K       dev [n_pages][Hkv][page][d] of `dtype`, 16-byte aligned
+ *   list    dev int32 [n][2]: page, rows.  page < 0: the entry is skipped.  A page or number of rows out of range sets
+ *           IG_DEVERR_INDEX, and the entry is skipped.  A page may be listed once.
+ *   codes   dev int8 [n_pages][Hkv][2][d] out, 16-byte aligned;  scales dev fp32 [n_pages][Hkv] out; pages that are not
+ *           listed keep theirs
+ * d must be 64 or 128; n >= 0 (0: nothing is done), n * Hkv < 2^31, n_pages * Hkv * page < 2^31. */
+ig_status ig_page_bounds(void* stream, int dtype, int n_pages, int Hkv, int page, int d, const uint16_t* K,
+                         int n, const int32_t* list, int8_t* codes, float* scales);
+
+/* The pages of each sequence that one new token's queries attend to, for each key head by itself.  A query's
+ * codes are round(q_c / v) (halves to even), v the least power of two from 2^-126 on that keeps them within
+ * -127 .. 127 (a query that is not finite has codes 0, v = 1); the score of page p is
+ *   u_p * max over the key head's queries of v * sum_c max(code_c * lo_c, code_c * hi_c)
+ * (at most the largest fp32 number, which it also is where u_p = +inf): about the largest q . K_t that its keys allow,
+ * exact but for fp32's range, so that no rounding decides.  The first `first` and the last `last` pages of a
+ * sequence are always taken, and of the others those with the largest scores (ties: the lower page) until
+ * there are `picks`; all where there are no more than that.
+ *   q           dev [B][Hq][d] of `dtype`, 16-byte aligned
+ *   codes, scales  as ig_page_bounds has written them for the sequences' pages
+ *   page_table  dev int32 [B][max_pages];  L_valid dev int32 [B] (both as for ig_paged_attend; a page number out of
+ *               range scores lowest and sets IG_DEVERR_INDEX)
+ *   chosen      dev int32 [B][Hkv][picks] out: page numbers in the sequence's order, then -1
+ *   tokens      dev int32 [B][Hkv] out: the tokens they hold (all are full but the sequence's last one)
+ * chosen and tokens are what ig_paged_attend_picked takes.  d must be 64 or 128; Hq / Hkv at most 256; last >= 1,
+ * first + last <= picks; max_pages at most 262144, max_pages * page and picks * page < 2^30, B * Hq < 2^27,
+ * n_pages * Hkv * page < 2^31. */
+ig_status ig_page_select(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page, int n_pages,
+                         int max_pages, int picks, int first, int last, const uint16_t* q,
+                         const int8_t* codes, const float* scales, const int32_t* page_table,
+                         const int32_t* L_valid, int32_t* chosen, int32_t* tokens);
+
+/* ig_paged_attend with a page table and a length for each key head:
+ *   chosen      dev int32 [B][Hkv][picks] in place of page_table
+ *   tokens      dev int32 [B][Hkv], 0 <= tokens <= picks * page, in place of L_valid
+ * Token t of a key head is row t % page of page chosen[b][h][t / page].  Everything else, the workspace too, is as
+ * for ig_paged_attend, with picks for max_pages. */
+ig_status ig_paged_attend_picked(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page,
+                                 int n_pages, int picks, float scale, const uint16_t* q,
+                                 const uint16_t* K, const uint16_t* V, const int32_t* chosen,
+                                 const int32_t* tokens, float* out, float* lse, void* workspace,
+                                 size_t workspace_bytes);
+
+/* Attention of a tree of drafted tokens per request over its pages (to check them all in one pass).  The tokens are
+ * packed: request i's are first[i] .. first[i+1] - 1, n_i of them, the last n_i of the L_valid tokens of its sequence.  Token t
+ * sees token j of its sequence when j < L - n_i, or when bit j - (L - n_i) of masks[t] is set; for each query head
+ *   z_j = scale * q . K_j,  o = sum_j w_j V_j,  w = softmax over the tokens it sees,  lse = log(sum_j exp(z_j))
+ * in one pass over K and V for up to 128 (two at a time: 256) queries of a key head; products in fp16/bf16 with fp32 sums, softmax in
+ * fp32, the weights rounded to `dtype` for the second product (their sum is not), o rounded once.  In fp16, weights keep 11 bits down
+ * to 2^-28 of the largest and fewer down to 2^-38.  A token that sees nothing has o = 0 and lse = -inf.  What the pages hold past a sequence's last
+ * token, and in drafted rows that a token does not see, may be anything, NaN included; among what it sees, a logit
+ * of -inf has weight zero, a logit that is NaN or +inf, or a value that is not finite, gives non-finite results.
+ *   q           dev [T][Hq][d] of `dtype`, 16-byte aligned
+ *   page_table  dev int32 [seqs][max_pages];  L_valid dev int32 [seqs]: as for ig_paged_attend
+ *   seq         dev int32 [n]: the requests' sequences, or NULL (request i is sequence i)
+ *   first       dev int32 [n + 1], masks dev uint64 [T] (8-byte aligned): as ig_page_slots writes them.  A request whose
+ *               numbers cannot be (n_i outside 0 .. T_max, tokens past T, fewer than n_i tokens or more than the table holds)
+ *               sets IG_DEVERR_INDEX and its rows are left as they are
+ *   out         dev [T][Hq][d] of `dtype` out, 16-byte aligned;  lse dev fp32 [T][Hq] out, or NULL; rows of no
+ *               request are left as they are
+ *   workspace   dev, >= ig_paged_tree_attend_workspace_bytes(n, T_max, Hq, Hkv, d) bytes, 256-byte aligned; arbitrary
+ *               content, not shared by calls that may run at the same time
+ * T_max (1 .. 64): at least every n_i.  T >= 0 (0: nothing is done).  d must be 64 or 128; |scale| < 1e38; Hq <= 65536,
+ * T * Hq < 2^31, max_pages * page < 2^30, n_pages * Hkv * page < 2^31. */
+size_t ig_paged_tree_attend_workspace_bytes(int n, int T_max, int Hq, int Hkv, int d);
+ig_status ig_paged_tree_attend(void* stream, int dtype, int n, int T, int T_max, int Hq, int Hkv, int d,
+                               int page, int n_pages, int seqs, int max_pages, float scale,
+                               const uint16_t* q, const uint16_t* K, const uint16_t* V,
+                               const int32_t* page_table, const int32_t* L_valid, const int32_t* seq,
+                               const int32_t* first, const uint64_t* masks, uint16_t* out, float* lse,
+                               void* workspace, size_t workspace_bytes);
+
+/* Where the new tokens of n requests go, on the GPU, from the lengths and the page table.  Request i adds counts[i] tokens
+ * to its sequence, whose L_valid tokens include them; the tokens are packed, request by request:
+ *   first[i]      sum of the counts before request i (first[n]: of all)
+ *   slots[t]      slot of token t (the i-th new one of its request lies at L - count + i of its sequence)
+ *   positions[t]  L - count + i; for a tree (parents given) L - count + the token's depth
+ *   masks[t]      bits of its request's new tokens that are its ancestors, and its own
+ * as ig_qk_norm_rope and ig_paged_tree_attend take them.  Entries from first[n] up to T: slot -1, position 0, mask 0 (tokens
+ * that a step of a fixed size has to spare).
+ *   page_table  dev int32 [seqs][max_pages];  L_valid dev int32 [seqs]
+ *   seq         dev int32 [n]: the requests' sequences, each once, or NULL (request i is sequence i)
+ *   counts      dev int32 [n]
+ *   parents     dev int32 [T]: the parent of each token among the new tokens of its request, a lower number than its own, or
+ *               -1 (it follows the sequence's earlier tokens); NULL: each follows the one before it
+ *   first       dev int32 [n + 1] out;  slots, positions dev int32 [T] out;  masks dev uint64 [T] out, or NULL
+ * A request that cannot be (a sequence or length out of range, a negative count, more tokens than its sequence has, tokens past T, with
+ * parents or masks more than 64) sets IG_DEVERR_INDEX and its tokens get slot -1, position 0, mask 0; so does a page
+ * number out of range for the slot alone, and a parent out of range, which counts as -1.  first never exceeds T.
+ * 1 <= n <= 8192; T >= 0; page a positive multiple of 8; max_pages * page < 2^30, n_pages * page < 2^31.
+ * (Outputs and inputs must not overlap.) */
+ig_status ig_page_slots(void* stream, int n, int seqs, int page, int n_pages, int max_pages, int T,
+                        const int32_t* page_table, const int32_t* L_valid, const int32_t* seq,
+                        const int32_t* counts, const int32_t* parents, int32_t* first, int32_t* slots,
+                        int32_t* positions, uint64_t* masks);
+
+/* Of each request's drafted tokens the ones that are kept, moved to the front of them in every layer: row path[first[i] + k] of the drafted
+ * rows goes to row k, for k < kept[i], for every head of K and V.  (The caller then cuts the sequence back to
+ * L - n_i + kept[i] tokens: ig_pages_truncate.)
+ *   K, V    host arrays [layers] of dev pages [n_pages][Hkv][page][d] (16-bit elements of any type)
+ *   page_table, L_valid, seq, first  as for ig_paged_tree_attend (L_valid with the drafted tokens); no sequence twice, and no other
+ *           sequence shares the pages of the drafted rows (ig_pages_extend sees to that)
+ *   path    dev int32 [T]: from first[i] on, request i's kept tokens, ascending;  kept dev int32 [n]
+ * A request with a number out of range, more than 64 drafted tokens or a path that does not ascend sets IG_DEVERR_INDEX, and none
+ * of its rows move.  At most 128 layers per call; d a multiple of 8; n >= 0 (0: nothing is done);
+ * max_pages * page < 2^30, n_pages * Hkv * page < 2^31. */
+ig_status ig_tree_keep(void* stream, int layers, int n_pages, int Hkv, int page, int d,
+                       uint16_t* const* K, uint16_t* const* V, int n, int seqs, int max_pages, int T,
+                       const int32_t* page_table, const int32_t* L_valid, const int32_t* seq,
+                       const int32_t* first, const int32_t* path, const int32_t* kept);
+
 /* Rotary frequencies on the host, as ig_qk_norm_rope takes them: turns[j] is the fraction of a
  * turn that pair j moves per position, f_j / (2 pi) modulo 1, times 2^64 (so that the angle at
  * position p is the low 64 bits of p * turns[j], exact for every 32-bit position).

@@ -94,6 +94,8 @@ struct PaShape {
   int box;                 // rows of a TMA box, a power of two that divides page
   float scale2;            // scale * log2(e)
   int by_unit;             // info is indexed by unit (units <= CTAs) or by CTA
+  int KH;                  // key heads of a page
+  int own;                 // each key head has a table of its own: B and Hkv here are B * KH and 1
 };
 
 // shared memory behind the ring
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
     int first = 0, ids = -1, n = w.left > 0 ? window(w, first, ids) : 0;
     bool going = true;
     while (n > 0 && going) {
-      const int tile = w.tile(), hk = w.unit() / s.QT, L = w.L;
+      const int tile = w.tile(), hk = s.own ? w.b % s.KH : w.unit() / s.QT, L = w.L;
       w.advance(n);
       int first2 = 0, ids2 = -1;
       const int n2 = w.left > 0 ? window(w, first2, ids2) : 0;
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(pa_threads(WQ), kPaCtasPerSm) k_paged_attend(
         __syncwarp();
         if (ok)
           tma_load_3d(ring + st * kPaStageBytes + is_v * kKvBytes + box_at * (D * 2), is_v ? &map_v : &map_k, 0,
-                      (g * s.Hkv + hk) * s.page + row, 0, &sh.full[st]);
+                      (g * s.KH + hk) * s.page + row, 0, &sh.full[st]);
         ++it;
         if (++st == NS) {
           st = 0;
@@ -1104,7 +1106,7 @@ ig_status launch_paged(cudaStream_t st, PaShape s, const uint16_t* q, const uint
   while (s.page % s.box) s.box >>= 1;
   const long long most = (long long)s.B * ((s.max_pages * s.page + TT - 1) / TT) * s.Hkv * s.QT;
   IG_REQUIRE(most < (1ll << 31), "B*max_pages*page*Hkv is too large: %lld tiles", most);
-  const int rows = s.n_pages * s.Hkv * s.page;
+  const int rows = s.n_pages * s.KH * s.page;
   CUtensorMap mk, mv;
   ig_status r = make_map_halves(&mk, K, rows, D, s.box);
   if (r == IG_OK) r = make_map_halves(&mv, V, rows, D, s.box);
@@ -1164,18 +1166,20 @@ extern "C" size_t ig_paged_attend_workspace_bytes(int B, int Hq, int Hkv, int d)
   return pa_part_bytes(Hq / Hkv, d) + pa_info_bytes();
 }
 
-extern "C" ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page, int n_pages,
-                                     int max_pages, float scale, const uint16_t* q, const uint16_t* K,
-                                     const uint16_t* V, const int32_t* page_table, const int32_t* L_valid, float* out,
-                                     float* lse, void* workspace, size_t workspace_bytes) {
+namespace {
+
+// `own`: a table and a length for each key head
+ig_status attend_pages(bool own, void* stream, int dtype, int B, int Hq, int Hkv, int d, int page, int n_pages, int max_pages,
+                       float scale, const uint16_t* q, const uint16_t* K, const uint16_t* V, const int32_t* page_table,
+                       const int32_t* L_valid, float* out, float* lse, void* workspace, size_t workspace_bytes) {
   IG_REQUIRE(dtype == IG_F16 || dtype == IG_BF16, "dtype must be IG_F16 or IG_BF16 (got %d)", dtype);
   IG_REQUIRE(B > 0 && Hq > 0 && Hkv > 0, "B, Hq, Hkv must be positive");
   IG_REQUIRE(Hq % Hkv == 0, "Hq = %d is not a multiple of Hkv = %d", Hq, Hkv);
   IG_REQUIRE(d == 64 || d == 128, "d must be 64 or 128 (got %d)", d);
   IG_REQUIRE(page > 0 && page % 8 == 0, "page must be a positive multiple of 8 (got %d)", page);
-  IG_REQUIRE(n_pages > 0 && max_pages > 0, "n_pages and max_pages must be positive");
+  IG_REQUIRE(n_pages > 0 && max_pages > 0, "n_pages and %s must be positive", own ? "picks" : "max_pages");
   IG_REQUIRE(Hq <= 65536 && (long long)B * Hq < (1ll << 31), "Hq at most 65536, B*Hq below 2^31");
-  IG_REQUIRE((long long)max_pages * page < (1ll << 30), "max_pages*page must stay below 2^30");
+  IG_REQUIRE((long long)max_pages * page < (1ll << 30), "%s*page must stay below 2^30", own ? "picks" : "max_pages");
   IG_REQUIRE((double)n_pages * Hkv * page < 2147483648.0, "n_pages*Hkv*page must stay below 2^31 rows");
   IG_REQUIRE(isfinite(scale) && fabsf(scale) < 1e38f, "scale must be finite (and below 1e38)");
   IG_REQUIRE(q && K && V && page_table && L_valid && out, "null pointer argument");
@@ -1189,10 +1193,13 @@ extern "C" ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int
   IG_REQUIRE(aligned(workspace, 256), "workspace must be 256-byte aligned");
   cudaStream_t st = as_stream(stream);
   PaShape s{};
-  s.B = B;
-  s.Hq = Hq;
-  s.Hkv = Hkv;
+  // with a table for each key head, key heads are sequences: queries, results and tables lie as they did
+  s.B = own ? B * Hkv : B;
+  s.Hq = own ? Hq / Hkv : Hq;
+  s.Hkv = own ? 1 : Hkv;
   s.G = Hq / Hkv;
+  s.KH = Hkv;
+  s.own = own ? 1 : 0;
   s.page = page;
   s.n_pages = n_pages;
   s.max_pages = max_pages;
@@ -1202,4 +1209,22 @@ extern "C" ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int
                     : launch_rows<false, 64>(st, s, q, K, V, page_table, L_valid, out, lse, workspace);
   return d == 128 ? launch_rows<true, 128>(st, s, q, K, V, page_table, L_valid, out, lse, workspace)
                   : launch_rows<true, 64>(st, s, q, K, V, page_table, L_valid, out, lse, workspace);
+}
+
+}  // namespace
+
+extern "C" ig_status ig_paged_attend(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page, int n_pages,
+                                     int max_pages, float scale, const uint16_t* q, const uint16_t* K,
+                                     const uint16_t* V, const int32_t* page_table, const int32_t* L_valid, float* out,
+                                     float* lse, void* workspace, size_t workspace_bytes) {
+  return attend_pages(false, stream, dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scale, q, K, V, page_table, L_valid, out, lse,
+                      workspace, workspace_bytes);
+}
+
+extern "C" ig_status ig_paged_attend_picked(void* stream, int dtype, int B, int Hq, int Hkv, int d, int page, int n_pages,
+                                            int picks, float scale, const uint16_t* q, const uint16_t* K, const uint16_t* V,
+                                            const int32_t* chosen, const int32_t* tokens, float* out, float* lse,
+                                            void* workspace, size_t workspace_bytes) {
+  return attend_pages(true, stream, dtype, B, Hq, Hkv, d, page, n_pages, picks, scale, q, K, V, chosen, tokens, out, lse,
+                      workspace, workspace_bytes);
 }

@@ -119,6 +119,14 @@ _sig("ig_dense_attend", _i, _vp, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _v
 _sig("ig_append_kv", _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp)
 _sig("ig_paged_attend_workspace_bytes", _sz, _i, _i, _i, _i)
 _sig("ig_paged_attend", _i, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz)
+_sig("ig_paged_attend_picked", _i, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz)
+_sig("ig_page_bounds", _i, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp)
+_sig("ig_page_select", _i, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp)
+_sig("ig_paged_tree_attend_workspace_bytes", _sz, _i, _i, _i, _i, _i)
+_sig("ig_paged_tree_attend", _i, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+     _vp, _vp, _vp, _sz)
+_sig("ig_page_slots", _i, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp)
+_sig("ig_tree_keep", _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp)
 _sig("ig_rope_turns", _i, _i, _d, _i, _d, _i, _d, _d, _vp, C.POINTER(_f))
 _sig("ig_qk_norm_rope", _i, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _f, _vp, _vp, _f,
      _vp, _i, _i, _vp, _vp, _vp)
@@ -495,6 +503,60 @@ def ig_paged_attend(stream, dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scal
     _ok(_lib.ig_paged_attend(_s(stream), dtype, B, Hq, Hkv, d, page, n_pages, max_pages, scale, _q(q, h), _q(K, h),
                              _q(V, h), _q(page_table, h), _q(L_valid, h), _q(out, h), _q(lse, h), _q(workspace, h),
                              workspace_bytes), "ig_paged_attend")
+
+
+def ig_paged_attend_picked(stream, dtype, B, Hq, Hkv, d, page, n_pages, picks, scale, q, K, V, chosen, tokens, out, lse,
+                           workspace, workspace_bytes):
+    h = _here()
+    _ok(_lib.ig_paged_attend_picked(_s(stream), dtype, B, Hq, Hkv, d, page, n_pages, picks, scale, _q(q, h), _q(K, h),
+                                    _q(V, h), _q(chosen, h), _q(tokens, h), _q(out, h), _q(lse, h), _q(workspace, h),
+                                    workspace_bytes), "ig_paged_attend_picked")
+
+
+def ig_page_bounds(stream, dtype, n_pages, Hkv, page, d, K, n, list, codes, scales):
+    h = _here()
+    _ok(_lib.ig_page_bounds(_s(stream), dtype, n_pages, Hkv, page, d, _q(K, h), n, _q(list, h), _q(codes, h), _q(scales, h)),
+        "ig_page_bounds")
+
+
+def ig_page_select(stream, dtype, B, Hq, Hkv, d, page, n_pages, max_pages, picks, first, last, q, codes, scales, page_table,
+                   L_valid, chosen, tokens):
+    h = _here()
+    _ok(_lib.ig_page_select(_s(stream), dtype, B, Hq, Hkv, d, page, n_pages, max_pages, picks, first, last, _q(q, h),
+                            _q(codes, h), _q(scales, h), _q(page_table, h), _q(L_valid, h), _q(chosen, h), _q(tokens, h)),
+        "ig_page_select")
+
+
+def ig_paged_tree_attend_workspace_bytes(n, T_max, Hq, Hkv, d) -> int:
+    return _lib.ig_paged_tree_attend_workspace_bytes(n, T_max, Hq, Hkv, d)
+
+
+def ig_paged_tree_attend(stream, dtype, n, T, T_max, Hq, Hkv, d, page, n_pages, seqs, max_pages, scale, q, K, V, page_table,
+                         L_valid, seq, first, masks, out, lse, workspace, workspace_bytes):
+    h = _here()
+    _ok(_lib.ig_paged_tree_attend(_s(stream), dtype, n, T, T_max, Hq, Hkv, d, page, n_pages, seqs, max_pages, scale, _q(q, h),
+                                  _q(K, h), _q(V, h), _q(page_table, h), _q(L_valid, h), _q(seq, h), _q(first, h),
+                                  _q(masks, h), _q(out, h), _q(lse, h), _q(workspace, h), workspace_bytes),
+        "ig_paged_tree_attend")
+
+
+def ig_page_slots(stream, n, seqs, page, n_pages, max_pages, T, page_table, L_valid, seq, counts, parents, first, slots,
+                  positions, masks=None):
+    h = _here()
+    _ok(_lib.ig_page_slots(_s(stream), n, seqs, page, n_pages, max_pages, T, _q(page_table, h), _q(L_valid, h), _q(seq, h),
+                           _q(counts, h), _q(parents, h), _q(first, h), _q(slots, h), _q(positions, h), _q(masks, h)),
+        "ig_page_slots")
+
+
+def ig_tree_keep(stream, layers, n_pages, Hkv, page, d, K, V, n, seqs, max_pages, T, page_table, L_valid, seq, first, path,
+                 kept):
+    """K, V: lists of every layer's device pages."""
+    if len(K) != layers or len(V) != layers:
+        raise ValueError("one K and one V per layer")
+    h, arr = _here(), _vp * layers
+    K, V = arr(*_qs(K, h)), arr(*_qs(V, h))
+    _ok(_lib.ig_tree_keep(_s(stream), layers, n_pages, Hkv, page, d, K, V, n, seqs, max_pages, T, _q(page_table, h),
+                          _q(L_valid, h), _q(seq, h), _q(first, h), _q(path, h), _q(kept, h)), "ig_tree_keep")
 
 
 def ig_rope_turns(rot, theta, scaling, factor, context, p0, p1, turns) -> float:
