@@ -1,8 +1,33 @@
 // Attention of a tree of drafted tokens per request over a paged KV cache.
 //
 // Mathematics.  Request b has L tokens, the last n of them drafted.  Drafted token t sees key j when j < L - n, or when bit
-// j - (L - n) of its mask is set (its ancestors and itself); for each query head
-//   z_j = scale q . K_j,  o = sum_j e^(z_j) V_j / sum_j e^(z_j)  over the keys it sees.
+// j - (L - n) of its mask is set (its ancestors and itself); for each of the G = Hq / Hkv query heads of a key head
+//   z_j = scale q . K_j,  o = sum_j e^(z_j) V_j / sum_j e^(z_j)  over the keys it sees,
+// in one pass over the tokens: every part keeps a reference m, l = sum 2^(z - m) and o = sum 2^(z - m) V (log2(e) is in
+// the scale), and two parts join as m = max(m1, m2), l = sum l_i 2^(m_i - m), o likewise.
+//
+// What bounds it.  The n G rows of a key head share its keys and values: 4 d n G flop for 4 d bytes, so HBM up to about
+// 280 rows and the tensor cores beyond.  Rows are the M = 128 of tcgen05.mma, tokens its N and the second product's K:
+//   S[rows][128 tokens] = Q K^T (both in shared memory),  O[rows][d] += P V (P in tensor memory, where S was).
+//
+// A CTA (one an SM): a warp moves tiles of 128 tokens with TMA into a ring, keys and values in turn, in the order they are used; one
+// thread issues the MMAs; a warp fetches the units' queries; two groups of four warps turn S into P, a row a thread, each
+// with S and O columns of its own, so that one works on its logits while the tensor cores work for the other.
+// Up to 128 rows the groups take tiles in turn and join their parts at the end (SPLIT); with more, a
+// unit is 256 rows, and each group has 128 of them and every tile (PAIR), which halves what is read.
+//
+// Precision.  Weights are rounded to the type for the second product.  Fp16 has few exponents: the reference lies 2^14 below the
+// largest logit, so that weights keep their 11 bits down to 2^-28 of it.  The reference moves (and O is scaled by
+// the factor) only when a logit is more than 2^(1 or 8) above what it was set by.  Sums of weights are fp32, unrounded.
+//
+// What is not attended.  Logits of tokens that a row does not see are left out by bits (the tile's tokens that hold
+// anything, the row's mask), whatever they are.  A value of zero weight must not be NaN in an MMA: rows without a token are
+// cleared in shared memory, and in drafted rows, which only some see, elements that are not finite; the rows that
+// see them get them at the end.
+//
+// Work split.  As in the attention of one token: all tiles of all units in order, cut in equal shares, one a CTA; a unit in
+// several CTAs leaves partials in the workspace (two slots a CTA: the unit it starts with, the unit it ends with), joined in
+// order by a second kernel.  No atomics: the result does not depend on timing.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -50,75 +75,932 @@ __device__ __forceinline__ uint16_t from_float(float v) {
   else return __half_as_ushort(__float2half_rn(v));
 }
 
-// A block a token and key head, a warp a query; a lane a key for the logits, a lane D/32 columns for the sums.
-template <bool BF, int D>
-__global__ void __launch_bounds__(128) k_tree_simple(const uint16_t* __restrict__ q, const uint16_t* __restrict__ K,
-                                                     const uint16_t* __restrict__ V, const TreeShape a, uint16_t* __restrict__ out,
-                                                     float* __restrict__ lse, int* err) {
-  __shared__ float sq[4][D];
-  const int t = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int r = 0;
-  while (r < a.B && __ldca(a.first + r + 1) <= t) ++r;
-  if (r >= a.B || __ldca(a.first + r) > t) return;
-  TreeRequest x;
-  if (!tree_request(a, r, x)) {
-    if (threadIdx.x == 0) raise_error(err, IG_DEVERR_INDEX);
-    return;
-  }
-  const unsigned long long mask = __ldca(a.masks + t);
-  for (int g = warp; g < a.G; g += 4) {
-    const size_t at = (size_t)t * a.Hq + (size_t)h * a.G + g;
-    for (int i = lane; i < D; i += 32) sq[warp][i] = to_float<BF>(q[at * D + i]);
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[D / 32];
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    for (int j0 = 0; j0 < x.L; j0 += 32) {
-      const int j = j0 + lane, bit = j - (x.L - x.n);
-      bool seen = j < x.L && (bit < 0 || (mask >> bit & 1));
-      int row = 0;
-      if (seen) {
-        const int pg = __ldca(a.table + (size_t)x.s * a.max_pages + j / a.page);
-        if (pg < 0 || pg >= a.n_pages) {
-          raise_error(err, IG_DEVERR_INDEX);
-          seen = false;
-        } else {
-          row = (pg * a.Hkv + h) * a.page + j % a.page;
-        }
-      }
-      float z = -INFINITY;
-      if (seen) {
-        float acc = 0.f;
-        for (int i = 0; i < D; ++i) acc = fmaf(sq[warp][i], to_float<BF>(K[(size_t)row * D + i]), acc);
-        z = acc * a.scale2;
-      }
-      float mx = z;
-      for (int s = 16; s; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-      const float mn = fmaxf(m, mx), m0 = mn == -INFINITY ? 0.f : mn;
-      const float c = ex2(m - m0), p = seen ? ex2(z - m0) : 0.f;
-      l = l * c + p;
-      for (int i = 0; i < D / 32; ++i) o[i] *= c;
-      for (unsigned left = __ballot_sync(0xffffffffu, seen); left; left &= left - 1) {
-        const int k = __ffs(left) - 1;
-        const float pk = __shfl_sync(0xffffffffu, p, k);
-        const int rk = __shfl_sync(0xffffffffu, row, k);
-        for (int i = 0; i < D / 32; ++i) o[i] = fmaf(pk, to_float<BF>(V[(size_t)rk * D + i * 32 + lane]), o[i]);
-      }
-      m = mn;
+constexpr int kTreeTile = 128;                 // tokens of a tile, rows of a block
+constexpr int kTreeThreads = 352;              // warps: 0 TMA, 1 MMA, 2 .. 9 softmax, 10 queries
+constexpr int kTreeSoftmax = 2;                // first softmax warp
+constexpr int kMaxTreeCtas = 160;              // upper bound of the grid (sizes the workspace)
+constexpr int kTreePartHead = 4;               // a partial: [m, l, -, -, o[D]]
+constexpr uint32_t kTreeTmem = 512;            // columns: S of either group, then O of either
+// Units that could have a CTA each are not cut where the longest has at most kTreeWhole tiles, or where there are enough
+// of them to keep HBM busy and the longest is at most kTreeEven tiles above the mean.
+constexpr int kTreeWhole = 4;
+constexpr int kTreeEven = 3;
+
+template <int D>
+__host__ __device__ constexpr int tree_slots() { return D == 128 ? 5 : 8; }
+template <int D>
+__host__ __device__ constexpr uint32_t tree_slot_bytes() { return kTreeTile * D * 2; }
+
+struct TreeShared {
+  uint64_t full[8], empty[8];       // the ring's slots
+  uint64_t s_full[2], p_full[2];    // a group's logits are there, its weights are
+  uint64_t o_done[2];               // its last product of a unit
+  uint64_t q_full[2], q_empty[2];   // queries
+  uint64_t half[2], o_free[2];      // a group's part of a unit is there for the other, has been taken
+  uint64_t drain;
+  uint32_t valid[8][4];             // tokens of a tile that hold anything
+  float2 ml[kTreeTile];
+  int poison[4];                    // by unit: 1 + its number, if it has drafted values that are not finite
+  int scan[kTreeThreads / 32][3];
+  uint32_t tmem;
+  int start_r, start_off, abort;
+};
+
+template <int D>
+constexpr size_t tree_smem() {
+  return 1024 + 2 * tree_slot_bytes<D>() + tree_slots<D>() * tree_slot_bytes<D>() + sizeof(TreeShared);
+}
+static_assert(tree_smem<128>() <= 232448, "more shared memory than a CTA can have");
+
+// Descriptor of an MN-major, 128B-swizzled tile (values: rows are tokens, the product's K): 64-column halves `half` bytes
+// apart (leading offset), groups of 8 rows 1024 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t half) {
+  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(half >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tm_ld64(uint32_t (&r)[64], uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+      "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tree_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tree_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// A bounded wait that ends together with the CTA's other waits; one verdict for the warp.
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit, int* err) {
+  bool ok = false;
+  for (uint32_t i = 0; i < limit && !*abort; ++i)
+    if (mbar_try_wait(bar, parity)) {
+      ok = true;
+      break;
     }
-    for (int s = 16; s; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = 0; i < D / 32; ++i) out[at * D + i * 32 + lane] = from_float<BF>(o[i] * inv);
-    if (lse && lane == 0) lse[at] = (m + log2f(l)) * 0.6931471805599453f;
-    __syncwarp();
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok && (threadIdx.x & 31) == 0 && !atomicExch(const_cast<int*>(abort), 1)) raise_error(err, IG_DEVERR_TIMEOUT);
+  return ok;
+}
+
+// The units of a CTA's share, in order: of each request its key heads, of each key head its blocks of rows.
+struct TreeWalk {
+  int RU;        // rows of a unit
+  bool whole;    // shares of whole units
+  int r, left;   // request; tiles (whole units) left
+  TreeRequest x;
+  int blocks, units, nt, u, tile;  // blocks of rows of a key head, units of the request, tiles of a unit; unit and tile in it
+
+  __device__ bool enter(const TreeShape& a) {
+    if (!tree_request(a, r, x) || x.n == 0) return false;
+    blocks = (x.n * a.G + RU - 1) / RU;
+    units = blocks * a.Hkv;
+    nt = (x.L + kTreeTile - 1) / kTreeTile;
+    return true;
+  }
+  __device__ void start(const TreeShape& a, int request, int off, int n) {
+    r = request;
+    left = n;
+    u = tile = 0;
+    if (left <= 0 || !enter(a)) {
+      left = 0;
+      return;
+    }
+    u = whole ? off : off / nt;
+    tile = whole ? 0 : off % nt;
+  }
+  __device__ int run() const { return whole ? nt : min(nt - tile, left); }
+  __device__ void next(const TreeShape& a) {
+    left -= whole ? 1 : run();
+    tile = 0;
+    if (left <= 0 || ++u < units) return;
+    u = 0;
+    do ++r;
+    while (r < a.B && !enter(a));
+    if (r >= a.B) left = 0;
+  }
+};
+
+// Bits of the 32 tokens from `off` on (counted from the first drafted one) that a row with this mask sees.
+__device__ __forceinline__ uint32_t seen_bits(unsigned long long mask, int off) {
+  if (off >= 64) return 0u;
+  if (off >= 0) return (uint32_t)(mask >> off);
+  if (off <= -32) return ~0u;
+  return (uint32_t)(mask << -off) | ((1u << -off) - 1);
+}
+
+// 16-bit pairs: whether either is not finite
+template <bool BF>
+__device__ __forceinline__ uint32_t odd_pair(uint32_t v) {
+  return BF ? ((v & 0x7f807f80u) + 0x00800080u) & 0x80008000u : ((v & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (BF) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
 
-template <bool BF, int D>
+template <bool BF, int D, bool PAIR>
+__global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const uint16_t* __restrict__ q,
+    const uint16_t* __restrict__ V, const TreeShape a, const int box, uint16_t* __restrict__ out, float* __restrict__ lse,
+    float* __restrict__ part, int4* __restrict__ info, int* err) {
+  constexpr int NS = tree_slots<D>(), RU = PAIR ? 2 * kTreeTile : kTreeTile;
+  constexpr uint32_t kSlot = tree_slot_bytes<D>(), kHalf = kTreeTile * 128;
+  // kind::f16, D fp32, A and B of the type; N >> 3 at bits 17-22, M >> 4 at bits 24-28; bit 16: B is MN-major
+  constexpr uint32_t kType = (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(kTreeTile >> 4) << 24);
+  constexpr uint32_t kIdS = kType | ((uint32_t)(kTreeTile >> 3) << 17);
+  constexpr uint32_t kIdO = kType | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sq = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  unsigned char* ring = sq + 2 * kSlot;
+  TreeShared& sh = *reinterpret_cast<TreeShared*>(ring + NS * kSlot);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_done[i], 1);
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_empty[i], 1);
+      mbar_init(&sh.half[i], 4);
+      mbar_init(&sh.o_free[i], 4);
+    }
+    mbar_init(&sh.drain, 1);
+    for (int i = 0; i < 4; ++i) sh.poison[i] = 0;
+    sh.abort = 0;
+    fence_mbar_init();
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  // Tensor memory is taken when the kernels before have ended and before the next may start: none of them waits for
+  // columns that another holds while it waits.
+  pdl_wait();
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "r"(kTreeTmem));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+
+  // ---- this CTA's share of all tiles, and the request it starts in
+  TreeWalk w;
+  w.RU = RU;
+  const int per = (a.B + kTreeThreads - 1) / kTreeThreads;
+  const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
+  int tiles = 0, units = 0, longest = 0;
+  for (w.r = b0; w.r < b1; ++w.r) {
+    if (w.enter(a)) {
+      tiles += w.units * w.nt;
+      units += w.units;
+      longest = max(longest, w.nt);
+    } else if (blockIdx.x == 0 && !tree_request(a, w.r, w.x)) {
+      raise_error(err, IG_DEVERR_INDEX);
+    }
+  }
+  int tiles_in = tiles, units_in = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, tiles_in, o), y2 = __shfl_up_sync(0xffffffffu, units_in, o);
+    if (lane >= o) {
+      tiles_in += y;
+      units_in += y2;
+    }
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+  }
+  if (lane == 31) {
+    sh.scan[warp][0] = tiles_in;
+    sh.scan[warp][1] = units_in;
+    sh.scan[warp][2] = longest;
+  }
+  if (threadIdx.x == 0) info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = sh.tmem;
+  int tiles_before = tiles_in - tiles, units_before = units_in - units, all_tiles = 0, all_units = 0;
+#pragma unroll
+  for (int i = 0; i < kTreeThreads / 32; ++i) {
+    tiles_before += i < warp ? sh.scan[i][0] : 0;
+    units_before += i < warp ? sh.scan[i][1] : 0;
+    all_tiles += sh.scan[i][0];
+    all_units += sh.scan[i][1];
+    longest = max(longest, sh.scan[i][2]);
+  }
+  const int cta = blockIdx.x;
+  w.whole = all_units <= (int)gridDim.x &&
+            (longest <= kTreeWhole ||
+             (2 * all_units >= (int)gridDim.x && (long long)longest * all_units <= (long long)all_tiles + kTreeEven * all_units));
+  const int total = w.whole ? all_units : all_tiles, before = w.whole ? units_before : tiles_before,
+            mine = w.whole ? units : tiles, ctas = min((int)gridDim.x, total);
+  const unsigned each = ctas ? (unsigned)total / ctas : 0, rest = ctas ? (unsigned)total % ctas : 0;
+  auto first_of = [&](unsigned c) -> int { return (int)(each * c + rest * c / (unsigned)ctas); };  // CTA c's first share
+  const int r0 = cta < ctas ? first_of(cta) : 0, r1 = cta < ctas ? first_of(cta + 1) : 0;
+  if (r1 > r0 && r0 >= before && r0 < before + mine) {
+    int at = before;
+    for (w.r = b0; w.r < b1; ++w.r) {
+      const int n = w.enter(a) ? w.units * (w.whole ? 1 : w.nt) : 0;
+      if (r0 < at + n) {
+        sh.start_r = w.r;
+        sh.start_off = r0 - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  w.start(a, sh.start_r, sh.start_off, r1 - r0);
+  const uint32_t most_iters = (uint32_t)kDefaultWaitIters;
+  uint32_t it = 0, hole = ~0u;  // the producer's ring: slots filled, and one left out
+
+  if (warp == 0) {
+    // ---- tiles.  Lane i moves box i / halves, half i % halves; a page's number is read two tiles ahead of its keys.
+    constexpr int H = D / 64;
+    const int box_at = lane / H * box, col = lane % H;
+    const uint32_t box_bytes = (uint32_t)box * 128;
+    struct Tile {
+      int token0, L, hk, id;
+      bool is;
+    };
+    int at = 0, run = w.left > 0 ? w.run() : 0;
+    auto fetch = [&]() -> Tile {
+      Tile t{0, 0, 0, -1, false};
+      if (w.left <= 0) return t;
+      t.is = true;
+      t.token0 = (w.tile + at) * kTreeTile;
+      t.L = w.x.L;
+      t.hk = w.u / w.blocks;
+      const int token = t.token0 + box_at;
+      if (box_at < kTreeTile && token < t.L) t.id = __ldca(a.table + (size_t)w.x.s * a.max_pages + token / a.page);
+      if (++at == run) {
+        w.next(a);
+        at = 0;
+        run = w.left > 0 ? w.run() : 0;
+      }
+      return t;
+    };
+    uint32_t tile = 0;
+    // a tile's keys or values into the ring's next slot; false when the CTA gives up
+    auto load = [&](const Tile& t, bool values) -> bool {
+      const uint32_t st = it % NS;
+      if (it >= NS && !tree_wait(&sh.empty[st], (it / NS - 1) & 1, &sh.abort, most_iters, err)) return false;
+      const int token = t.token0 + box_at;
+      const bool want = box_at < kTreeTile && token < t.L, ok = want && t.id >= 0 && t.id < a.n_pages;
+      const unsigned moving = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, want && !ok);
+      if (lane == 0) {
+        if (!values) {
+          const int live = min(t.L - t.token0, kTreeTile);
+          uint32_t v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = live >= 32 * i + 32 ? ~0u : live <= 32 * i ? 0u : (1u << (live - 32 * i)) - 1;
+          if (bad) {
+            raise_error(err, IG_DEVERR_INDEX);
+            for (unsigned m = bad; m; m &= m - 1) {
+              const int b = (__ffs(m) - 1) / H * box;
+              for (int i = 0; i < box; i += 8) v[(b + i) >> 5] &= ~(0xffu << ((b + i) & 31));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sh.valid[tile & 7][i] = v[i];
+        }
+        mbar_arrive_expect_tx(&sh.full[st], (uint32_t)__popc(moving) * box_bytes);
+      }
+      __syncwarp();
+      if (ok)
+        tma_load_2d(ring + st * kSlot + col * kHalf + box_at * 128, values ? &map_v : &map_k, col * 64,
+                    (t.id * a.Hkv + t.hk) * a.page + token % a.page, &sh.full[st]);
+      ++it;
+      if (!values) ++tile;
+      return true;
+    };
+    Tile t0 = fetch(), t1 = fetch();
+    bool going = t0.is && load(t0, false);
+    while (going && t0.is) {
+      const Tile t2 = fetch();
+      if constexpr (PAIR) {
+        going = load(t0, true) && (!t1.is || load(t1, false));
+      } else {
+        if (t1.is) going = load(t1, false);
+        else hole = it++;
+        going = going && load(t0, true);
+      }
+      t0 = t1;
+      t1 = t2;
+    }
+  } else if (warp == 1) {
+    // ---- the MMAs.  One thread issues them; the warp walks and waits together.
+    uint32_t q_used = 0, p_seen[2] = {0, 0};
+    bool ok = true;
+    const bool issuer = lane == 0;
+    auto full = [&](uint32_t idx) -> bool {
+      const bool f = tree_wait(&sh.full[idx % NS], (idx / NS) & 1, &sh.abort, most_iters, err);
+      tc_fence_after();
+      return f;
+    };
+    // S of group g from queries at qa and the keys in slot idx
+    auto logits = [&](int g, uint32_t qa, uint32_t idx) {
+      const uint32_t kb = smem_addr(ring + idx % NS * kSlot);
+      if (issuer) {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t o = (ks / 4) * kHalf + (ks % 4) * 32;
+          asm volatile(
+              "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+                  tmem + g * kTreeTile),
+              "l"(sw128_desc(qa + o)), "l"(sw128_desc(kb + o)), "r"(kIdS), "r"(ks > 0 ? 1u : 0u));
+        }
+        tree_commit(&sh.s_full[g]);
+      }
+      __syncwarp();
+    };
+    // O of group g, from its weights and the values in slot idx
+    auto values = [&](int g, uint32_t idx, bool more) {
+      const uint32_t vb = smem_addr(ring + idx % NS * kSlot);
+      if (issuer) {
+#pragma unroll
+        for (int ks = 0; ks < kTreeTile / 16; ++ks)
+          asm volatile(
+              "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
+                  tmem + 2 * kTreeTile + g * kTreeTile),
+              "r"(tmem + g * kTreeTile + ks / 4 * 64 + ks % 4 * 8), "l"(sw128_desc_mn(vb + ks * 2048, kHalf)), "r"(kIdO),
+              "r"(more || ks > 0 ? 1u : 0u));
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (issuer) tree_commit(bar);
+      __syncwarp();
+    };
+    auto weights = [&](int g) -> bool {
+      const bool f = tree_wait(&sh.p_full[g], p_seen[g]++ & 1, &sh.abort, most_iters, err);
+      tc_fence_after();
+      return f;
+    };
+    if constexpr (!PAIR) {
+      // logits of a tile ahead of the values of the one before; tile i is of group i & 1
+      uint32_t i = 0;             // tile whose logits are next
+      int seg_run = w.left > 0 ? w.run() : 0, seg_at = 0;
+      auto ahead = [&]() -> bool {  // the next tile's logits
+        const uint32_t buf = q_used & 1;
+        if (seg_at == 0 && !tree_wait(&sh.q_full[buf], (q_used >> 1) & 1, &sh.abort, most_iters, err)) return false;
+        const uint32_t idx = i == 0 ? 0 : 2 * i - 1;
+        if (!full(idx)) return false;
+        logits(i & 1, smem_addr(sq + buf * kSlot), idx);
+        commit(&sh.empty[idx % NS]);
+        ++i;
+        if (++seg_at == seg_run) {
+          commit(&sh.q_empty[buf]);
+          ++q_used;
+          w.next(a);
+          seg_at = 0;
+          seg_run = w.left > 0 ? w.run() : 0;
+        }
+        return true;
+      };
+      TreeWalk v = w;  // of the values
+      if (w.left > 0) ok = ahead();
+      for (uint32_t j = 0; ok && v.left > 0; v.next(a)) {
+        const int run = v.run();
+        for (int k = 0; k < run && ok; ++k, ++j) {
+          if (w.left > 0) ok = ahead();
+          const uint32_t idx = 2 * j + 2;
+          ok = ok && weights(j & 1) && full(idx);
+          if (!ok) break;
+          values(j & 1, idx, k >= 2);
+          commit(&sh.empty[idx % NS]);
+          if (k >= run - 2) commit(&sh.o_done[j & 1]);
+        }
+      }
+    } else {
+      uint32_t j = 0;
+      const uint32_t qa = smem_addr(sq), qb = qa + kSlot;
+      for (; ok && w.left > 0; w.next(a)) {
+        const int run = w.run(), rows = w.x.n * a.G - w.u % w.blocks * RU;
+        const bool two = rows > kTreeTile;
+        ok = tree_wait(&sh.q_full[0], q_used & 1, &sh.abort, most_iters, err) && full(2 * j);
+        if (!ok) break;
+        logits(0, qa, 2 * j);
+        if (two) logits(1, qb, 2 * j);
+        commit(&sh.empty[2 * j % NS]);
+        if (run == 1) commit(&sh.q_empty[0]);
+        for (int k = 0; k < run && ok; ++k, ++j) {
+          const uint32_t vi = 2 * j + 1, ki = 2 * j + 2;
+          ok = weights(0) && full(vi);
+          if (!ok) break;
+          values(0, vi, k > 0);
+          if (k == run - 1) commit(&sh.o_done[0]);
+          if (k < run - 1) {
+            ok = full(ki);
+            if (!ok) break;
+            logits(0, qa, ki);
+          }
+          if (two) {
+            ok = weights(1);
+            if (!ok) break;
+            values(1, vi, k > 0);
+            if (k == run - 1) commit(&sh.o_done[1]);
+            if (k < run - 1) logits(1, qb, ki);
+          }
+          commit(&sh.empty[vi % NS]);
+          if (k < run - 1) commit(&sh.empty[ki % NS]);
+          if (k == run - 2) commit(&sh.q_empty[0]);
+        }
+        ++q_used;
+      }
+    }
+  } else if (warp == kTreeThreads / 32 - 1) {
+    // ---- queries, rows in the order (token, head), rows behind the last one left as they are
+    for (uint32_t seg = 0; w.left > 0; ++seg, w.next(a)) {
+      const uint32_t buf = PAIR ? 0 : seg & 1, round = PAIR ? seg : seg >> 1;
+      if (round > 0 && !tree_wait(&sh.q_empty[buf], (round - 1) & 1, &sh.abort, most_iters, err)) break;
+      const int row0 = w.u % w.blocks * RU, rows = min(RU, w.x.n * a.G - row0), hk = w.u / w.blocks;
+      const int ch = lane % (D / 8);
+      for (int row = lane / (D / 8); row < rows; row += 32 / (D / 8)) {
+        const int i = (row0 + row) / a.G, g = (row0 + row) % a.G;
+        const uint16_t* p = q + ((size_t)(w.x.f + i) * a.Hq + (size_t)hk * a.G + g) * D + ch * 8;
+        unsigned char* to = sq + buf * kSlot + row / kTreeTile * kSlot + ch / 8 * kHalf + row % kTreeTile * 128 +
+                            (((ch & 7) ^ (row & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(p) : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) tree_arrive(&sh.q_full[buf]);
+    }
+  } else {
+    // ---- softmax: group gs, a row a thread
+    const int gs = (warp - kTreeSoftmax) >> 2, quarter = warp & 3;  // a warp reads the tensor memory lanes of its quarter
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_at = tmem + lanes + gs * kTreeTile, o_at = s_at + 2 * kTreeTile, o_other = tmem + lanes + 2 * kTreeTile + (1 - gs) * kTreeTile;
+    const uint32_t limit = wait_limit(err);
+    constexpr float kBelow = BF ? 0.f : 14.f, kAbove = BF ? 8.f : 15.f;  // of the reference: the largest weight, and what moves it
+    const float sc = a.scale2 == 0.f ? 1.f : fabsf(a.scale2), sgn = a.scale2 > 0.f ? 1.f : a.scale2 < 0.f ? -1.f : 0.f;
+    uint32_t at_tile = 0, s_seen = 0, o_seen = 0, half_seen = 0, free_seen = 0;
+    bool ok = true, lent = false, cut = false;  // lent: the other group still reads this one's O
+    for (uint32_t seg = 0; ok && w.left > 0; ++seg) {
+      const int run = w.run(), tile0 = w.tile, nt = w.nt, hk = w.u / w.blocks, block = w.u % w.blocks;
+      const TreeRequest x = w.x;
+      const int unit_r = w.r, unit_u = w.u, left = w.left;
+      const int rows_all = min(RU, x.n * a.G - block * RU);
+      const int my_row = PAIR ? gs * kTreeTile + row : row;  // in the unit
+      const bool live = my_row < rows_all, warp_live = my_row - lane < rows_all;
+      const int rr = block * RU + my_row, node = live ? rr / a.G : 0, head = live ? rr % a.G : 0;
+      const bool done = tile0 == 0 && run == nt;
+      cut = tile0 == 0 && !done;
+      w.next(a);
+      const unsigned long long mask = live ? __ldca(a.masks + x.f + node) : 0;
+      const int k0 = PAIR ? 0 : (int)((at_tile & 1) ^ (uint32_t)gs);  // this group's first tile of the run
+      if (k0 >= run || (PAIR && gs * kTreeTile >= rows_all)) {
+        at_tile += run;
+        continue;
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int k = k0; ok && k < run; k += PAIR ? 1 : 2) {
+        const uint32_t j = at_tile + k;  // tile of the CTA
+        ok = tree_wait(&sh.s_full[gs], s_seen++ & 1, &sh.abort, limit, err);
+        if (!ok) break;
+        tc_fence_after();
+        const int t0 = (tile0 + k) * kTreeTile, drafted = x.L - x.n;
+        const volatile uint32_t* va = sh.valid[j & 7];
+        const uint32_t valid[4] = {va[0], va[1], va[2], va[3]};
+        const bool plain = (valid[0] & valid[1] & valid[2] & valid[3]) == ~0u && t0 + kTreeTile <= drafted;
+        // 64 logits of the row, what it does not see as -inf
+        auto half_row = [&](uint32_t (&s)[64], int half) {
+          tm_ld64(s, s_at + 64 * half);
+          tm_wait_ld();
+          if (sgn != 1.f) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * sgn);
+          }
+          if (!plain) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t vis = valid[2 * half + c] & seen_bits(mask, t0 + 64 * half + 32 * c - drafted);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[32 * c + i] = vis >> i & 1 ? s[32 * c + i] : 0xff800000u;
+            }
+          }
+        };
+        if (warp_live) {
+          // the row's largest logit; the second half of the row stays in registers, the first is read again
+          uint32_t s[64];
+          float top = -INFINITY;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            half_row(s, half);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 64; ++i) mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(s[i]));
+            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+          }
+          top *= sc;
+          const bool move = live && top > m + kAbove;  // (from -inf on: whenever there is anything)
+          if (__any_sync(0xffffffffu, move)) {
+            const float to = move ? top - kBelow : m, f = move ? ex2(m - to) : 1.f;
+            m = to;
+            l *= f;
+            if (k > k0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tm_ld32(o, o_at + 32 * c);
+                tm_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tm_st32(o_at + 32 * c, o);
+              }
+            }
+          }
+          const float m0 = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int half = 1; half >= 0; --half) {  // weights over the logits of their half
+            if (half == 0) half_row(s, 0);
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              const float y0 = ex2(fmaf(__uint_as_float(s[i]), sc, -m0)), y1 = ex2(fmaf(__uint_as_float(s[i + 1]), sc, -m0));
+              sum[i / 2 % 4] += y0;
+              sum[i / 2 % 4] += y1;
+              p[i / 2] = pack2<BF>(y0, y1);
+            }
+            tm_st32(s_at + 64 * half, p);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tm_wait_st();
+        }
+        if (!plain && (!PAIR || gs == 0)) {
+          // values without a token are cleared, and what is not finite in drafted ones: a row of the tile a thread
+          const uint32_t vi = PAIR ? 2 * j + 1 : 2 * j + 2;
+          ok = tree_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.abort, most_iters, err);
+          if (!ok) break;
+          uint4* vr = reinterpret_cast<uint4*>(ring + vi % NS * kSlot + row * 128);
+          if (!(valid[quarter] >> lane & 1)) {
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) vr[c / 8 * (kHalf / 16) + c % 8] = make_uint4(0, 0, 0, 0);
+          } else if (t0 + row >= drafted) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 y = vr[c / 8 * (kHalf / 16) + c % 8];
+              odd |= odd_pair<BF>(y.x) | odd_pair<BF>(y.y) | odd_pair<BF>(y.z) | odd_pair<BF>(y.w);
+            }
+            if (odd) {
+              uint16_t* e = reinterpret_cast<uint16_t*>(vr);
+              for (int c = 0; c < D; ++c) {
+                uint16_t& y = e[c / 64 * (kHalf / 2) + c % 64];
+                if (odd_pair<BF>(y)) y = 0;
+              }
+              *(volatile int*)&sh.poison[seg & 3] = (int)seg + 1;
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (lent) {  // O is free again once the other group has taken what it needs
+          ok = tree_wait(&sh.o_free[gs], free_seen++ & 1, &sh.abort, most_iters, err);
+          if (!ok) break;
+          lent = false;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tree_arrive(&sh.p_full[gs]);
+      }
+      if (!ok) break;
+      // ---- the unit's end in this CTA
+      ok = tree_wait(&sh.o_done[gs], o_seen++ & 1, &sh.abort, most_iters, err);
+      if (!ok) break;
+      tc_fence_after();
+      const bool joined = !PAIR && run >= 2;
+      const int last_of = (int)((at_tile + run - 1) & 1);  // the group of the run's last tile writes
+      if (joined && gs != last_of) {
+        sh.ml[row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tree_arrive(&sh.half[gs]);
+        lent = true;
+        at_tile += run;
+        continue;
+      }
+      float f = 1.f, f2 = 0.f;
+      if (joined) {
+        ok = tree_wait(&sh.half[1 - gs], half_seen++ & 1, &sh.abort, most_iters, err);
+        if (!ok) break;
+        tc_fence_after();
+        const float2 y = sh.ml[row];
+        const float M = fmaxf(m, y.x), m0 = M == -INFINITY ? 0.f : M;
+        f = ex2(m - m0);
+        f2 = ex2(y.x - m0);
+        l = l * f + y.y * f2;
+        m = M;
+      }
+      const bool poisoned = *(volatile int*)&sh.poison[seg & 3] == (int)seg + 1;
+      const size_t at = live ? (size_t)(x.f + node) * a.Hq + (size_t)hk * a.G + head : 0;
+      // the unit it starts with, begun by an earlier CTA, to slot 0; one it begins to slot 1
+      float* wp = part + ((size_t)(2 * cta + (tile0 == 0 ? 1 : 0)) * RU + my_row) * (D + kTreePartHead);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (warp_live) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          __syncwarp();
+          tm_ld32(o, o_at + 32 * c);
+          if (joined) {
+            uint32_t o2[32];
+            tm_ld32(o2, o_other + 32 * c);
+            tm_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f + __uint_as_float(o2[i]) * f2);
+          } else {
+            tm_wait_ld();
+          }
+          if (poisoned && live) {
+            // drafted values that are not finite, of the tiles here: to the rows that see them
+            for (int d = 0; d < x.n; ++d) {
+              const int token = x.L - x.n + d;
+              if (!(mask >> d & 1) || token < tile0 * kTreeTile || token >= (tile0 + run) * kTreeTile) continue;
+              const int id = __ldca(a.table + (size_t)x.s * a.max_pages + token / a.page);
+              if (id < 0 || id >= a.n_pages) continue;
+              const uint16_t* vp = V + ((size_t)(id * a.Hkv + hk) * a.page + token % a.page) * D + 32 * c;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const uint16_t y = __ldca(vp + i);
+                if (odd_pair<BF>(y)) o[i] = __float_as_uint(__uint_as_float(o[i]) + to_float<BF>(y));
+              }
+            }
+          }
+          if (live && done) {
+            uint4* to = reinterpret_cast<uint4*>(out + at * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t h[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                h[y] = pack2<BF>(__uint_as_float(o[8 * i + 2 * y]) * inv, __uint_as_float(o[8 * i + 2 * y + 1]) * inv);
+              to[i] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          } else if (live) {
+            uint4* to = reinterpret_cast<uint4*>(wp + kTreePartHead + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (live) {
+          if (done) {
+            if (lse) lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+          } else {
+            *reinterpret_cast<float2*>(wp) = make_float2(m, l);
+          }
+        }
+      }
+      if (joined) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tree_arrive(&sh.o_free[1 - gs]);
+      }
+      // what the second kernel joins: a unit that begins here and goes on in later CTAs
+      if (cut && row == 0 && (!PAIR || gs == 0)) {
+        const int end = r1 - left + nt - 1;  // its last tile: a cut unit is this CTA's last, `left` tiles long here
+        int last = min(ctas - 1, (int)((float)end * ((float)ctas / (float)total)));  // within 1
+        while (last + 1 < ctas && first_of(last + 1) <= end) ++last;
+        while (first_of(last) > end) --last;
+        info[cta] = make_int4(unit_r, unit_u, last, 0);
+      }
+      at_tile += run;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // Where a wait ran out (only here, where every role is done, is it known), copies and products may be in flight: they end
+  // before the CTA gives back its shared and its tensor memory.
+  if (*(volatile int*)&sh.abort) {
+    if (warp == 0)
+      for (uint32_t x = it > NS ? it - NS : 0; x < it; ++x)
+        if (x != hole) mbar_wait_bounded(&sh.full[x % NS], (x / NS) & 1);
+    if (warp == 1) {
+      if (lane == 0) tree_commit(&sh.drain);
+      __syncwarp();
+      mbar_wait_bounded(&sh.drain, 0);
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTreeTmem));
+  }
+}
+
+// Joins the partials of the units that were cut: block (x, y) takes the unit that CTA x began and rows y * RB ... of it, WPR
+// warps a row; a warp takes every WPR-th partial in order, and the warps join in order.
+template <bool BF, int D, int WPR, int RB>
+__global__ void __launch_bounds__(WPR * RB * 32) k_tree_join(const float* __restrict__ part, const int4* __restrict__ info,
+                                                            const TreeShape a, int RU, uint16_t* __restrict__ out,
+                                                            float* __restrict__ lse) {
+  constexpr int VEC = D / 32;
+  __shared__ float sm[WPR * RB], sl[WPR * RB], so[WPR * RB][WPR > 1 ? D : 1];
+  pdl_trigger();
+  pdl_wait();
+  const int4 e = __ldca(info + blockIdx.x);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (e.x < 0) return;
+  const int c0 = blockIdx.x, n = e.z - c0 + 1;
+  const int f = __ldca(a.first + e.x), rows = (__ldca(a.first + e.x + 1) - f) * a.G, blocks = (rows + RU - 1) / RU;
+  const int hk = e.y / blocks, row = blockIdx.y * RB + warp / WPR, rr = e.y % blocks * RU + row;
+  const bool live = row < RU && rr < rows;
+  float m = -INFINITY, l = 0.f, o[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) o[i] = 0.f;
+  if (live) {
+    // this warp's partials are w0, w0 + WPR, ...: 32 references and sums at a time (one a lane), outputs U at a time,
+    // the first U on their way before the references are there
+    constexpr int U = 8;
+    const int w0 = warp % WPR, mine = (n - w0 + WPR - 1) / WPR;
+    auto at = [&](int i) -> const float* {
+      const int j = w0 + i * WPR;
+      return part + ((size_t)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * RU + row) * (D + kTreePartHead);
+    };
+    auto load = [&](int i0, float (&v)[U][VEC]) {
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+        if (i0 + x < mine) {
+          const float* p = at(i0 + x) + kTreePartHead + lane * VEC;
+          if constexpr (VEC == 4) {
+            const float4 y = __ldca(reinterpret_cast<const float4*>(p));
+            v[x][0] = y.x, v[x][1] = y.y, v[x][2] = y.z, v[x][3] = y.w;
+          } else {
+            const float2 y = __ldca(reinterpret_cast<const float2*>(p));
+            v[x][0] = y.x, v[x][1] = y.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[x][i] = 0.f;
+        }
+      }
+    };
+    float v[U][VEC];
+    for (int b0 = 0; b0 < mine; b0 += 32) {
+      load(b0, v);
+      const float2 h = b0 + lane < mine ? __ldca(reinterpret_cast<const float2*>(at(b0 + lane))) : make_float2(-INFINITY, 0.f);
+      float mx = h.x;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+      const float mn = fmaxf(m, mx), m0 = mn == -INFINITY ? 0.f : mn;
+      const float fo = ex2(m - m0), g = ex2(h.x - m0);
+      float sum = h.y * g;
+#pragma unroll
+      for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      l = l * fo + sum;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] *= fo;
+      m = mn;
+      for (int i0 = 0; i0 < 32 && b0 + i0 < mine; i0 += U) {
+        if (i0) load(b0 + i0, v);
+#pragma unroll
+        for (int x = 0; x < U; ++x) {
+          const float gx = __shfl_sync(0xffffffffu, g, i0 + x);
+          // (a partial past the end has weight 0 and values 0)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) o[i] = fmaf(v[x][i], gx, o[i]);
+        }
+      }
+    }
+  }
+  if constexpr (WPR > 1) {
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) so[warp][lane * VEC + i] = o[i];
+    __syncthreads();
+    if (warp % WPR) return;
+    m = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) m = fmaxf(m, sm[warp + x]);
+    const float m0 = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) {
+      const float fx = ex2(sm[warp + x] - m0);
+      l += sl[warp + x] * fx;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o[i] += so[warp + x][lane * VEC + i] * fx;
+    }
+  }
+  if (!live) return;
+  const size_t at = (size_t)(f + rr / a.G) * a.Hq + (size_t)hk * a.G + rr % a.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t h[VEC / 2];
+#pragma unroll
+  for (int i = 0; i < VEC / 2; ++i) h[i] = pack2<BF>(o[2 * i] * inv, o[2 * i + 1] * inv);
+  if constexpr (VEC == 4) *reinterpret_cast<uint2*>(out + at * D + lane * VEC) = make_uint2(h[0], h[1]);
+  else *reinterpret_cast<uint32_t*>(out + at * D + lane * VEC) = h[0];
+  if (lse && lane == 0) lse[at] = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// rows of a unit
+inline int tree_rows(int T_max, int G) { return (long long)T_max * G > kTreeTile ? 2 * kTreeTile : kTreeTile; }
+
+// workspace: two partials per CTA, then the join's list
+inline size_t tree_part_bytes(int rows, int d) {
+  return round_up((size_t)2 * kMaxTreeCtas * rows * (d + kTreePartHead) * sizeof(float), 256);
+}
+
+template <bool BF, int D, bool PAIR>
 ig_status launch_tree(cudaStream_t st, const TreeShape& a, const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out,
                       float* lse, void* ws) {
-  k_tree_simple<BF, D><<<dim3((unsigned)a.T, (unsigned)a.Hkv), 128, 0, st>>>(q, K, V, a, out, lse, error_word());
+  constexpr int RU = PAIR ? 2 * kTreeTile : kTreeTile;
+  const long long tiles = ((long long)a.max_pages * a.page + kTreeTile - 1) / kTreeTile;
+  const long long blocks = ((long long)a.T_max * a.G + RU - 1) / RU;
+  const double most = (double)a.B * a.Hkv * blocks * tiles;
+  IG_REQUIRE(most < 2147483648.0, "n*max_pages*page*Hq is too large: %.0f tiles", most);
+  int box = kTreeTile;
+  while (a.page % box) box >>= 1;
+  CUtensorMap mk, mv;
+  ig_status r = make_map(&mk, K, a.n_pages * a.Hkv * a.page, D, box);
+  if (r == IG_OK) r = make_map(&mv, V, a.n_pages * a.Hkv * a.page, D, box);
+  if (r != IG_OK) return r;
+  constexpr size_t smem = tree_smem<D>();
+  cudaError_t e = cudaFuncSetAttribute(k_tree_attend<BF, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention smem attribute");
+  int grid = sm_count(st);
+  if (grid > kMaxTreeCtas) grid = kMaxTreeCtas;
+  if (grid > most) grid = (int)most;
+  float* part = static_cast<float*>(ws);
+  int4* info = reinterpret_cast<int4*>(static_cast<char*>(ws) + tree_part_bytes(RU, D));
+  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, out, lse, part, info,
+                 error_word());
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   IG_CHECK_LAUNCH("tree attention launch");
+  if (grid == 1 || ((double)a.B * a.Hkv * blocks <= grid && tiles <= kTreeWhole)) return IG_OK;  // nothing can have been cut
+  const int rows = (long long)a.T_max * a.G < RU ? a.T_max * a.G : RU;
+  const float* cpart = part;
+  const int4* cinfo = info;
+  const double partials = grid / ((double)a.B * a.Hkv * blocks);  // of a unit, about
+#define IG_TJ(WPR, RB)                                                                                                     \
+  e = launch_pdl(k_tree_join<BF, D, WPR, RB>, dim3(grid, (rows + RB - 1) / RB), dim3(WPR * RB * 32), 0, st, cpart, cinfo, a, RU, out, \
+                 lse)
+  if (partials >= 16) IG_TJ(4, 1);
+  else IG_TJ(1, 4);
+#undef IG_TJ
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention join launch");
+  IG_CHECK_LAUNCH("tree attention join launch");
   return IG_OK;
+}
+
+template <bool BF, int D>
+ig_status launch_rows(cudaStream_t st, const TreeShape& a, const uint16_t* q, const uint16_t* K, const uint16_t* V, uint16_t* out,
+                      float* lse, void* ws) {
+  return tree_rows(a.T_max, a.G) == kTreeTile ? launch_tree<BF, D, false>(st, a, q, K, V, out, lse, ws)
+                                              : launch_tree<BF, D, true>(st, a, q, K, V, out, lse, ws);
 }
 
 }  // namespace
@@ -128,7 +1010,7 @@ using namespace ig;
 
 extern "C" size_t ig_paged_tree_attend_workspace_bytes(int n, int T_max, int Hq, int Hkv, int d) {
   if (n <= 0 || T_max <= 0 || T_max > kTreeMost || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (d != 64 && d != 128)) return 0;
-  return 256;
+  return tree_part_bytes(tree_rows(T_max, Hq / Hkv), d) + round_up(kMaxTreeCtas * sizeof(int4), 256);
 }
 
 extern "C" ig_status ig_paged_tree_attend(void* stream, int dtype, int n, int T, int T_max, int Hq, int Hkv, int d, int page,
@@ -164,8 +1046,8 @@ extern "C" ig_status ig_paged_tree_attend(void* stream, int dtype, int n, int T,
                     seq, first, reinterpret_cast<const unsigned long long*>(masks)};
   cudaStream_t st = as_stream(stream);
   if (dtype == IG_F16)
-    return d == 128 ? launch_tree<false, 128>(st, a, q, K, V, out, lse, workspace)
-                    : launch_tree<false, 64>(st, a, q, K, V, out, lse, workspace);
-  return d == 128 ? launch_tree<true, 128>(st, a, q, K, V, out, lse, workspace)
-                  : launch_tree<true, 64>(st, a, q, K, V, out, lse, workspace);
+    return d == 128 ? launch_rows<false, 128>(st, a, q, K, V, out, lse, workspace)
+                    : launch_rows<false, 64>(st, a, q, K, V, out, lse, workspace);
+  return d == 128 ? launch_rows<true, 128>(st, a, q, K, V, out, lse, workspace)
+                  : launch_rows<true, 64>(st, a, q, K, V, out, lse, workspace);
 }

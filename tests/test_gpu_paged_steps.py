@@ -1005,3 +1005,27 @@ def test_cache_refuses_what_cannot_be_drafted_or_kept(ig):
             call()
     cache.close()
 
+
+
+@pytest.mark.parametrize("limit", [0, 1, 2, 7])
+@pytest.mark.parametrize("n,lengths", [(1, [100, 5]), (16, [100, 300]), (16, [20000, 40]), (64, [3000, 100]), (64, [64, 64])])
+def test_tree_short_waits_are_reported_and_leave_the_next_call_right(ig, limit, n, lengths):
+    """Short wait limits: the call ends by itself, its copies and products ended, ig_check names it, and the next one is right."""
+    c = make_tree(20, "bf16", lengths, [n, 1], 12, 2, 128, 16)
+    want = attend_tree(ig, c)
+    ig.ig_check()
+    ig.ig_set_wait_limit(limit)
+    try:
+        for _ in range(3):
+            attend_tree(ig, c)
+        try:
+            ig.ig_check()
+            assert limit > 0  # logits may be there at the first probe
+        except ig.IGError as e:
+            assert e.status == ig.IG_ERR_TIMEOUT
+    finally:
+        ig.ig_set_wait_limit(-1)
+    got = attend_tree(ig, c)
+    ig.ig_check()
+    check_tree(c, *got)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
