@@ -133,22 +133,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t addr) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tm_ld64(uint32_t (&r)[64], uint32_t addr) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(addr));
-}
 __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -157,6 +141,13 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) 
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
       "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
       "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -168,17 +159,17 @@ __device__ __forceinline__ void tree_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// A bounded wait that ends together with the CTA's other waits; one verdict for the warp.
-__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit, int* err) {
+// A bounded wait that ends together with the CTA's other waits; one verdict for the warp.  What is there already costs one look.
+__device__ __noinline__ bool tree_wait_on(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit, int* err) {
   bool ok = false;
-  for (uint32_t i = 0; i < limit && !*abort; ++i)
-    if (mbar_try_wait(bar, parity)) {
-      ok = true;
-      break;
-    }
+  for (uint32_t i = 0; i < limit && !*abort && !ok; ++i) ok = mbar_try_wait(bar, parity);
   ok = __all_sync(0xffffffffu, ok);
   if (!ok && (threadIdx.x & 31) == 0 && !atomicExch(const_cast<int*>(abort), 1)) raise_error(err, IG_DEVERR_TIMEOUT);
   return ok;
+}
+__device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit, int* err) {
+  if (limit > 0 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return tree_wait_on(bar, parity, abort, limit, err);
 }
 
 // The units of a CTA's share, in order: of each request its key heads, of each key head its blocks of rows.
@@ -445,15 +436,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     };
     // S of group g from queries at qa and the keys in slot idx
     auto logits = [&](int g, uint32_t qa, uint32_t idx) {
-      const uint32_t kb = smem_addr(ring + idx % NS * kSlot);
       if (issuer) {
-#pragma unroll
+        const uint64_t ad = sw128_desc(qa), bd = sw128_desc(smem_addr(ring + idx % NS * kSlot));
+#pragma unroll 1
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks / 4) * kHalf + (ks % 4) * 32;
+          const uint32_t o = (ks / 4) * (kHalf >> 4) + (ks % 4) * 2;
           asm volatile(
               "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
                   tmem + g * kTreeTile),
-              "l"(sw128_desc(qa + o)), "l"(sw128_desc(kb + o)), "r"(kIdS), "r"(ks > 0 ? 1u : 0u));
+              "l"(ad + o), "l"(bd + o), "r"(kIdS), "r"(ks));
         }
         tree_commit(&sh.s_full[g]);
       }
@@ -461,15 +452,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     };
     // O of group g, from its weights and the values in slot idx
     auto values = [&](int g, uint32_t idx, bool more) {
-      const uint32_t vb = smem_addr(ring + idx % NS * kSlot);
       if (issuer) {
-#pragma unroll
+        const uint64_t bd = sw128_desc_mn(smem_addr(ring + idx % NS * kSlot), kHalf);
+#pragma unroll 1
         for (int ks = 0; ks < kTreeTile / 16; ++ks)
           asm volatile(
               "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
                   tmem + 2 * kTreeTile + g * kTreeTile),
-              "r"(tmem + g * kTreeTile + ks / 4 * 64 + ks % 4 * 8), "l"(sw128_desc_mn(vb + ks * 2048, kHalf)), "r"(kIdO),
-              "r"(more || ks > 0 ? 1u : 0u));
+              "r"(tmem + g * kTreeTile + ks * 8), "l"(bd + ks * 128), "r"(kIdO), "r"((uint32_t)more | (uint32_t)ks));
       }
       __syncwarp();
     };
@@ -486,35 +476,41 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       // logits of a tile ahead of the values of the one before; tile i is of group i & 1
       uint32_t i = 0;             // tile whose logits are next
       int seg_run = w.left > 0 ? w.run() : 0, seg_at = 0;
-      auto ahead = [&]() -> bool {  // the next tile's logits
-        const uint32_t buf = q_used & 1;
-        if (seg_at == 0 && !tree_wait(&sh.q_full[buf], (q_used >> 1) & 1, &sh.abort, most_iters, err)) return false;
-        const uint32_t idx = i == 0 ? 0 : 2 * i - 1;
-        if (!full(idx)) return false;
-        logits(i & 1, smem_addr(sq + buf * kSlot), idx);
-        commit(&sh.empty[idx % NS]);
-        ++i;
-        if (++seg_at == seg_run) {
-          commit(&sh.q_empty[buf]);
-          ++q_used;
-          w.next(a);
-          seg_at = 0;
-          seg_run = w.left > 0 ? w.run() : 0;
-        }
-        return true;
-      };
-      TreeWalk v = w;  // of the values
-      if (w.left > 0) ok = ahead();
-      for (uint32_t j = 0; ok && v.left > 0; v.next(a)) {
-        const int run = v.run();
-        for (int k = 0; k < run && ok; ++k, ++j) {
-          if (w.left > 0) ok = ahead();
-          const uint32_t idx = 2 * j + 2;
-          ok = ok && weights(j & 1) && full(idx);
+      TreeWalk v = w;             // of the values
+      uint32_t j = 0;
+      int run = v.left > 0 ? v.run() : 0, k = 0;
+      for (bool first = true; ok && v.left > 0;) {
+        if (w.left > 0) {  // the next tile's logits
+          const uint32_t buf = q_used & 1, idx = i == 0 ? 0 : 2 * i - 1;
+          if (seg_at == 0) ok = tree_wait(&sh.q_full[buf], (q_used >> 1) & 1, &sh.abort, most_iters, err);
+          ok = ok && full(idx);
           if (!ok) break;
-          values(j & 1, idx, k >= 2);
+          logits(i & 1, smem_addr(sq + buf * kSlot), idx);
           commit(&sh.empty[idx % NS]);
-          if (k >= run - 2) commit(&sh.o_done[j & 1]);
+          ++i;
+          if (++seg_at == seg_run) {
+            commit(&sh.q_empty[buf]);
+            ++q_used;
+            w.next(a);
+            seg_at = 0;
+            seg_run = w.left > 0 ? w.run() : 0;
+          }
+        }
+        if (first) {
+          first = false;
+          continue;
+        }
+        const uint32_t idx = 2 * j + 2;
+        ok = weights(j & 1) && full(idx);
+        if (!ok) break;
+        values(j & 1, idx, k >= 2);
+        commit(&sh.empty[idx % NS]);
+        if (k >= run - 2) commit(&sh.o_done[j & 1]);
+        ++j;
+        if (++k == run) {
+          v.next(a);
+          k = 0;
+          run = v.left > 0 ? v.run() : 0;
         }
       }
     } else {
@@ -609,35 +605,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         tc_fence_after();
         const int t0 = (tile0 + k) * kTreeTile, drafted = x.L - x.n;
         const volatile uint32_t* va = sh.valid[j & 7];
-        const uint32_t valid[4] = {va[0], va[1], va[2], va[3]};
-        const bool plain = (valid[0] & valid[1] & valid[2] & valid[3]) == ~0u && t0 + kTreeTile <= drafted;
-        // 64 logits of the row, what it does not see as -inf
-        auto half_row = [&](uint32_t (&s)[64], int half) {
-          tm_ld64(s, s_at + 64 * half);
-          tm_wait_ld();
-          if (sgn != 1.f) {
+        const bool plain = (va[0] & va[1] & va[2] & va[3]) == ~0u && t0 + kTreeTile <= drafted;
+        if (warp_live && (!plain || sgn != 1.f)) {  // the row's logits put right where they are: what it does not see is -inf
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t vis = va[c] & seen_bits(mask, t0 + 32 * c - drafted);
+            uint32_t y[32];
+            tm_ld32(y, s_at + 32 * c);
+            tm_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * sgn);
+            for (int i = 0; i < 32; ++i) y[i] = vis >> i & 1 ? __float_as_uint(__uint_as_float(y[i]) * sgn) : 0xff800000u;
+            tm_st32(s_at + 32 * c, y);
           }
-          if (!plain) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t vis = valid[2 * half + c] & seen_bits(mask, t0 + 64 * half + 32 * c - drafted);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s[32 * c + i] = vis >> i & 1 ? s[32 * c + i] : 0xff800000u;
-            }
-          }
-        };
+          tm_wait_st();
+        }
         if (warp_live) {
-          // the row's largest logit; the second half of the row stays in registers, the first is read again
-          uint32_t s[64];
+          // (Loops over 32 logits at a time, read twice, keep the code small: unrolled over the row, all roles' code is more
+          // than the instruction caches hold, and every instruction takes several times as long.)
           float top = -INFINITY;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            half_row(s, half);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            tm_ld32(y, s_at + 32 * c);
+            tm_wait_ld();
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 64; ++i) mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(s[i]));
+            for (int i = 0; i < 32; ++i) mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(y[i]));
             top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
           }
           top *= sc;
@@ -647,7 +640,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
             m = to;
             l *= f;
             if (k > k0) {
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tm_ld32(o, o_at + 32 * c);
@@ -660,18 +653,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           }
           const float m0 = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {  // weights go where logits were that have been read
+            uint32_t y[32], p[16];
+            tm_ld32(y, s_at + 32 * c);
+            tm_wait_ld();
 #pragma unroll
-          for (int half = 1; half >= 0; --half) {  // weights over the logits of their half
-            if (half == 0) half_row(s, 0);
-            uint32_t p[32];
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              const float y0 = ex2(fmaf(__uint_as_float(s[i]), sc, -m0)), y1 = ex2(fmaf(__uint_as_float(s[i + 1]), sc, -m0));
+            for (int i = 0; i < 32; i += 2) {
+              const float y0 = ex2(fmaf(__uint_as_float(y[i]), sc, -m0)), y1 = ex2(fmaf(__uint_as_float(y[i + 1]), sc, -m0));
               sum[i / 2 % 4] += y0;
               sum[i / 2 % 4] += y1;
               p[i / 2] = pack2<BF>(y0, y1);
             }
-            tm_st32(s_at + 64 * half, p);
+            tm_st16(s_at + 16 * c, p);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tm_wait_st();
@@ -682,7 +676,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           ok = tree_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.abort, most_iters, err);
           if (!ok) break;
           uint4* vr = reinterpret_cast<uint4*>(ring + vi % NS * kSlot + row * 128);
-          if (!(valid[quarter] >> lane & 1)) {
+          if (!(va[quarter] >> lane & 1)) {
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) vr[c / 8 * (kHalf / 16) + c % 8] = make_uint4(0, 0, 0, 0);
           } else if (t0 + row >= drafted) {
@@ -746,7 +740,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       float* wp = part + ((size_t)(2 * cta + (tile0 == 0 ? 1 : 0)) * RU + my_row) * (D + kTreePartHead);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (warp_live) {
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           __syncwarp();
