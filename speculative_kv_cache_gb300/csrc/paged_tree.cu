@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     auto logits = [&](int g, uint32_t qa, uint32_t idx) {
       if (issuer) {
         const uint64_t ad = sw128_desc(qa), bd = sw128_desc(smem_addr(ring + idx % NS * kSlot));
-#pragma unroll 1
+#pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t o = (ks / 4) * (kHalf >> 4) + (ks % 4) * 2;
           asm volatile(
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     auto values = [&](int g, uint32_t idx, bool more) {
       if (issuer) {
         const uint64_t bd = sw128_desc_mn(smem_addr(ring + idx % NS * kSlot), kHalf);
-#pragma unroll 1
+#pragma unroll
         for (int ks = 0; ks < kTreeTile / 16; ++ks)
           asm volatile(
               "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
@@ -514,40 +514,32 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         }
       }
     } else {
+      // a tile's values and the next tile's logits, group by group; a unit begins with logits alone
       uint32_t j = 0;
-      const uint32_t qa = smem_addr(sq), qb = qa + kSlot;
       for (; ok && w.left > 0; w.next(a)) {
-        const int run = w.run(), rows = w.x.n * a.G - w.u % w.blocks * RU;
-        const bool two = rows > kTreeTile;
-        ok = tree_wait(&sh.q_full[0], q_used & 1, &sh.abort, most_iters, err) && full(2 * j);
-        if (!ok) break;
-        logits(0, qa, 2 * j);
-        if (two) logits(1, qb, 2 * j);
-        commit(&sh.empty[2 * j % NS]);
-        if (run == 1) commit(&sh.q_empty[0]);
-        for (int k = 0; k < run && ok; ++k, ++j) {
-          const uint32_t vi = 2 * j + 1, ki = 2 * j + 2;
-          ok = weights(0) && full(vi);
+        const int run = w.run(), groups = w.x.n * a.G - w.u % w.blocks * RU > kTreeTile ? 2 : 1;
+        ok = tree_wait(&sh.q_full[0], q_used++ & 1, &sh.abort, most_iters, err);
+        for (int k = -1; k < run && ok; ++k) {
+          const uint32_t vi = 2 * (j + k) + 1, ki = vi + 1;
+          for (int g = 0; g < groups && ok; ++g) {
+            if (k >= 0) {
+              ok = weights(g) && (g > 0 || full(vi));
+              if (!ok) break;
+              values(g, vi, k > 0);
+              if (k == run - 1) commit(&sh.o_done[g]);
+            }
+            if (k < run - 1) {
+              ok = g > 0 || full(ki);
+              if (!ok) break;
+              logits(g, smem_addr(sq) + g * kSlot, ki);
+            }
+          }
           if (!ok) break;
-          values(0, vi, k > 0);
-          if (k == run - 1) commit(&sh.o_done[0]);
-          if (k < run - 1) {
-            ok = full(ki);
-            if (!ok) break;
-            logits(0, qa, ki);
-          }
-          if (two) {
-            ok = weights(1);
-            if (!ok) break;
-            values(1, vi, k > 0);
-            if (k == run - 1) commit(&sh.o_done[1]);
-            if (k < run - 1) logits(1, qb, ki);
-          }
-          commit(&sh.empty[vi % NS]);
+          if (k >= 0) commit(&sh.empty[vi % NS]);
           if (k < run - 1) commit(&sh.empty[ki % NS]);
           if (k == run - 2) commit(&sh.q_empty[0]);
         }
-        ++q_used;
+        j += run;
       }
     }
   } else if (warp == kTreeThreads / 32 - 1) {
