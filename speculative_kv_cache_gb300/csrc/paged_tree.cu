@@ -76,8 +76,8 @@ __device__ __forceinline__ uint16_t from_float(float v) {
 }
 
 constexpr int kTreeTile = 128;                 // tokens of a tile, rows of a block
-constexpr int kTreeThreads = 352;              // warps: 0 TMA, 1 MMA, 2 .. 9 softmax, 10 queries
-constexpr int kTreeSoftmax = 2;                // first softmax warp
+constexpr int kTreeThreads = 352;              // warps: 0 TMA, 1 MMAs, 2 .. 9 softmax, 10 queries
+constexpr int kTreeSoftmax = 2, kTreeQueries = 10;
 constexpr int kMaxTreeCtas = 160;              // upper bound of the grid (sizes the workspace)
 constexpr int kTreePartHead = 4;               // a partial: [m, l, -, -, o[D]]
 constexpr uint32_t kTreeTmem = 512;            // columns: S of either group, then O of either
@@ -92,15 +92,18 @@ template <int D>
 __host__ __device__ constexpr uint32_t tree_slot_bytes() { return kTreeTile * D * 2; }
 
 struct TreeShared {
-  uint64_t full[8], empty[8];       // the ring's slots
+  // A tile's keys and values are there (by tile, as the groups each see every other tile of SPLIT, and a barrier's phases
+  // can be told by their parity only by one that follows them all); a slot of the ring is free.
+  uint64_t k_full[8], v_full[8], empty[8];
   uint64_t s_full[2], p_full[2];    // a group's logits are there, its weights are
   uint64_t o_done[2];               // its last product of a unit
   uint64_t q_full[2], q_empty[2];   // queries
   uint64_t half[2], o_free[2];      // a group's part of a unit is there for the other, has been taken
+  uint64_t clean[8];                // a tile's values, which both groups use, hold nothing that they must not
   uint64_t drain;
   uint32_t valid[8][4];             // tokens of a tile that hold anything
   float2 ml[kTreeTile];
-  int poison[4];                    // by unit: 1 + its number, if it has drafted values that are not finite
+  int poison[8];                    // by unit: 1 + its number, if it has drafted values that are not finite
   int scan[kTreeThreads / 32][3];
   uint32_t tmem;
   int start_r, start_off, abort;
@@ -150,6 +153,17 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) 
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// Waits for the loads, and ties their registers to the wait.
+__device__ __forceinline__ void tm_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tree_commit(uint64_t* bar) {
@@ -170,6 +184,17 @@ __device__ __noinline__ bool tree_wait_on(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit, int* err) {
   if (limit > 0 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return tree_wait_on(bar, parity, abort, limit, err);
+}
+
+// The same by one thread.
+__device__ __noinline__ bool tree_wait1_on(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  for (uint32_t i = 0; i < (uint32_t)kDefaultWaitIters && !*abort; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  if (!atomicExch(const_cast<int*>(abort), 1)) raise_error(err, IG_DEVERR_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool tree_wait1(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
+  return mbar_try_wait(bar, parity) || tree_wait1_on(bar, parity, abort, err);
 }
 
 // The units of a CTA's share, in order: of each request its key heads, of each key head its blocks of rows.
@@ -252,9 +277,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   TreeShared& sh = *reinterpret_cast<TreeShared*>(ring + NS * kSlot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&sh.full[i], 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.v_full[i], 1);
       mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.clean[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
@@ -266,7 +293,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       mbar_init(&sh.o_free[i], 4);
     }
     mbar_init(&sh.drain, 1);
-    for (int i = 0; i < 4; ++i) sh.poison[i] = 0;
+    for (int i = 0; i < 8; ++i) sh.poison[i] = 0;
     sh.abort = 0;
     fence_mbar_init();
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -348,7 +375,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   __syncthreads();
   w.start(a, sh.start_r, sh.start_off, r1 - r0);
   const uint32_t most_iters = (uint32_t)kDefaultWaitIters;
-  uint32_t it = 0, hole = ~0u;  // the producer's ring: slots filled, and one left out
+  uint32_t it = 0, k_sent = 0, v_sent = 0;  // the producer's slots; tiles whose keys and values it has sent for
 
   if (warp == 0) {
     // ---- tiles.  Lane i moves box i / halves, half i % halves; a page's number is read two tiles ahead of its keys.
@@ -376,10 +403,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       }
       return t;
     };
-    uint32_t tile = 0;
     // a tile's keys or values into the ring's next slot; false when the CTA gives up
     auto load = [&](const Tile& t, bool values) -> bool {
       const uint32_t st = it % NS;
+      uint64_t* bar = values ? &sh.v_full[v_sent & 7] : &sh.k_full[k_sent & 7];
       if (it >= NS && !tree_wait(&sh.empty[st], (it / NS - 1) & 1, &sh.abort, most_iters, err)) return false;
       const int token = t.token0 + box_at;
       const bool want = box_at < kTreeTile && token < t.L, ok = want && t.id >= 0 && t.id < a.n_pages;
@@ -398,16 +425,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sh.valid[tile & 7][i] = v[i];
+          for (int i = 0; i < 4; ++i) sh.valid[k_sent & 7][i] = v[i];
         }
-        mbar_arrive_expect_tx(&sh.full[st], (uint32_t)__popc(moving) * box_bytes);
+        mbar_arrive_expect_tx(bar, (uint32_t)__popc(moving) * box_bytes);
       }
       __syncwarp();
       if (ok)
         tma_load_2d(ring + st * kSlot + col * kHalf + box_at * 128, values ? &map_v : &map_k, col * 64,
-                    (t.id * a.Hkv + t.hk) * a.page + token % a.page, &sh.full[st]);
+                    (t.id * a.Hkv + t.hk) * a.page + token % a.page, bar);
       ++it;
-      if (!values) ++tile;
+      if (values) ++v_sent;
+      else ++k_sent;
       return true;
     };
     Tile t0 = fetch(), t1 = fetch();
@@ -418,26 +446,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         going = load(t0, true) && (!t1.is || load(t1, false));
       } else {
         if (t1.is) going = load(t1, false);
-        else hole = it++;
+        else ++it;  // (a slot left out keeps the order)
         going = going && load(t0, true);
       }
       t0 = t1;
       t1 = t2;
     }
   } else if (warp == 1) {
-    // ---- the MMAs.  One thread issues them; the warp walks and waits together.
-    uint32_t q_used = 0, p_seen[2] = {0, 0};
-    bool ok = true;
-    const bool issuer = lane == 0;
-    auto full = [&](uint32_t idx) -> bool {
-      const bool f = tree_wait(&sh.full[idx % NS], (idx / NS) & 1, &sh.abort, most_iters, err);
-      tc_fence_after();
-      return f;
-    };
-    // S of group g from queries at qa and the keys in slot idx
-    auto logits = [&](int g, uint32_t qa, uint32_t idx) {
-      if (issuer) {
+    // ---- the MMAs, by one thread.  (Two, one a group: 158 -> 190 us for two trees of 64 tokens on 65536.)
+    if (lane == 0) {
+      uint32_t p_seen[2] = {0, 0};
+      bool ok = true;
+      auto full = [&](uint64_t* bars, uint32_t tile) -> bool { return tree_wait1(&bars[tile & 7], tile >> 3 & 1, &sh.abort, err); };
+      // S of group g from queries at qa and the keys in slot idx
+      auto logits = [&](int g, uint32_t qa, uint32_t idx) {
         const uint64_t ad = sw128_desc(qa), bd = sw128_desc(smem_addr(ring + idx % NS * kSlot));
+        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t o = (ks / 4) * (kHalf >> 4) + (ks % 4) * 2;
@@ -447,102 +471,91 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
               "l"(ad + o), "l"(bd + o), "r"(kIdS), "r"(ks));
         }
         tree_commit(&sh.s_full[g]);
-      }
-      __syncwarp();
-    };
-    // O of group g, from its weights and the values in slot idx
-    auto values = [&](int g, uint32_t idx, bool more) {
-      if (issuer) {
+      };
+      // O of group g, from its weights and the values in slot idx
+      auto values = [&](int g, uint32_t idx, bool more) {
         const uint64_t bd = sw128_desc_mn(smem_addr(ring + idx % NS * kSlot), kHalf);
+        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < kTreeTile / 16; ++ks)
           asm volatile(
               "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
                   tmem + 2 * kTreeTile + g * kTreeTile),
               "r"(tmem + g * kTreeTile + ks * 8), "l"(bd + ks * 128), "r"(kIdO), "r"((uint32_t)more | (uint32_t)ks));
-      }
-      __syncwarp();
-    };
-    auto commit = [&](uint64_t* bar) {
-      if (issuer) tree_commit(bar);
-      __syncwarp();
-    };
-    auto weights = [&](int g) -> bool {
-      const bool f = tree_wait(&sh.p_full[g], p_seen[g]++ & 1, &sh.abort, most_iters, err);
-      tc_fence_after();
-      return f;
-    };
-    if constexpr (!PAIR) {
-      // logits of a tile ahead of the values of the one before; tile i is of group i & 1
-      uint32_t i = 0;             // tile whose logits are next
-      int seg_run = w.left > 0 ? w.run() : 0, seg_at = 0;
-      TreeWalk v = w;             // of the values
-      uint32_t j = 0;
-      int run = v.left > 0 ? v.run() : 0, k = 0;
-      for (bool first = true; ok && v.left > 0;) {
-        if (w.left > 0) {  // the next tile's logits
-          const uint32_t buf = q_used & 1, idx = i == 0 ? 0 : 2 * i - 1;
-          if (seg_at == 0) ok = tree_wait(&sh.q_full[buf], (q_used >> 1) & 1, &sh.abort, most_iters, err);
-          ok = ok && full(idx);
-          if (!ok) break;
-          logits(i & 1, smem_addr(sq + buf * kSlot), idx);
-          commit(&sh.empty[idx % NS]);
-          ++i;
-          if (++seg_at == seg_run) {
-            commit(&sh.q_empty[buf]);
-            ++q_used;
-            w.next(a);
-            seg_at = 0;
-            seg_run = w.left > 0 ? w.run() : 0;
-          }
-        }
-        if (first) {
-          first = false;
-          continue;
-        }
-        const uint32_t idx = 2 * j + 2;
-        ok = weights(j & 1) && full(idx);
-        if (!ok) break;
-        values(j & 1, idx, k >= 2);
-        commit(&sh.empty[idx % NS]);
-        if (k >= run - 2) commit(&sh.o_done[j & 1]);
-        ++j;
-        if (++k == run) {
-          v.next(a);
-          k = 0;
-          run = v.left > 0 ? v.run() : 0;
-        }
-      }
-    } else {
-      // a tile's values and the next tile's logits, group by group; a unit begins with logits alone
-      uint32_t j = 0;
-      for (; ok && w.left > 0; w.next(a)) {
-        const int run = w.run(), groups = w.x.n * a.G - w.u % w.blocks * RU > kTreeTile ? 2 : 1;
-        ok = tree_wait(&sh.q_full[0], q_used++ & 1, &sh.abort, most_iters, err);
-        for (int k = -1; k < run && ok; ++k) {
-          const uint32_t vi = 2 * (j + k) + 1, ki = vi + 1;
-          for (int g = 0; g < groups && ok; ++g) {
-            if (k >= 0) {
-              ok = weights(g) && (g > 0 || full(vi));
-              if (!ok) break;
-              values(g, vi, k > 0);
-              if (k == run - 1) commit(&sh.o_done[g]);
-            }
-            if (k < run - 1) {
-              ok = g > 0 || full(ki);
-              if (!ok) break;
-              logits(g, smem_addr(sq) + g * kSlot, ki);
+      };
+      auto weights = [&](int g) -> bool { return tree_wait1(&sh.p_full[g], p_seen[g]++ & 1, &sh.abort, err); };
+      if constexpr (!PAIR) {
+        // logits of a tile ahead of the values of the one before; tile i is of group i & 1
+        uint32_t i = 0, seg = 0;    // tile whose logits are next, and its unit
+        TreeWalk v = w;             // of the values
+        uint32_t j = 0;
+        int seg_run = w.left > 0 ? w.run() : 0, seg_at = 0, run = seg_run, k = 0;
+        for (bool first = true; ok && v.left > 0;) {
+          if (w.left > 0) {  // the next tile's logits
+            const uint32_t buf = seg & 1, idx = i == 0 ? 0 : 2 * i - 1;
+            if (seg_at == 0) ok = tree_wait1(&sh.q_full[buf], seg >> 1 & 1, &sh.abort, err);
+            ok = ok && full(sh.k_full, i);
+            if (!ok) break;
+            logits(i & 1, smem_addr(sq + buf * kSlot), idx);
+            tree_commit(&sh.empty[idx % NS]);
+            ++i;
+            if (++seg_at == seg_run) {
+              tree_commit(&sh.q_empty[buf]);
+              ++seg;
+              w.next(a);
+              seg_at = 0;
+              seg_run = w.left > 0 ? w.run() : 0;
             }
           }
+          if (first) {
+            first = false;
+            continue;
+          }
+          const uint32_t idx = 2 * j + 2;
+          ok = full(sh.v_full, j) && weights(j & 1);
           if (!ok) break;
-          if (k >= 0) commit(&sh.empty[vi % NS]);
-          if (k < run - 1) commit(&sh.empty[ki % NS]);
-          if (k == run - 2) commit(&sh.q_empty[0]);
+          values(j & 1, idx, k >= 2);
+          tree_commit(&sh.empty[idx % NS]);
+          if (k >= run - 2) tree_commit(&sh.o_done[j & 1]);
+          ++j;
+          if (++k == run) {
+            v.next(a);
+            k = 0;
+            run = v.left > 0 ? v.run() : 0;
+          }
         }
-        j += run;
+      } else {
+        // a tile's values and the next tile's logits, group by group; a unit begins with logits alone
+        uint32_t j = 0;
+        for (uint32_t seg = 0; ok && w.left > 0; w.next(a), ++seg) {
+          const int run = w.run(), groups = w.x.n * a.G - w.u % w.blocks * RU > kTreeTile ? 2 : 1;
+          ok = tree_wait1(&sh.q_full[0], seg & 1, &sh.abort, err);
+          for (int k = -1; k < run && ok; ++k) {
+            const uint32_t vi = 2 * (j + k) + 1, ki = vi + 1;
+            for (int g = 0; g < groups && ok; ++g) {
+              if (k >= 0) {
+                ok = (g > 0 || full(sh.v_full, j + k)) && weights(g);
+                if (!ok) break;
+                values(g, vi, k > 0);
+                if (k == run - 1) tree_commit(&sh.o_done[g]);
+              }
+              if (k < run - 1) {
+                ok = g > 0 || full(sh.k_full, j + k + 1);
+                if (!ok) break;
+                logits(g, smem_addr(sq) + g * kSlot, ki);
+              }
+            }
+            if (!ok) break;
+            if (k >= 0) tree_commit(&sh.empty[vi % NS]);
+            if (k < run - 1) tree_commit(&sh.empty[ki % NS]);
+            if (k == run - 2) tree_commit(&sh.q_empty[0]);
+          }
+          j += run;
+        }
       }
     }
-  } else if (warp == kTreeThreads / 32 - 1) {
+    __syncwarp();
+  } else if (warp == kTreeQueries) {
     // ---- queries, rows in the order (token, head), rows behind the last one left as they are
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(a)) {
       const uint32_t buf = PAIR ? 0 : seg & 1, round = PAIR ? seg : seg >> 1;
@@ -615,15 +628,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           // (Loops over 32 logits at a time, read twice, keep the code small: unrolled over the row, all roles' code is more
           // than the instruction caches hold, and every instruction takes several times as long.)
           float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t y[32];
-            tm_ld32(y, s_at + 32 * c);
-            tm_wait_ld();
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t ya[32], yb[32];  // 32 logits are on their way while 32 are worked on
+          auto largest = [&](const uint32_t (&y)[32]) {
+            float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; ++i) mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(y[i]));
-            top = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          };
+          tm_ld32(ya, s_at);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tm_wait_ld32(ya);
+            tm_ld32(yb, s_at + 32 * c + 32);
+            largest(ya);
+            tm_wait_ld32(yb);
+            tm_ld32(ya, s_at + (32 * c + 64) % 128);  // (at the end the first ones, for the weights)
+            largest(yb);
           }
           top *= sc;
           const bool move = live && top > m + kAbove;  // (from -inf on: whenever there is anything)
@@ -645,11 +665,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           }
           const float m0 = m == -INFINITY ? 0.f : m;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {  // weights go where logits were that have been read
-            uint32_t y[32], p[16];
-            tm_ld32(y, s_at + 32 * c);
-            tm_wait_ld();
+          auto weigh = [&](const uint32_t (&y)[32], int c) {  // weights go where logits were that have been read
+            uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float y0 = ex2(fmaf(__uint_as_float(y[i]), sc, -m0)), y1 = ex2(fmaf(__uint_as_float(y[i + 1]), sc, -m0));
@@ -658,6 +675,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
               p[i / 2] = pack2<BF>(y0, y1);
             }
             tm_st16(s_at + 16 * c, p);
+          };
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tm_wait_ld32(ya);
+            tm_ld32(yb, s_at + 32 * c + 32);
+            weigh(ya, c);
+            tm_wait_ld32(yb);
+            if (c == 0) tm_ld32(ya, s_at + 64);
+            weigh(yb, c + 1);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tm_wait_st();
@@ -665,7 +691,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         if (!plain && (!PAIR || gs == 0)) {
           // values without a token are cleared, and what is not finite in drafted ones: a row of the tile a thread
           const uint32_t vi = PAIR ? 2 * j + 1 : 2 * j + 2;
-          ok = tree_wait(&sh.full[vi % NS], (vi / NS) & 1, &sh.abort, most_iters, err);
+          ok = tree_wait(&sh.v_full[j & 7], j >> 3 & 1, &sh.abort, most_iters, err);
           if (!ok) break;
           uint4* vr = reinterpret_cast<uint4*>(ring + vi % NS * kSlot + row * 128);
           if (!(va[quarter] >> lane & 1)) {
@@ -684,10 +710,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
                 uint16_t& y = e[c / 64 * (kHalf / 2) + c % 64];
                 if (odd_pair<BF>(y)) y = 0;
               }
-              *(volatile int*)&sh.poison[seg & 3] = (int)seg + 1;
+              *(volatile int*)&sh.poison[seg & 7] = (int)seg + 1;
             }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (PAIR) {
+          if (gs == 0) {
+            __syncwarp();
+            if (lane == 0) tree_arrive(&sh.clean[j & 7]);
+          } else if (!plain) {
+            ok = tree_wait(&sh.clean[j & 7], j >> 3 & 1, &sh.abort, most_iters, err);
+            if (!ok) break;
+          }
         }
         if (lent) {  // O is free again once the other group has taken what it needs
           ok = tree_wait(&sh.o_free[gs], free_seen++ & 1, &sh.abort, most_iters, err);
@@ -726,7 +761,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         l = l * f + y.y * f2;
         m = M;
       }
-      const bool poisoned = *(volatile int*)&sh.poison[seg & 3] == (int)seg + 1;
+      const bool poisoned = *(volatile int*)&sh.poison[seg & 7] == (int)seg + 1;
       const size_t at = live ? (size_t)(x.f + node) * a.Hq + (size_t)hk * a.G + head : 0;
       // the unit it starts with, begun by an earlier CTA, to slot 0; one it begins to slot 1
       float* wp = part + ((size_t)(2 * cta + (tile0 == 0 ? 1 : 0)) * RU + my_row) * (D + kTreePartHead);
@@ -803,16 +838,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   }
   tc_fence_before();
   __syncthreads();
-  // Where a wait ran out (only here, where every role is done, is it known), copies and products may be in flight: they end
-  // before the CTA gives back its shared and its tensor memory.
+  // The products in flight (where a wait ran out there may be some) and the arrivals of commits come before the CTA leaves.
+  if (warp == 1 && lane == 0) tree_commit(&sh.drain);
+  __syncwarp();
+  if (warp == 1) mbar_wait_bounded(&sh.drain, 0);
+  // Where a wait ran out (only here, where every role is done, is it known), copies may be in flight: they land
+  // before the CTA's shared memory is another's.
   if (*(volatile int*)&sh.abort) {
-    if (warp == 0)
-      for (uint32_t x = it > NS ? it - NS : 0; x < it; ++x)
-        if (x != hole) mbar_wait_bounded(&sh.full[x % NS], (x / NS) & 1);
-    if (warp == 1) {
-      if (lane == 0) tree_commit(&sh.drain);
-      __syncwarp();
-      mbar_wait_bounded(&sh.drain, 0);
+    if (warp == 0) {
+      for (uint32_t x = k_sent > 8 ? k_sent - 8 : 0; x < k_sent; ++x) mbar_wait_bounded(&sh.k_full[x & 7], x >> 3 & 1);
+      for (uint32_t x = v_sent > 8 ? v_sent - 8 : 0; x < v_sent; ++x) mbar_wait_bounded(&sh.v_full[x & 7], x >> 3 & 1);
     }
   }
   __syncthreads();
