@@ -183,26 +183,29 @@ __device__ __forceinline__ uint32_t score_key(float s) {
 }
 constexpr uint32_t kAlways = 0xffffffffu;
 
-// One cluster of CL CTAs a sequence and key head, each with a run of its pages: scores into shared memory, then the
-// picks-th largest key by four passes over 8 bits each (histograms in shared memory, summed over the cluster), then the pages
-// above it, and of those equal to it the first, in order.
-template <bool BF, int D>
+// One cluster of CL CTAs a sequence and key head, each with a run of its pages: scores into shared memory, then the least key
+// that is taken, eight bits at a time from the first one in which the keys differ (histograms in shared memory, summed
+// over the cluster) until its bin is taken whole, then the pages above it, and of those equal to it the first, in
+// order.  Bound by latency: a page's number, its bounds, a few rounds through the cluster; U pages a thread's loads ahead.
+template <bool BF, int D, int U>
 __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, int CL, int* err) {
   constexpr int LP = D / 32, PW = 32 / LP;  // lanes of a page (4 pieces of 16 bytes each), pages of a warp
   constexpr int NC = D / 8;                 // 16-byte pieces of a page's bounds: lo, then hi
+  constexpr int NW = kSelThreads / 32;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   uint4* qs = reinterpret_cast<uint4*>(smem_raw);              // [G][NC]: min(q, 0), then max(q, 0)
   float* unit = reinterpret_cast<float*>(qs + (size_t)a.G * NC);  // [G]
   uint32_t* key = reinterpret_cast<uint32_t*>(unit + a.G);     // [share]
   __shared__ uint32_t hist[4][256];
   __shared__ uint32_t count[2];  // of this CTA's share: keys above the threshold, and equal to it
-  __shared__ uint32_t found[2], warp_sum[kSelThreads / 32];
+  __shared__ uint32_t range[2];  // its keys' complement's largest, and their largest
+  __shared__ uint32_t found[3], warp_sum[2][NW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = CL > 1 ? (int)cluster_rank() : 0;
   const int row = blockIdx.x / CL, b = row / a.Hkv, h = row % a.Hkv;
   pdl_trigger();
   for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
-  if (tid < 2) count[tid] = 0;
+  if (tid < 2) count[tid] = range[tid] = 0;
   pdl_wait();
   int L = __ldca(a.L + b);
   if (L < 0 || L > a.max_pages * a.page) {
@@ -218,8 +221,17 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     for (int i = rank * kSelThreads + tid; i < P; i += CL * kSelThreads) chosen[i] = __ldca(table + i);
     return;
   }
+  // this CTA's pages; the first ones' numbers are on their way while the queries are prepared
+  const int each = (P + CL - 1) / CL, p0 = min(P, rank * each), p1 = min(P, p0 + each), mine = p1 - p0;
+  const int sub = lane % LP;
+  int id[U];
+  auto numbers = [&](int at) {
+#pragma unroll
+    for (int x = 0; x < U; ++x) id[x] = at + x * NW * PW < p1 ? __ldca(table + min(at + x * NW * PW + lane / LP, p1 - 1)) : 0;
+  };
+  numbers(p0 + warp * PW);
   // ---- the queries as whole numbers, a warp each
-  for (int g = warp; g < a.G; g += kSelThreads / 32) {
+  for (int g = warp; g < a.G; g += NW) {
     const uint16_t* q = a.q + ((size_t)b * a.Hq + (size_t)h * a.G + g) * D;
     float x[D / 32], most = 0.f;
     bool finite = true;
@@ -250,53 +262,96 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     if (lane == 0) unit[g] = power_of_two(e);
   }
   __syncthreads();
-  // ---- scores of this CTA's pages
-  const int each = (P + CL - 1) / CL, p0 = min(P, rank * each), p1 = min(P, p0 + each);
-  const int sub = lane % LP;
-  for (int at = p0 + warp * PW; at < p1; at += kSelThreads / 32 * PW) {
-    const int p = at + lane / LP, pc = min(p, p1 - 1);
-    int g = __ldca(table + pc);
-    const bool bad = g < 0 || g >= a.n_pages;
-    const size_t head = (size_t)(bad ? 0 : g) * a.Hkv + h;
-    uint4 v[4];
+  // ---- scores of this CTA's pages, U pages of a lane at a time
+  uint32_t low = 0, high = 0;  // of the keys that are compared: their complement's largest, their largest
+  for (int at = p0 + warp * PW; at < p1; at += U * NW * PW) {
+    uint4 v[U][4];
+    float scale[U];
+    bool bad[U];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __ldca(a.codes + head * NC + sub + k * LP);
-    const float scale = __ldca(a.scales + head);
-    float best = -INFINITY;
-    for (int x = 0; x < a.G; ++x) {
-      int dot = 0;
+    for (int x = 0; x < U; ++x) {
+      bad[x] = id[x] < 0 || id[x] >= a.n_pages;
+      if (at + x * NW * PW >= p1) continue;  // (the same for the warp)
+      const size_t head = (size_t)(bad[x] ? 0 : id[x]) * a.Hkv + h;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[x][k] = __ldca(a.codes + head * NC + sub + k * LP);
+      scale[x] = __ldca(a.scales + head);
+    }
+    numbers(at + U * NW * PW);
+    float best[U];
+#pragma unroll
+    for (int x = 0; x < U; ++x) best[x] = -INFINITY;
+    for (int g = 0; g < a.G; ++g) {
+      int dot[U];
+#pragma unroll
+      for (int x = 0; x < U; ++x) dot[x] = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4 w = qs[(size_t)x * NC + sub + k * LP];
-        dot = __dp4a((int)v[k].x, (int)w.x, dot);
-        dot = __dp4a((int)v[k].y, (int)w.y, dot);
-        dot = __dp4a((int)v[k].z, (int)w.z, dot);
-        dot = __dp4a((int)v[k].w, (int)w.w, dot);
-      }
+        const uint4 w = qs[(size_t)g * NC + sub + k * LP];
 #pragma unroll
-      for (int o = 1; o < LP; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      best = fmaxf(best, (float)dot * unit[x]);
+        for (int x = 0; x < U; ++x) {
+          dot[x] = __dp4a((int)v[x][k].x, (int)w.x, dot[x]);
+          dot[x] = __dp4a((int)v[x][k].y, (int)w.y, dot[x]);
+          dot[x] = __dp4a((int)v[x][k].z, (int)w.z, dot[x]);
+          dot[x] = __dp4a((int)v[x][k].w, (int)w.w, dot[x]);
+        }
+      }
+      const float u = unit[g];
+#pragma unroll
+      for (int x = 0; x < U; ++x) {
+#pragma unroll
+        for (int o = 1; o < LP; o <<= 1) dot[x] += __shfl_xor_sync(0xffffffffu, dot[x], o);
+        best[x] = fmaxf(best[x], (float)dot[x] * u);
+      }
     }
-    if (sub == 0 && p < p1) {
-      const float s = scale == INFINITY ? kMostScore : fminf(best * scale, kMostScore);
-      key[p - p0] = p < a.first || p >= P - a.last ? kAlways : bad ? 0u : score_key(s);
-      if (bad) raise_error(err, IG_DEVERR_INDEX);
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int p = at + x * NW * PW + lane / LP;
+      if (p >= p1 || sub) continue;
+      const float s = scale[x] == INFINITY ? kMostScore : fminf(best[x] * scale[x], kMostScore);
+      uint32_t k = kAlways;
+      if (p >= a.first && p < P - a.last) {
+        k = bad[x] ? 0u : score_key(s);
+        low = max(low, ~k);
+        high = max(high, k);
+      }
+      key[p - p0] = k;
+      if (bad[x]) raise_error(err, IG_DEVERR_INDEX);
     }
   }
+  low = __reduce_max_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    atomicMax(&range[0], low);
+    atomicMax(&range[1], high);
+  }
   __syncthreads();
-  // ---- the take-th largest key, byte by byte from the top
-  uint32_t prefix = 0, want = (uint32_t)a.picks;  // the want-th largest of the keys that begin with prefix
-  const int mine = p1 - p0;
-#pragma unroll
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
+  if (CL > 1) {
+    cluster_sync();
+    low = high = 0;
+    for (int r = 0; r < CL; ++r) {
+      low = max(low, peer_load(&range[0], (uint32_t)r));
+      high = max(high, peer_load(&range[1], (uint32_t)r));
+    }
+  } else {
+    low = range[0];
+    high = range[1];
+  }
+  // ---- of the pages that are not always taken, the `want`-th largest key; keys agree from bit `top` on
+  uint32_t want = (uint32_t)(a.picks - a.first - a.last);
+  int top = 32 - __clz(high ^ ~low), shift = top;
+  uint32_t prefix = top < 32 ? high >> top : 0u;  // keys >> shift that decide: above it taken, equal to it the first `want`
+  auto begins = [&](uint32_t k, int s) -> uint32_t { return s < 32 ? k >> s : 0u; };
+  for (int pass = 0; want > 0 && shift > 0; ++pass) {
+    const int next = max(shift - 8, 0);
+    const uint32_t mask = (1u << (shift - next)) - 1;
     for (int i = tid; i < mine; i += kSelThreads) {
       const uint32_t k = key[i];
-      if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[pass][(k >> shift) & 255], 1u);
+      if (k != kAlways && begins(k, shift) == prefix) atomicAdd(&hist[pass][(k >> next) & mask], 1u);
     }
     if (CL > 1) cluster_sync();
     else __syncthreads();
-    uint32_t n = 0;  // thread t: the keys with byte 255 - t
+    uint32_t n = 0;  // thread t: the keys with digit 255 - t
     if (CL > 1) {
       for (int r = 0; r < CL; ++r) n += peer_load(&hist[pass][255 - tid], (uint32_t)r);
     } else {
@@ -308,32 +363,43 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
       const uint32_t y = __shfl_up_sync(0xffffffffu, in, o);
       if (lane >= o) in += y;
     }
-    if (lane == 31) warp_sum[warp] = in;
+    if (lane == 31) warp_sum[pass & 1][warp] = in;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) in += warp_sum[w];
+    for (int w = 0; w < warp; ++w) in += warp_sum[pass & 1][w];
     if (in - n < want && want <= in) {
       found[0] = (uint32_t)(255 - tid);
       found[1] = want - (in - n);
+      found[2] = n;
     }
     __syncthreads();
-    prefix = prefix << 8 | found[0];
+    prefix = prefix << (shift - next) | found[0];
     want = found[1];
-    __syncthreads();
+    shift = next;
+    if (want == found[2]) break;  // all that begin so are taken
   }
+  // (the next write to `found` or `warp_sum` comes after a barrier that follows every read of them)
+  __syncthreads();
   // ---- keys above the threshold are taken, and the first `want` of those equal to it
-  uint32_t above = 0, equal = 0;
-  for (int i = tid; i < mine; i += kSelThreads) {
-    above += key[i] > prefix;
-    equal += key[i] == prefix;
-  }
-  above = __reduce_add_sync(0xffffffffu, above);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 0) {
-    atomicAdd(&count[0], above);
-    atomicAdd(&count[1], equal);
-  }
+  auto judge = [&](int i, bool& gt, bool& eq) {
+    const uint32_t k = i < mine ? key[i] : 0u, y = begins(k, shift);
+    gt = i < mine && (k == kAlways || y > prefix);
+    eq = i < mine && k != kAlways && y == prefix;
+  };
   uint32_t pos = 0, ties = 0;  // taken, and equal ones seen, before this share
   if (CL > 1) {
+    uint32_t above = 0, equal = 0;
+    for (int i = tid; i < mine; i += kSelThreads) {
+      bool gt, eq;
+      judge(i, gt, eq);
+      above += gt;
+      equal += eq;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+      atomicAdd(&count[0], above);
+      atomicAdd(&count[1], equal);
+    }
     cluster_sync();
     for (int r = 0; r < rank; ++r) {
       pos += peer_load(&count[0], (uint32_t)r);
@@ -341,18 +407,19 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     }
     pos += min(ties, want);
   }
-  for (int i0 = 0; i0 < mine; i0 += kSelThreads) {
+  int turn = 0;
+  for (int i0 = 0; i0 < mine; i0 += kSelThreads, turn ^= 1) {
     const int i = i0 + tid;
-    const uint32_t k = i < mine ? key[i] : 0u;
-    const bool gt = i < mine && k > prefix, eq = i < mine && k == prefix;
+    bool gt, eq;
+    judge(i, gt, eq);
     const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq), lt = (1u << lane) - 1;
-    if (lane == 0) warp_sum[warp] = __popc(bg) | __popc(be) << 16;
+    if (lane == 0) warp_sum[turn][warp] = __popc(bg) | __popc(be) << 16;
     __syncthreads();
     uint32_t before = 0, all = 0;
 #pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w) {
-      before += w < warp ? warp_sum[w] : 0;
-      all += warp_sum[w];
+    for (int w = 0; w < NW; ++w) {
+      before += w < warp ? warp_sum[turn][w] : 0;
+      all += warp_sum[turn][w];
     }
     const uint32_t g_at = (before & 0xffff) + __popc(bg & lt), e_at = (before >> 16) + __popc(be & lt);
     // equal ones taken before this page: of those in this round, as many as the first `want` reach
@@ -360,22 +427,23 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     if (gt || (eq && ties + e_at < want)) chosen[pos + g_at + e_taken] = __ldca(table + p0 + i);
     pos += (all & 0xffff) + min(ties + (all >> 16), want) - min(ties, want);
     ties += all >> 16;
-    __syncthreads();
   }
   if (CL > 1) cluster_sync();  // no CTA leaves while others may read its shared memory
 }
 
 template <bool BF, int D>
 ig_status launch_select(cudaStream_t st, SelArgs a) {
-  // CTAs of a cluster: more where there are few rows, as long as each has 256 pages or more; and as many as the keys need
+  // CTAs of a cluster: more where there are few rows, as long as each has 256 pages or more (not on a partition of the SMs,
+  // which need not have room for clusters side by side); and as many as the keys need
   const long long rows = (long long)a.B * a.Hkv;
   int CL = 1;
-  while (CL < kMaxCluster && ((rows * CL < 2 * sm_count(st) && a.max_pages / (2 * CL) >= 256) ||
+  const bool spread = stream_sms(st) == 0;
+  while (CL < kMaxCluster && ((spread && rows * CL < 2 * sm_count(st) && a.max_pages / (2 * CL) >= 256) ||
                               (size_t)((a.max_pages + CL - 1) / CL) * 4 > (size_t)kSelKeyBytes))
     CL *= 2;
   a.share = (a.max_pages + CL - 1) / CL;
   const size_t smem = (size_t)a.G * (2 * D + 4) + (size_t)a.share * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_page_select<BF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k_page_select<BF, D, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_fail(e, "page select smem attribute");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * CL));
@@ -390,7 +458,7 @@ ig_status launch_select(cudaStream_t st, SelArgs a) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CL > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k_page_select<BF, D>, a, CL, error_word());
+  e = cudaLaunchKernelEx(&cfg, k_page_select<BF, D, 4>, a, CL, error_word());
   if (e != cudaSuccess) return cuda_fail(e, "page select launch");
   IG_CHECK_LAUNCH("page select launch");
   return IG_OK;
