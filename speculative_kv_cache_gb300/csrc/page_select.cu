@@ -146,13 +146,13 @@ __global__ void __launch_bounds__(kBoundsThreads) k_page_bounds(const uint4* __r
 // choice
 // ---------------------------------------------------------------------------------------
 constexpr int kSelThreads = 256;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16, kPortableCluster = 8;
 constexpr int kMaxGroup = 256;        // queries of a key head
 constexpr int kSelKeyBytes = 128 << 10;  // keys of a CTA's share, at most
 constexpr float kMostScore = 3.402823466e38f;
 
 struct SelArgs {
-  int B, Hq, Hkv, G, page, n_pages, max_pages, picks, first, last, share;  // share: pages of a CTA, at most
+  int B, Hq, Hkv, G, page, n_pages, max_pages, picks, first, last;
   const uint16_t* q;
   const uint4* codes;
   const float* scales;
@@ -168,12 +168,17 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
 }
-// a word of another CTA's shared memory
-__device__ __forceinline__ uint32_t peer_load(const void* p, uint32_t rank) {
-  uint32_t at, v;
+// Sums and maxima into a word of another CTA's shared memory.  (Each CTA sends what the others need before a barrier of the cluster,
+// rather than fetch theirs after it: a trip less, and none may leave late.)
+__device__ __forceinline__ void peer_add(void* p, uint32_t rank, uint32_t v) {
+  uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ void peer_max(void* p, uint32_t rank, uint32_t v) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
 
 // Scores in the order of whole numbers; a page that is always taken is above them all.
@@ -196,16 +201,16 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
   uint4* qs = reinterpret_cast<uint4*>(smem_raw);              // [G][NC]: min(q, 0), then max(q, 0)
   float* unit = reinterpret_cast<float*>(qs + (size_t)a.G * NC);  // [G]
   uint32_t* key = reinterpret_cast<uint32_t*>(unit + a.G);     // [share]
-  __shared__ uint32_t hist[4][256];
-  __shared__ uint32_t count[2];  // of this CTA's share: keys above the threshold, and equal to it
-  __shared__ uint32_t range[2];  // its keys' complement's largest, and their largest
+  __shared__ uint32_t hist[4][256], sum[4][256];  // digits of this CTA's keys, and of the cluster's
+  __shared__ uint32_t count[2], ahead[2];  // keys above the threshold, and equal to it: this CTA's, and those of the CTAs before it
+  __shared__ uint32_t range[2], all[2];    // the keys' complement's largest, and their largest: this CTA's, the cluster's
   __shared__ uint32_t found[3], warp_sum[2][NW];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = CL > 1 ? (int)cluster_rank() : 0;
   const int row = blockIdx.x / CL, b = row / a.Hkv, h = row % a.Hkv;
   pdl_trigger();
-  for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
-  if (tid < 2) count[tid] = range[tid] = 0;
+  for (int i = tid; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = (&sum[0][0])[i] = 0;
+  if (tid < 2) count[tid] = ahead[tid] = range[tid] = all[tid] = 0;
   pdl_wait();
   int L = __ldca(a.L + b);
   if (L < 0 || L > a.max_pages * a.page) {
@@ -221,6 +226,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     for (int i = rank * kSelThreads + tid; i < P; i += CL * kSelThreads) chosen[i] = __ldca(table + i);
     return;
   }
+  if (CL > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA is there, its sums begin at zero
   // this CTA's pages; the first ones' numbers are on their way while the queries are prepared
   const int each = (P + CL - 1) / CL, p0 = min(P, rank * each), p1 = min(P, p0 + each), mine = p1 - p0;
   const int sub = lane % LP;
@@ -327,12 +333,11 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
   }
   __syncthreads();
   if (CL > 1) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    if (tid < 2 * CL) peer_max(&all[tid & 1], (uint32_t)tid >> 1, range[tid & 1]);
     cluster_sync();
-    low = high = 0;
-    for (int r = 0; r < CL; ++r) {
-      low = max(low, peer_load(&range[0], (uint32_t)r));
-      high = max(high, peer_load(&range[1], (uint32_t)r));
-    }
+    low = all[0];
+    high = all[1];
   } else {
     low = range[0];
     high = range[1];
@@ -349,13 +354,12 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
       const uint32_t k = key[i];
       if (k != kAlways && begins(k, shift) == prefix) atomicAdd(&hist[pass][(k >> next) & mask], 1u);
     }
-    if (CL > 1) cluster_sync();
-    else __syncthreads();
-    uint32_t n = 0;  // thread t: the keys with digit 255 - t
+    __syncthreads();
+    uint32_t n = hist[pass][255 - tid];  // thread t: the keys with digit 255 - t
     if (CL > 1) {
-      for (int r = 0; r < CL; ++r) n += peer_load(&hist[pass][255 - tid], (uint32_t)r);
-    } else {
-      n = hist[pass][255 - tid];
+      for (int r = 0; n && r < CL; ++r) peer_add(&sum[pass][255 - tid], (uint32_t)r, n);
+      cluster_sync();
+      n = sum[pass][255 - tid];
     }
     uint32_t in = n;
 #pragma unroll
@@ -385,7 +389,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     gt = i < mine && (k == kAlways || y > prefix);
     eq = i < mine && k != kAlways && y == prefix;
   };
-  uint32_t pos = 0, ties = 0;  // taken, and equal ones seen, before this share
+  uint32_t pos = 0, ties = 0;  // taken, and equal ones seen, before this share (nothing is sent after the last barrier)
   if (CL > 1) {
     uint32_t above = 0, equal = 0;
     for (int i = tid; i < mine; i += kSelThreads) {
@@ -400,12 +404,11 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
       atomicAdd(&count[0], above);
       atomicAdd(&count[1], equal);
     }
+    __syncthreads();
+    if (tid < 2 * CL && tid >> 1 > rank) peer_add(&ahead[tid & 1], (uint32_t)tid >> 1, count[tid & 1]);
     cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-      pos += peer_load(&count[0], (uint32_t)r);
-      ties += peer_load(&count[1], (uint32_t)r);
-    }
-    pos += min(ties, want);
+    ties = ahead[1];
+    pos = ahead[0] + min(ties, want);
   }
   int turn = 0;
   for (int i0 = 0; i0 < mine; i0 += kSelThreads, turn ^= 1) {
@@ -428,25 +431,18 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     pos += (all & 0xffff) + min(ties + (all >> 16), want) - min(ties, want);
     ties += all >> 16;
   }
-  if (CL > 1) cluster_sync();  // no CTA leaves while others may read its shared memory
 }
 
-template <bool BF, int D>
-ig_status launch_select(cudaStream_t st, SelArgs a) {
-  // CTAs of a cluster: more where there are few rows, as long as each has 256 pages or more (not on a partition of the SMs,
-  // which need not have room for clusters side by side); and as many as the keys need
-  const long long rows = (long long)a.B * a.Hkv;
-  int CL = 1;
-  const bool spread = stream_sms(st) == 0;
-  while (CL < kMaxCluster && ((spread && rows * CL < 2 * sm_count(st) && a.max_pages / (2 * CL) >= 256) ||
-                              (size_t)((a.max_pages + CL - 1) / CL) * 4 > (size_t)kSelKeyBytes))
-    CL *= 2;
-  a.share = (a.max_pages + CL - 1) / CL;
-  const size_t smem = (size_t)a.G * (2 * D + 4) + (size_t)a.share * 4;
-  cudaError_t e = cudaFuncSetAttribute(k_page_select<BF, D, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_fail(e, "page select smem attribute");
+// U: with many rows two pages a lane, so that three CTAs share an SM (64 sequences of up to 512 pages, 8 key heads: 14.8 us, with
+// four 18.4); with few four, so that more is on its way (8 rows of 8192: 17 us, with two 22).
+template <bool BF, int D, int U>
+ig_status launch_select_u(cudaStream_t st, const SelArgs& a, int CL, size_t smem) {
+  cudaError_t e = cudaFuncSetAttribute(k_page_select<BF, D, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && CL > kPortableCluster)
+    e = cudaFuncSetAttribute(k_page_select<BF, D, U>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return cuda_fail(e, "page select attributes");
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(rows * CL));
+  cfg.gridDim = dim3((unsigned)((long long)a.B * a.Hkv * CL));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -458,10 +454,23 @@ ig_status launch_select(cudaStream_t st, SelArgs a) {
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CL > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, k_page_select<BF, D, 4>, a, CL, error_word());
+  e = cudaLaunchKernelEx(&cfg, k_page_select<BF, D, U>, a, CL, error_word());
   if (e != cudaSuccess) return cuda_fail(e, "page select launch");
   IG_CHECK_LAUNCH("page select launch");
   return IG_OK;
+}
+
+template <bool BF, int D>
+ig_status launch_select(cudaStream_t st, SelArgs a) {
+  // CTAs of a cluster: more where there are few rows, as long as each has 256 pages or more (not on a partition of the SMs,
+  // which need not have room for clusters side by side); and as many as the keys need
+  const long long rows = (long long)a.B * a.Hkv;
+  auto share = [&](int CL) -> size_t { return (size_t)((a.max_pages + CL - 1) / CL); };
+  int CL = 1;
+  while (CL < kMaxCluster && stream_sms(st) == 0 && rows * CL < sm_count(st) && a.max_pages / (2 * CL) >= 256) CL *= 2;
+  while (CL < kPortableCluster && share(CL) * 4 > (size_t)kSelKeyBytes) CL *= 2;
+  const size_t smem = (size_t)a.G * (2 * D + 4) + share(CL) * 4;
+  return rows * CL > sm_count(st) ? launch_select_u<BF, D, 2>(st, a, CL, smem) : launch_select_u<BF, D, 4>(st, a, CL, smem);
 }
 
 }  // namespace
@@ -504,7 +513,7 @@ extern "C" ig_status ig_page_select(void* stream, int dtype, int B, int Hq, int 
   IG_REQUIRE(page > 0 && page % 8 == 0, "page must be a positive multiple of 8 (got %d)", page);
   IG_REQUIRE(n_pages > 0 && max_pages > 0, "n_pages and max_pages must be positive");
   IG_REQUIRE((long long)max_pages * page < (1ll << 30), "max_pages*page must stay below 2^30");
-  IG_REQUIRE(max_pages <= kMaxCluster * kSelKeyBytes / 4, "max_pages at most %d", kMaxCluster * kSelKeyBytes / 4);
+  IG_REQUIRE(max_pages <= kPortableCluster * kSelKeyBytes / 4, "max_pages at most %d", kPortableCluster * kSelKeyBytes / 4);
   IG_REQUIRE((double)n_pages * Hkv * page < 2147483648.0, "n_pages*Hkv*page must stay below 2^31 rows");
   IG_REQUIRE((double)B * Hq < 134217728.0, "B*Hq must stay below 2^27");
   IG_REQUIRE(first >= 0 && last >= 1 && (long long)first + last <= picks,
@@ -514,7 +523,7 @@ extern "C" ig_status ig_page_select(void* stream, int dtype, int B, int Hq, int 
   IG_REQUIRE(aligned(q, 16) && aligned(codes, 16), "q, codes must be 16-byte aligned");
   IG_REQUIRE(aligned(scales, 4) && aligned(page_table, 4) && aligned(L_valid, 4) && aligned(chosen, 4) && aligned(tokens, 4),
              "misaligned buffer");
-  const SelArgs a{B, Hq, Hkv, Hq / Hkv, page, n_pages, max_pages, picks, first, last, 0, q, reinterpret_cast<const uint4*>(codes),
+  const SelArgs a{B, Hq, Hkv, Hq / Hkv, page, n_pages, max_pages, picks, first, last, q, reinterpret_cast<const uint4*>(codes),
                   scales, page_table, L_valid, chosen, tokens};
   cudaStream_t st = as_stream(stream);
   if (dtype == IG_F16) return d == 128 ? launch_select<false, 128>(st, a) : launch_select<false, 64>(st, a);
