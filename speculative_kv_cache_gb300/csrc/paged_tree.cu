@@ -166,6 +166,11 @@ __device__ __forceinline__ void tm_wait_ld32(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 __device__ __forceinline__ void tree_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
@@ -276,6 +281,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   unsigned char* ring = sq + 2 * kSlot;
   TreeShared& sh = *reinterpret_cast<TreeShared*>(ring + NS * kSlot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.k_full[i], 1);
@@ -453,35 +462,37 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       t1 = t2;
     }
   } else if (warp == 1) {
-    // ---- the MMAs, by one thread.  (Two, one a group: 158 -> 190 us for two trees of 64 tokens on 65536.)
+    // ---- the MMAs, by one thread.  An issue returns about when its product begins, so the tensor cores wait for whatever is
+    // done between two products, and 170 cycles more to begin again: with two blocks a group's values and its next logits
+    // are issued in one go, with all that they need in hand (165 -> 161 us for two trees of 64 tokens on 65536).  (Two issuing threads, one
+    // a group, whose products come mixed: 190 us.)
     if (lane == 0) {
       uint32_t p_seen[2] = {0, 0};
       bool ok = true;
+      const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(sq);
+      const uint32_t desc_hi = (uint32_t)(sw128_desc(0) >> 32), desc_lo = (uint32_t)sw128_desc(0), mn_lo = (uint32_t)sw128_desc_mn(0, kHalf);
       auto full = [&](uint64_t* bars, uint32_t tile) -> bool { return tree_wait1(&bars[tile & 7], tile >> 3 & 1, &sh.abort, err); };
       // S of group g from queries at qa and the keys in slot idx
       auto logits = [&](int g, uint32_t qa, uint32_t idx) {
-        const uint64_t ad = sw128_desc(qa), bd = sw128_desc(smem_addr(ring + idx % NS * kSlot));
-        tc_fence_after();
+        const uint32_t ad = desc_lo + (qa >> 4), bd = desc_lo + ((ring_at + idx % NS * kSlot) >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const uint32_t o = (ks / 4) * (kHalf >> 4) + (ks % 4) * 2;
           asm volatile(
-              "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
-                  tmem + g * kTreeTile),
-              "l"(ad + o), "l"(bd + o), "r"(kIdS), "r"(ks));
+              "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+              " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(tmem + g * kTreeTile),
+              "r"(ad + o), "r"(bd + o), "r"(kIdS), "r"(ks), "r"(desc_hi));
         }
-        tree_commit(&sh.s_full[g]);
       };
       // O of group g, from its weights and the values in slot idx
       auto values = [&](int g, uint32_t idx, bool more) {
-        const uint64_t bd = sw128_desc_mn(smem_addr(ring + idx % NS * kSlot), kHalf);
-        tc_fence_after();
+        const uint32_t bd = mn_lo + ((ring_at + idx % NS * kSlot) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kTreeTile / 16; ++ks)
           asm volatile(
-              "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(
-                  tmem + 2 * kTreeTile + g * kTreeTile),
-              "r"(tmem + g * kTreeTile + ks * 8), "l"(bd + ks * 128), "r"(kIdO), "r"((uint32_t)more | (uint32_t)ks));
+              "{\n .reg .pred p;\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+              " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(tmem + 2 * kTreeTile + g * kTreeTile),
+              "r"(tmem + g * kTreeTile + ks * 8), "r"(bd + ks * 128), "r"(kIdO), "r"((uint32_t)more | (uint32_t)ks), "r"(desc_hi));
       };
       auto weights = [&](int g) -> bool { return tree_wait1(&sh.p_full[g], p_seen[g]++ & 1, &sh.abort, err); };
       if constexpr (!PAIR) {
@@ -496,7 +507,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
             if (seg_at == 0) ok = tree_wait1(&sh.q_full[buf], seg >> 1 & 1, &sh.abort, err);
             ok = ok && full(sh.k_full, i);
             if (!ok) break;
-            logits(i & 1, smem_addr(sq + buf * kSlot), idx);
+            tc_fence_after();
+            logits(i & 1, q_at + buf * kSlot, idx);
+            tree_commit(&sh.s_full[i & 1]);
             tree_commit(&sh.empty[idx % NS]);
             ++i;
             if (++seg_at == seg_run) {
@@ -514,6 +527,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           const uint32_t idx = 2 * j + 2;
           ok = full(sh.v_full, j) && weights(j & 1);
           if (!ok) break;
+          tc_fence_after();
           values(j & 1, idx, k >= 2);
           tree_commit(&sh.empty[idx % NS]);
           if (k >= run - 2) tree_commit(&sh.o_done[j & 1]);
@@ -532,23 +546,24 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           ok = tree_wait1(&sh.q_full[0], seg & 1, &sh.abort, err);
           for (int k = -1; k < run && ok; ++k) {
             const uint32_t vi = 2 * (j + k) + 1, ki = vi + 1;
+            const bool old = k >= 0, next = k < run - 1;
+            ok = (!old || full(sh.v_full, j + k)) && (!next || full(sh.k_full, j + k + 1));
             for (int g = 0; g < groups && ok; ++g) {
-              if (k >= 0) {
-                ok = (g > 0 || full(sh.v_full, j + k)) && weights(g);
-                if (!ok) break;
-                values(g, vi, k > 0);
-                if (k == run - 1) tree_commit(&sh.o_done[g]);
+              ok = !old || weights(g);
+              if (!ok) break;
+              tc_fence_after();
+              if (old) values(g, vi, k > 0);
+              if (next) {
+                logits(g, q_at + g * kSlot, ki);
+                tree_commit(&sh.s_full[g]);
               }
-              if (k < run - 1) {
-                ok = g > 0 || full(sh.k_full, j + k + 1);
-                if (!ok) break;
-                logits(g, smem_addr(sq) + g * kSlot, ki);
+              if (g == groups - 1) {
+                if (old) tree_commit(&sh.empty[vi % NS]);
+                if (next) tree_commit(&sh.empty[ki % NS]);
+                if (k == run - 2) tree_commit(&sh.q_empty[0]);
               }
+              if (!next) tree_commit(&sh.o_done[g]);  // (the unit's last: what comes before it has come when it is seen)
             }
-            if (!ok) break;
-            if (k >= 0) tree_commit(&sh.empty[vi % NS]);
-            if (k < run - 1) tree_commit(&sh.empty[ki % NS]);
-            if (k == run - 2) tree_commit(&sh.q_empty[0]);
           }
           j += run;
         }
@@ -632,8 +647,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           auto largest = [&](const uint32_t (&y)[32]) {
             float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx[i % 4] = fmaxf(mx[i % 4], __uint_as_float(y[i]));
-            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            for (int i = 0; i < 32; i += 2) mx[i / 2 % 4] = max3(mx[i / 2 % 4], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           };
           tm_ld32(ya, s_at);
 #pragma unroll 1
@@ -685,8 +700,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
             if (c == 0) tm_ld32(ya, s_at + 64);
             weigh(yb, c + 1);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tm_wait_st();
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
         if (!plain && (!PAIR || gs == 0)) {
           // values without a token are cleared, and what is not finite in drafted ones: a row of the tile a thread
@@ -838,19 +853,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   }
   tc_fence_before();
   __syncthreads();
-  // The products in flight (where a wait ran out there may be some) and the arrivals of commits come before the CTA leaves.
-  if (warp == 1 && lane == 0) tree_commit(&sh.drain);
-  __syncwarp();
-  if (warp == 1) mbar_wait_bounded(&sh.drain, 0);
-  // Where a wait ran out (only here, where every role is done, is it known), copies may be in flight: they land
-  // before the CTA's shared memory is another's.
+  // Where a wait ran out (only here, where every role is done, is it known), copies and products may be in flight: they end
+  // before the CTA gives back its shared and its tensor memory.  (Else the last commit of all has been waited for.)
   if (*(volatile int*)&sh.abort) {
+    if (warp == 1) {
+      if (lane == 0) tree_commit(&sh.drain);
+      __syncwarp();
+      mbar_wait_bounded(&sh.drain, 0);
+    }
     if (warp == 0) {
       for (uint32_t x = k_sent > 8 ? k_sent - 8 : 0; x < k_sent; ++x) mbar_wait_bounded(&sh.k_full[x & 7], x >> 3 & 1);
       for (uint32_t x = v_sent > 8 ? v_sent - 8 : 0; x < v_sent; ++x) mbar_wait_bounded(&sh.v_full[x & 7], x >> 3 & 1);
     }
+    __syncthreads();
   }
-  __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTreeTmem));
