@@ -171,8 +171,18 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
   return r;
 }
-__device__ __forceinline__ void tree_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+// A number that is the same in every lane, as one the compiler knows to be so (and may keep in a uniform register).
+__device__ __forceinline__ int uniform(int x) { return (int)__reduce_max_sync(0xffffffffu, (unsigned)x); }
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t y;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(y));
+  return y;
+}
+__device__ __forceinline__ void tree_commit(uint64_t* bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %1, 0;\n"
+      " @p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_addr(bar)), "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ void tree_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -189,17 +199,6 @@ __device__ __noinline__ bool tree_wait_on(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit, int* err) {
   if (limit > 0 && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return tree_wait_on(bar, parity, abort, limit, err);
-}
-
-// The same by one thread.
-__device__ __noinline__ bool tree_wait1_on(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  for (uint32_t i = 0; i < (uint32_t)kDefaultWaitIters && !*abort; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  if (!atomicExch(const_cast<int*>(abort), 1)) raise_error(err, IG_DEVERR_TIMEOUT);
-  return false;
-}
-__device__ __forceinline__ bool tree_wait1(uint64_t* bar, uint32_t parity, volatile int* abort, int* err) {
-  return mbar_try_wait(bar, parity) || tree_wait1_on(bar, parity, abort, err);
 }
 
 // The units of a CTA's share, in order: of each request its key heads, of each key head its blocks of rows.
@@ -462,110 +461,131 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       t1 = t2;
     }
   } else if (warp == 1) {
-    // ---- the MMAs, by one thread.  An issue returns about when its product begins, so the tensor cores wait for whatever is
-    // done between two products, and 170 cycles more to begin again: with two blocks a group's values and its next logits
-    // are issued in one go, with all that they need in hand (165 -> 161 us for two trees of 64 tokens on 65536).  (Two issuing threads, one
-    // a group, whose products come mixed: 190 us.)
-    if (lane == 0) {
-      uint32_t p_seen[2] = {0, 0};
-      bool ok = true;
-      const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(sq);
-      const uint32_t desc_hi = (uint32_t)(sw128_desc(0) >> 32), desc_lo = (uint32_t)sw128_desc(0), mn_lo = (uint32_t)sw128_desc_mn(0, kHalf);
-      auto full = [&](uint64_t* bars, uint32_t tile) -> bool { return tree_wait1(&bars[tile & 7], tile >> 3 & 1, &sh.abort, err); };
-      // S of group g from queries at qa and the keys in slot idx
-      auto logits = [&](int g, uint32_t qa, uint32_t idx) {
-        const uint32_t ad = desc_lo + (qa >> 4), bd = desc_lo + ((ring_at + idx % NS * kSlot) >> 4);
+    // ---- the MMAs.  The warp goes together, and one lane issues, by predicate: what the products take is then known to be the same
+    // in every lane and stays in uniform registers, where the instructions want it.  An issue returns about when its
+    // product begins, so the tensor cores wait for whatever is done between two products, and 170 cycles more to begin
+    // again: with two blocks a group's values and its next logits are issued in one go, with all that they need in hand.
+    // (Two issuing threads, one a group, whose products come mixed: 158 -> 190 us for two trees of 64 tokens on 65536.)
+    const uint32_t lead = elected();
+    uint32_t p_seen0 = 0, p_seen1 = 0;
+    bool ok = true;
+    const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(sq);
+    const uint32_t desc_hi = (uint32_t)(sw128_desc(0) >> 32), desc_lo = (uint32_t)sw128_desc(0), mn_lo = (uint32_t)sw128_desc_mn(0, kHalf);
+    const uint32_t tm = (uint32_t)uniform((int)tmem);
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return tree_wait(bar, parity, &sh.abort, most_iters, err); };
+    // S of group g from queries at qa and the keys in a slot
+    auto logits = [&](uint32_t g, uint32_t qa, uint32_t slot) {
+      const uint32_t ad = desc_lo + (qa >> 4), bd = desc_lo + ((ring_at + slot * kSlot) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t o = (ks / 4) * (kHalf >> 4) + (ks % 4) * 2;
-          asm volatile(
-              "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
-              " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(tmem + g * kTreeTile),
-              "r"(ad + o), "r"(bd + o), "r"(kIdS), "r"(ks), "r"(desc_hi));
-        }
-      };
-      // O of group g, from its weights and the values in slot idx
-      auto values = [&](int g, uint32_t idx, bool more) {
-        const uint32_t bd = mn_lo + ((ring_at + idx % NS * kSlot) >> 4);
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t o = (ks / 4) * (kHalf >> 4) + (ks % 4) * 2;
+        asm volatile(
+            "{\n .reg .pred p, q;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+            " setp.ne.b32 q, %6, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(tm + g * kTreeTile),
+            "r"(ad + o), "r"(bd + o), "r"(kIdS), "r"(ks), "r"(desc_hi), "r"(lead));
+      }
+      tree_commit(&sh.s_full[g], lead);
+    };
+    // O of group g, from its weights and the values in a slot
+    auto values = [&](uint32_t g, uint32_t slot, uint32_t more) {
+      const uint32_t bd = mn_lo + ((ring_at + slot * kSlot) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < kTreeTile / 16; ++ks)
-          asm volatile(
-              "{\n .reg .pred p;\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
-              " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(tmem + 2 * kTreeTile + g * kTreeTile),
-              "r"(tmem + g * kTreeTile + ks * 8), "r"(bd + ks * 128), "r"(kIdO), "r"((uint32_t)more | (uint32_t)ks), "r"(desc_hi));
-      };
-      auto weights = [&](int g) -> bool { return tree_wait1(&sh.p_full[g], p_seen[g]++ & 1, &sh.abort, err); };
-      if constexpr (!PAIR) {
-        // logits of a tile ahead of the values of the one before; tile i is of group i & 1
-        uint32_t i = 0, seg = 0;    // tile whose logits are next, and its unit
-        TreeWalk v = w;             // of the values
-        uint32_t j = 0;
-        int seg_run = w.left > 0 ? w.run() : 0, seg_at = 0, run = seg_run, k = 0;
-        for (bool first = true; ok && v.left > 0;) {
-          if (w.left > 0) {  // the next tile's logits
-            const uint32_t buf = seg & 1, idx = i == 0 ? 0 : 2 * i - 1;
-            if (seg_at == 0) ok = tree_wait1(&sh.q_full[buf], seg >> 1 & 1, &sh.abort, err);
-            ok = ok && full(sh.k_full, i);
-            if (!ok) break;
-            tc_fence_after();
-            logits(i & 1, q_at + buf * kSlot, idx);
-            tree_commit(&sh.s_full[i & 1]);
-            tree_commit(&sh.empty[idx % NS]);
-            ++i;
-            if (++seg_at == seg_run) {
-              tree_commit(&sh.q_empty[buf]);
-              ++seg;
-              w.next(a);
-              seg_at = 0;
-              seg_run = w.left > 0 ? w.run() : 0;
-            }
-          }
-          if (first) {
-            first = false;
-            continue;
-          }
-          const uint32_t idx = 2 * j + 2;
-          ok = full(sh.v_full, j) && weights(j & 1);
+      for (int ks = 0; ks < kTreeTile / 16; ++ks)
+        asm volatile(
+            "{\n .reg .pred p, q;\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+            " setp.ne.b32 q, %6, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(
+                tm + (2 + g) * kTreeTile),
+            "r"(tm + g * kTreeTile + ks * 8), "r"(bd + ks * 128), "r"(kIdO), "r"(more | (uint32_t)ks), "r"(desc_hi), "r"(lead));
+    };
+    auto weights = [&](uint32_t g) -> bool {
+      const uint32_t parity = (g ? p_seen1++ : p_seen0++) & 1;
+      return wait(&sh.p_full[g], parity);
+    };
+    // the ring's slots, two further each time
+    auto step = [&](uint32_t slot) -> uint32_t { return slot + 2 < NS ? slot + 2 : slot + 2 - NS; };
+    if constexpr (!PAIR) {
+      // logits of a tile ahead of the values of the one before; tile i is of group i & 1
+      uint32_t i = 0, seg = 0, k_slot = 0;  // tile whose logits are next, its unit and its keys' slot
+      uint32_t j = 0, v_slot = 2 % NS;
+      TreeWalk v = w;                       // of the values
+      int left = uniform(w.left), v_left = left;
+      int seg_run = left > 0 ? uniform(w.run()) : 0, seg_at = 0, run = seg_run, k = 0;
+      for (bool first = true; ok && v_left > 0;) {
+        if (left > 0) {  // the next tile's logits
+          const uint32_t buf = seg & 1;
+          if (seg_at == 0) ok = wait(&sh.q_full[buf], seg >> 1 & 1);
+          ok = ok && wait(&sh.k_full[i & 7], i >> 3 & 1);
           if (!ok) break;
           tc_fence_after();
-          values(j & 1, idx, k >= 2);
-          tree_commit(&sh.empty[idx % NS]);
-          if (k >= run - 2) tree_commit(&sh.o_done[j & 1]);
-          ++j;
-          if (++k == run) {
-            v.next(a);
-            k = 0;
-            run = v.left > 0 ? v.run() : 0;
+          logits(i & 1, q_at + buf * kSlot, k_slot);
+          tree_commit(&sh.empty[k_slot], lead);
+          k_slot = i == 0 ? 1 : step(k_slot);
+          ++i;
+          if (++seg_at == seg_run) {
+            tree_commit(&sh.q_empty[buf], lead);
+            ++seg;
+            w.next(a);
+            left = uniform(w.left);
+            seg_at = 0;
+            seg_run = left > 0 ? uniform(w.run()) : 0;
           }
         }
-      } else {
-        // a tile's values and the next tile's logits, group by group; a unit begins with logits alone
-        uint32_t j = 0;
-        for (uint32_t seg = 0; ok && w.left > 0; w.next(a), ++seg) {
-          const int run = w.run(), groups = w.x.n * a.G - w.u % w.blocks * RU > kTreeTile ? 2 : 1;
-          ok = tree_wait1(&sh.q_full[0], seg & 1, &sh.abort, err);
-          for (int k = -1; k < run && ok; ++k) {
-            const uint32_t vi = 2 * (j + k) + 1, ki = vi + 1;
-            const bool old = k >= 0, next = k < run - 1;
-            ok = (!old || full(sh.v_full, j + k)) && (!next || full(sh.k_full, j + k + 1));
-            for (int g = 0; g < groups && ok; ++g) {
-              ok = !old || weights(g);
-              if (!ok) break;
-              tc_fence_after();
-              if (old) values(g, vi, k > 0);
-              if (next) {
-                logits(g, q_at + g * kSlot, ki);
-                tree_commit(&sh.s_full[g]);
-              }
-              if (g == groups - 1) {
-                if (old) tree_commit(&sh.empty[vi % NS]);
-                if (next) tree_commit(&sh.empty[ki % NS]);
-                if (k == run - 2) tree_commit(&sh.q_empty[0]);
-              }
-              if (!next) tree_commit(&sh.o_done[g]);  // (the unit's last: what comes before it has come when it is seen)
+        if (first) {
+          first = false;
+          continue;
+        }
+        const uint32_t g = j & 1;
+        ok = wait(&sh.v_full[j & 7], j >> 3 & 1) && weights(g);
+        if (!ok) break;
+        tc_fence_after();
+        values(g, v_slot, k >= 2);
+        tree_commit(&sh.empty[v_slot], lead);
+        if (k >= run - 2) tree_commit(&sh.o_done[g], lead);
+        v_slot = step(v_slot);
+        ++j;
+        if (++k == run) {
+          v.next(a);
+          v_left = uniform(v.left);
+          k = 0;
+          run = v_left > 0 ? uniform(v.run()) : 0;
+        }
+      }
+    } else {
+      // a tile's values and the next tile's logits, group by group; a unit begins with logits alone
+      uint32_t j = 0, k_slot = 0, v_slot = 1;
+      for (uint32_t seg = 0; ok && uniform(w.left) > 0; w.next(a), ++seg) {
+        const int run = uniform(w.run()), rows = uniform(w.x.n * a.G - w.u % w.blocks * RU);
+        const uint32_t groups = rows > kTreeTile ? 2 : 1;
+        ok = wait(&sh.q_full[0], seg & 1) && wait(&sh.k_full[j & 7], j >> 3 & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (uint32_t g = 0; g < groups; ++g) logits(g, q_at + g * kSlot, k_slot);
+        tree_commit(&sh.empty[k_slot], lead);
+        k_slot = step(k_slot);
+        if (run == 1) tree_commit(&sh.q_empty[0], lead);
+        for (int k = 0; k < run; ++k, ++j) {
+          const bool next = k < run - 1;
+          ok = wait(&sh.v_full[j & 7], j >> 3 & 1) && (!next || wait(&sh.k_full[(j + 1) & 7], (j + 1) >> 3 & 1));
+          for (uint32_t g = 0; ok && g < groups; ++g) {
+            ok = weights(g);
+            if (!ok) break;
+            tc_fence_after();
+            values(g, v_slot, k > 0);
+            if (next) {
+              logits(g, q_at + g * kSlot, k_slot);
+            } else {
+              if (g == groups - 1) tree_commit(&sh.empty[v_slot], lead);
+              tree_commit(&sh.o_done[g], lead);  // (the unit's last: what comes before it has come when it is seen)
             }
           }
-          j += run;
+          if (!ok) break;
+          if (next) {
+            tree_commit(&sh.empty[v_slot], lead);
+            tree_commit(&sh.empty[k_slot], lead);
+            if (k == run - 2) tree_commit(&sh.q_empty[0], lead);
+            k_slot = step(k_slot);
+          }
+          v_slot = step(v_slot);
         }
       }
     }
@@ -857,7 +877,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   // before the CTA gives back its shared and its tensor memory.  (Else the last commit of all has been waited for.)
   if (*(volatile int*)&sh.abort) {
     if (warp == 1) {
-      if (lane == 0) tree_commit(&sh.drain);
+      tree_commit(&sh.drain, elected());
       __syncwarp();
       mbar_wait_bounded(&sh.drain, 0);
     }
