@@ -76,8 +76,10 @@ __device__ __forceinline__ uint16_t from_float(float v) {
 }
 
 constexpr int kTreeTile = 128;                 // tokens of a tile, rows of a block
-constexpr int kTreeThreads = 352;              // warps: 0 TMA, 1 MMAs, 2 .. 9 softmax, 10 queries
-constexpr int kTreeSoftmax = 2, kTreeQueries = 10;
+// Warps 4 .. 11 are the softmax groups, warp w with the rows of quarter w % 4, which also is the quarter of the SM it runs on.  The
+// warp of the MMAs, which sets the pace, shares its own with the rows that are there last, as the TMA's nearly does.
+constexpr int kTreeThreads = 384;
+constexpr int kTreeQueries = 1, kTreeTma = 2, kTreeMma = 3, kTreeSoftmax = 4;
 constexpr int kMaxTreeCtas = 160;              // upper bound of the grid (sizes the workspace)
 constexpr int kTreePartHead = 4;               // a partial: [m, l, -, -, o[D]]
 constexpr uint32_t kTreeTmem = 512;            // columns: S of either group, then O of either
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   // Tensor memory is taken when the kernels before have ended and before the next may start: none of them waits for
   // columns that another holds while it waits.
   pdl_wait();
-  if (warp == 1) {
+  if (warp == kTreeMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "r"(kTreeTmem));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   const uint32_t most_iters = (uint32_t)kDefaultWaitIters;
   uint32_t it = 0, k_sent = 0, v_sent = 0;  // the producer's slots; tiles whose keys and values it has sent for
 
-  if (warp == 0) {
+  if (warp == kTreeTma) {
     // ---- tiles.  Lane i moves box i / halves, half i % halves; a page's number is read two tiles ahead of its keys.
     constexpr int H = D / 64;
     const int box_at = lane / H * box, col = lane % H;
@@ -460,7 +462,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       t0 = t1;
       t1 = t2;
     }
-  } else if (warp == 1) {
+  } else if (warp == kTreeMma) {
     // ---- the MMAs.  The warp goes together, and one lane issues, by predicate: what the products take is then known to be the same
     // in every lane and stays in uniform registers, where the instructions want it.  An issue returns about when its
     // product begins, so the tensor cores wait for whatever is done between two products, and 170 cycles more to begin
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       __syncwarp();
       if (lane == 0) tree_arrive(&sh.q_full[buf]);
     }
-  } else {
+  } else if (warp >= kTreeSoftmax) {
     // ---- softmax: group gs, a row a thread
     const int gs = (warp - kTreeSoftmax) >> 2, quarter = warp & 3;  // a warp reads the tensor memory lanes of its quarter
     const int row = quarter * 32 + lane;
@@ -876,18 +878,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   // Where a wait ran out (only here, where every role is done, is it known), copies and products may be in flight: they end
   // before the CTA gives back its shared and its tensor memory.  (Else the last commit of all has been waited for.)
   if (*(volatile int*)&sh.abort) {
-    if (warp == 1) {
+    if (warp == kTreeMma) {
       tree_commit(&sh.drain, elected());
       __syncwarp();
       mbar_wait_bounded(&sh.drain, 0);
     }
-    if (warp == 0) {
+    if (warp == kTreeTma) {
       for (uint32_t x = k_sent > 8 ? k_sent - 8 : 0; x < k_sent; ++x) mbar_wait_bounded(&sh.k_full[x & 7], x >> 3 & 1);
       for (uint32_t x = v_sent > 8 ? v_sent - 8 : 0; x < v_sent; ++x) mbar_wait_bounded(&sh.v_full[x & 7], x >> 3 & 1);
     }
     __syncthreads();
   }
-  if (warp == 1) {
+  if (warp == kTreeMma) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTreeTmem));
   }
