@@ -79,7 +79,7 @@ constexpr int kTreeTile = 128;                 // tokens of a tile, rows of a bl
 // Warps 4 .. 11 are the softmax groups, warp w with the rows of quarter w % 4, which also is the quarter of the SM it runs on.  The
 // warp of the MMAs, which sets the pace, shares its own with the rows that are there last, as the TMA's nearly does.
 constexpr int kTreeThreads = 384;
-constexpr int kTreeQueries = 1, kTreeTma = 2, kTreeMma = 3, kTreeSoftmax = 4;
+constexpr int kTreeTmaV = 0, kTreeQueries = 1, kTreeTmaK = 2, kTreeMma = 3, kTreeSoftmax = 4;
 constexpr int kMaxTreeCtas = 160;              // upper bound of the grid (sizes the workspace)
 constexpr int kTreePartHead = 4;               // a partial: [m, l, -, -, o[D]]
 constexpr uint32_t kTreeTmem = 512;            // columns: S of either group, then O of either
@@ -88,15 +88,20 @@ constexpr uint32_t kTreeTmem = 512;            // columns: S of either group, th
 constexpr int kTreeWhole = 4;
 constexpr int kTreeEven = 3;
 
+// slots of the rings of keys and of values
 template <int D>
-__host__ __device__ constexpr int tree_slots() { return D == 128 ? 5 : 8; }
+__host__ __device__ constexpr int tree_k_slots() { return D == 128 ? 3 : 4; }
+template <int D>
+__host__ __device__ constexpr int tree_v_slots() { return D == 128 ? 2 : 4; }
+template <int D>
+__host__ __device__ constexpr int tree_slots() { return tree_k_slots<D>() + tree_v_slots<D>(); }
 template <int D>
 __host__ __device__ constexpr uint32_t tree_slot_bytes() { return kTreeTile * D * 2; }
 
 struct TreeShared {
   // A tile's keys and values are there (by tile, as the groups each see every other tile of SPLIT, and a barrier's phases
-  // can be told by their parity only by one that follows them all); a slot of the ring is free.
-  uint64_t k_full[8], v_full[8], empty[8];
+  // can be told by their parity only by one that follows them all); a slot of the rings is free.
+  uint64_t k_full[8], v_full[8], empty[8];  // (keys' slots, then values')
   uint64_t s_full[2], p_full[2];    // a group's logits are there, its weights are
   uint64_t o_done[2];               // its last product of a unit
   uint64_t q_full[2], q_empty[2];   // queries
@@ -117,16 +122,10 @@ constexpr size_t tree_smem() {
 }
 static_assert(tree_smem<128>() <= 232448, "more shared memory than a CTA can have");
 
-// Descriptor of an MN-major, 128B-swizzled tile (values: rows are tokens, the product's K): 64-column halves `half` bytes
-// apart (leading offset), groups of 8 rows 1024 bytes apart (stride offset).
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t half) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(half >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
+// Words of a 128B-swizzled tile's descriptor, but for its address: 64-column halves `lead` bytes apart (read for an MN-major tile, as
+// the values are: rows are tokens, the product's K), groups of 8 rows `stride` bytes apart; version 1, SWIZZLE_128B.
+__device__ __forceinline__ uint32_t desc_low(uint32_t lead) { return (lead >> 4) << 16; }
+__device__ __forceinline__ uint32_t desc_high(uint32_t stride) { return stride >> 4 | 1u << 14 | 2u << 29; }
 
 __device__ __forceinline__ void tm_ld32(uint32_t (&r)[32], uint32_t addr) {
   asm volatile(
@@ -269,7 +268,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 template <bool BF, int D, bool PAIR>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const uint16_t* __restrict__ q,
-    const uint16_t* __restrict__ V, const TreeShape a, const int box, uint16_t* __restrict__ out, float* __restrict__ lse,
+    const uint16_t* __restrict__ V, const TreeShape a, const int box, const int fat, uint16_t* __restrict__ out, float* __restrict__ lse,
     float* __restrict__ part, int4* __restrict__ info, int* err) {
   constexpr int NS = tree_slots<D>(), RU = PAIR ? 2 * kTreeTile : kTreeTile;
   constexpr uint32_t kSlot = tree_slot_bytes<D>(), kHalf = kTreeTile * 128;
@@ -385,13 +384,17 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   __syncthreads();
   w.start(a, sh.start_r, sh.start_off, r1 - r0);
   const uint32_t most_iters = (uint32_t)kDefaultWaitIters;
-  uint32_t it = 0, k_sent = 0, v_sent = 0;  // the producer's slots; tiles whose keys and values it has sent for
+  uint32_t sent = 0;  // tiles whose keys (or values) have been sent for
 
-  if (warp == kTreeTma) {
-    // ---- tiles.  Lane i moves box i / halves, half i % halves; a page's number is read two tiles ahead of its keys.
-    constexpr int H = D / 64;
-    const int box_at = lane / H * box, col = lane % H;
-    const uint32_t box_bytes = (uint32_t)box * 128;
+  if (warp == kTreeTmaK || warp == kTreeTmaV) {
+    // ---- tiles, a warp the keys and a warp the values (a copy's issue takes 130 cycles, whatever it moves: pages of 16 rows
+    // 112 -> 97 us, of 8 rows 159 -> 99, for 131072 tokens, 64 rows).  A lane moves a box; a page's number is read a tile ahead.
+    const bool values = warp == kTreeTmaV, thin = values || fat;
+    const int halves = thin ? 1 : D / 64, box_at = lane / halves * box, col = lane % halves;
+    const uint32_t box_bytes = (uint32_t)box * (thin ? D * 2 : 128);
+    const int slots = values ? tree_v_slots<D>() : tree_k_slots<D>();
+    uint64_t *bars = values ? sh.v_full : sh.k_full, *free_bars = values ? sh.empty + tree_k_slots<D>() : sh.empty;
+    unsigned char* at_ring = ring + (values ? tree_k_slots<D>() * kSlot : 0u) + (thin ? box_at * D * 2 : col * kHalf + box_at * 128);
     struct Tile {
       int token0, L, hk, id;
       bool is;
@@ -413,11 +416,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       }
       return t;
     };
-    // a tile's keys or values into the ring's next slot; false when the CTA gives up
-    auto load = [&](const Tile& t, bool values) -> bool {
-      const uint32_t st = it % NS;
-      uint64_t* bar = values ? &sh.v_full[v_sent & 7] : &sh.k_full[k_sent & 7];
-      if (it >= NS && !tree_wait(&sh.empty[st], (it / NS - 1) & 1, &sh.abort, most_iters, err)) return false;
+    int slot = 0, round = 0;
+    Tile t = fetch();
+    while (t.is) {
+      const Tile next = fetch();
+      if (round > 0 && !tree_wait(&free_bars[slot], (round - 1) & 1, &sh.abort, most_iters, err)) break;
       const int token = t.token0 + box_at;
       const bool want = box_at < kTreeTile && token < t.L, ok = want && t.id >= 0 && t.id < a.n_pages;
       const unsigned moving = __ballot_sync(0xffffffffu, ok), bad = __ballot_sync(0xffffffffu, want && !ok);
@@ -430,37 +433,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           if (bad) {
             raise_error(err, IG_DEVERR_INDEX);
             for (unsigned m = bad; m; m &= m - 1) {
-              const int b = (__ffs(m) - 1) / H * box;
+              const int b = (__ffs(m) - 1) / halves * box;
               for (int i = 0; i < box; i += 8) v[(b + i) >> 5] &= ~(0xffu << ((b + i) & 31));
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sh.valid[k_sent & 7][i] = v[i];
+          for (int i = 0; i < 4; ++i) sh.valid[sent & 7][i] = v[i];
         }
-        mbar_arrive_expect_tx(bar, (uint32_t)__popc(moving) * box_bytes);
+        mbar_arrive_expect_tx(&bars[sent & 7], (uint32_t)__popc(moving) * box_bytes);
       }
       __syncwarp();
-      if (ok)
-        tma_load_2d(ring + st * kSlot + col * kHalf + box_at * 128, values ? &map_v : &map_k, col * 64,
-                    (t.id * a.Hkv + t.hk) * a.page + token % a.page, bar);
-      ++it;
-      if (values) ++v_sent;
-      else ++k_sent;
-      return true;
-    };
-    Tile t0 = fetch(), t1 = fetch();
-    bool going = t0.is && load(t0, false);
-    while (going && t0.is) {
-      const Tile t2 = fetch();
-      if constexpr (PAIR) {
-        going = load(t0, true) && (!t1.is || load(t1, false));
-      } else {
-        if (t1.is) going = load(t1, false);
-        else ++it;  // (a slot left out keeps the order)
-        going = going && load(t0, true);
+      if (ok) {
+        const int y = (t.id * a.Hkv + t.hk) * a.page + token % a.page;
+        if (thin) tma_load_3d(at_ring + slot * kSlot, values ? &map_v : &map_k, 0, y, 0, &bars[sent & 7]);
+        else tma_load_2d(at_ring + slot * kSlot, &map_k, col * 64, y, &bars[sent & 7]);
       }
-      t0 = t1;
-      t1 = t2;
+      ++sent;
+      if (++slot == slots) {
+        slot = 0;
+        ++round;
+      }
+      t = next;
     }
   } else if (warp == kTreeMma) {
     // ---- the MMAs.  The warp goes together, and one lane issues, by predicate: what the products take is then known to be the same
@@ -472,43 +465,48 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     uint32_t p_seen0 = 0, p_seen1 = 0;
     bool ok = true;
     const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(sq);
-    const uint32_t desc_hi = (uint32_t)(sw128_desc(0) >> 32), desc_lo = (uint32_t)sw128_desc(0), mn_lo = (uint32_t)sw128_desc_mn(0, kHalf);
+    // queries lie by halves; keys too, or box by box (boxes of 8: a group of rows a box); values box by box
+    const uint32_t q_high = desc_high(1024), k_high = desc_high(fat && box == 8 ? 16 * D : 1024), v_high = desc_high(box == 8 ? 16 * D : 1024);
+    const uint32_t low = desc_low(16), v_low = desc_low((uint32_t)box * 128), k_half = fat ? (uint32_t)box * 128 >> 4 : kHalf >> 4;
+    uint32_t v_step[kTreeTile / 16];  // where 16 tokens begin
+#pragma unroll
+    for (int ks = 0; ks < kTreeTile / 16; ++ks) v_step[ks] = (16 * ks / box * box * D * 2 + 16 * ks % box * 128) >> 4;
     const uint32_t tm = (uint32_t)uniform((int)tmem);
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return tree_wait(bar, parity, &sh.abort, most_iters, err); };
     // S of group g from queries at qa and the keys in a slot
     auto logits = [&](uint32_t g, uint32_t qa, uint32_t slot) {
-      const uint32_t ad = desc_lo + (qa >> 4), bd = desc_lo + ((ring_at + slot * kSlot) >> 4);
+      const uint32_t ad = low + (qa >> 4), bd = low + ((ring_at + slot * kSlot) >> 4);
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t o = (ks / 4) * (kHalf >> 4) + (ks % 4) * 2;
+      for (int ks = 0; ks < D / 16; ++ks)
         asm volatile(
-            "{\n .reg .pred p, q;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
+            "{\n .reg .pred p, q;\n .reg .b64 da, db;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %7};\n setp.ne.b32 p, %4, 0;\n"
             " setp.ne.b32 q, %6, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(tm + g * kTreeTile),
-            "r"(ad + o), "r"(bd + o), "r"(kIdS), "r"(ks), "r"(desc_hi), "r"(lead));
-      }
+            "r"(ad + ks / 4 * (kHalf >> 4) + ks % 4 * 2), "r"(bd + ks / 4 * k_half + ks % 4 * 2), "r"(kIdS), "r"(ks), "r"(q_high),
+            "r"(lead), "r"(k_high));
       tree_commit(&sh.s_full[g], lead);
     };
     // O of group g, from its weights and the values in a slot
     auto values = [&](uint32_t g, uint32_t slot, uint32_t more) {
-      const uint32_t bd = mn_lo + ((ring_at + slot * kSlot) >> 4);
+      const uint32_t bd = v_low + ((ring_at + (tree_k_slots<D>() + slot) * kSlot) >> 4);
 #pragma unroll
       for (int ks = 0; ks < kTreeTile / 16; ++ks)
         asm volatile(
             "{\n .reg .pred p, q;\n .reg .b64 db;\n mov.b64 db, {%2, %5};\n setp.ne.b32 p, %4, 0;\n"
             " setp.ne.b32 q, %6, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(
                 tm + (2 + g) * kTreeTile),
-            "r"(tm + g * kTreeTile + ks * 8), "r"(bd + ks * 128), "r"(kIdO), "r"(more | (uint32_t)ks), "r"(desc_hi), "r"(lead));
+            "r"(tm + g * kTreeTile + ks * 8), "r"(bd + v_step[ks]), "r"(kIdO), "r"(more | (uint32_t)ks), "r"(v_high), "r"(lead));
     };
     auto weights = [&](uint32_t g) -> bool {
       const uint32_t parity = (g ? p_seen1++ : p_seen0++) & 1;
       return wait(&sh.p_full[g], parity);
     };
-    // the ring's slots, two further each time
-    auto step = [&](uint32_t slot) -> uint32_t { return slot + 2 < NS ? slot + 2 : slot + 2 - NS; };
+    constexpr uint32_t NK = tree_k_slots<D>(), NV = tree_v_slots<D>();
+    uint64_t* v_empty = sh.empty + NK;
+    uint32_t k_slot = 0, v_slot = 0;  // of the next keys and values
+    auto step = [](uint32_t& slot, uint32_t n) { slot = slot + 1 < n ? slot + 1 : 0; };
     if constexpr (!PAIR) {
       // logits of a tile ahead of the values of the one before; tile i is of group i & 1
-      uint32_t i = 0, seg = 0, k_slot = 0;  // tile whose logits are next, its unit and its keys' slot
-      uint32_t j = 0, v_slot = 2 % NS;
+      uint32_t i = 0, seg = 0, j = 0;       // tile whose logits are next, its unit; tile whose values are
       TreeWalk v = w;                       // of the values
       int left = uniform(w.left), v_left = left;
       int seg_run = left > 0 ? uniform(w.run()) : 0, seg_at = 0, run = seg_run, k = 0;
@@ -521,7 +519,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           tc_fence_after();
           logits(i & 1, q_at + buf * kSlot, k_slot);
           tree_commit(&sh.empty[k_slot], lead);
-          k_slot = i == 0 ? 1 : step(k_slot);
+          step(k_slot, NK);
           ++i;
           if (++seg_at == seg_run) {
             tree_commit(&sh.q_empty[buf], lead);
@@ -541,9 +539,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         if (!ok) break;
         tc_fence_after();
         values(g, v_slot, k >= 2);
-        tree_commit(&sh.empty[v_slot], lead);
+        tree_commit(&v_empty[v_slot], lead);
         if (k >= run - 2) tree_commit(&sh.o_done[g], lead);
-        v_slot = step(v_slot);
+        step(v_slot, NV);
         ++j;
         if (++k == run) {
           v.next(a);
@@ -554,7 +552,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       }
     } else {
       // a tile's values and the next tile's logits, group by group; a unit begins with logits alone
-      uint32_t j = 0, k_slot = 0, v_slot = 1;
+      uint32_t j = 0;
       for (uint32_t seg = 0; ok && uniform(w.left) > 0; w.next(a), ++seg) {
         const int run = uniform(w.run()), rows = uniform(w.x.n * a.G - w.u % w.blocks * RU);
         const uint32_t groups = rows > kTreeTile ? 2 : 1;
@@ -563,7 +561,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         tc_fence_after();
         for (uint32_t g = 0; g < groups; ++g) logits(g, q_at + g * kSlot, k_slot);
         tree_commit(&sh.empty[k_slot], lead);
-        k_slot = step(k_slot);
+        step(k_slot, NK);
         if (run == 1) tree_commit(&sh.q_empty[0], lead);
         for (int k = 0; k < run; ++k, ++j) {
           const bool next = k < run - 1;
@@ -576,18 +574,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
             if (next) {
               logits(g, q_at + g * kSlot, k_slot);
             } else {
-              if (g == groups - 1) tree_commit(&sh.empty[v_slot], lead);
+              if (g == groups - 1) tree_commit(&v_empty[v_slot], lead);
               tree_commit(&sh.o_done[g], lead);  // (the unit's last: what comes before it has come when it is seen)
             }
           }
           if (!ok) break;
           if (next) {
-            tree_commit(&sh.empty[v_slot], lead);
+            tree_commit(&v_empty[v_slot], lead);
             tree_commit(&sh.empty[k_slot], lead);
             if (k == run - 2) tree_commit(&sh.q_empty[0], lead);
-            k_slot = step(k_slot);
+            step(k_slot, NK);
           }
-          v_slot = step(v_slot);
+          step(v_slot, NV);
         }
       }
     }
@@ -727,24 +725,25 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         }
         if (!plain && (!PAIR || gs == 0)) {
           // values without a token are cleared, and what is not finite in drafted ones: a row of the tile a thread
-          const uint32_t vi = PAIR ? 2 * j + 1 : 2 * j + 2;
           ok = tree_wait(&sh.v_full[j & 7], j >> 3 & 1, &sh.abort, most_iters, err);
           if (!ok) break;
-          uint4* vr = reinterpret_cast<uint4*>(ring + vi % NS * kSlot + row * 128);
+          uint4* vr = reinterpret_cast<uint4*>(ring + (tree_k_slots<D>() + j % tree_v_slots<D>()) * kSlot + row / box * box * D * 2 +
+                                               row % box * 128);
+          const int vh = box * 8;  // to the row's other half
           if (!(va[quarter] >> lane & 1)) {
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) vr[c / 8 * (kHalf / 16) + c % 8] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 8; ++c) vr[c / 8 * vh + c % 8] = make_uint4(0, 0, 0, 0);
           } else if (t0 + row >= drafted) {
             uint32_t odd = 0;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
-              const uint4 y = vr[c / 8 * (kHalf / 16) + c % 8];
+              const uint4 y = vr[c / 8 * vh + c % 8];
               odd |= odd_pair<BF>(y.x) | odd_pair<BF>(y.y) | odd_pair<BF>(y.z) | odd_pair<BF>(y.w);
             }
             if (odd) {
               uint16_t* e = reinterpret_cast<uint16_t*>(vr);
               for (int c = 0; c < D; ++c) {
-                uint16_t& y = e[c / 64 * (kHalf / 2) + c % 64];
+                uint16_t& y = e[c / 64 * vh * 8 + c % 64];
                 if (odd_pair<BF>(y)) y = 0;
               }
               *(volatile int*)&sh.poison[seg & 7] = (int)seg + 1;
@@ -883,10 +882,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       __syncwarp();
       mbar_wait_bounded(&sh.drain, 0);
     }
-    if (warp == kTreeTma) {
-      for (uint32_t x = k_sent > 8 ? k_sent - 8 : 0; x < k_sent; ++x) mbar_wait_bounded(&sh.k_full[x & 7], x >> 3 & 1);
-      for (uint32_t x = v_sent > 8 ? v_sent - 8 : 0; x < v_sent; ++x) mbar_wait_bounded(&sh.v_full[x & 7], x >> 3 & 1);
-    }
+    if (warp == kTreeTmaK || warp == kTreeTmaV)
+      for (uint32_t x = sent > 8 ? sent - 8 : 0; x < sent; ++x)
+        mbar_wait_bounded(warp == kTreeTmaV ? &sh.v_full[x & 7] : &sh.k_full[x & 7], x >> 3 & 1);
     __syncthreads();
   }
   if (warp == kTreeMma) {
@@ -1023,9 +1021,12 @@ ig_status launch_tree(cudaStream_t st, const TreeShape& a, const uint16_t* q, co
   IG_REQUIRE(most < 2147483648.0, "n*max_pages*page*Hq is too large: %.0f tiles", most);
   int box = kTreeTile;
   while (a.page % box) box >>= 1;
+  // Values lie box by box, both halves of its columns in one copy: their product takes 16 rows at a time, wherever they are.  Keys' 128
+  // rows have to lie evenly, so theirs do so where a box is a tile or a group of 8 rows, else a half a copy.
+  const int fat = D == 64 || box == 8 || box == kTreeTile ? 1 : 0, rows = a.n_pages * a.Hkv * a.page;
   CUtensorMap mk, mv;
-  ig_status r = make_map(&mk, K, a.n_pages * a.Hkv * a.page, D, box);
-  if (r == IG_OK) r = make_map(&mv, V, a.n_pages * a.Hkv * a.page, D, box);
+  ig_status r = fat ? make_map_halves(&mk, K, rows, D, box) : make_map(&mk, K, rows, D, box);
+  if (r == IG_OK) r = make_map_halves(&mv, V, rows, D, box);
   if (r != IG_OK) return r;
   constexpr size_t smem = tree_smem<D>();
   cudaError_t e = cudaFuncSetAttribute(k_tree_attend<BF, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -1035,17 +1036,17 @@ ig_status launch_tree(cudaStream_t st, const TreeShape& a, const uint16_t* q, co
   if (grid > most) grid = (int)most;
   float* part = static_cast<float*>(ws);
   int4* info = reinterpret_cast<int4*>(static_cast<char*>(ws) + tree_part_bytes(RU, D));
-  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, out, lse, part, info,
+  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, fat, out, lse, part, info,
                  error_word());
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   IG_CHECK_LAUNCH("tree attention launch");
   if (grid == 1 || ((double)a.B * a.Hkv * blocks <= grid && tiles <= kTreeWhole)) return IG_OK;  // nothing can have been cut
-  const int rows = (long long)a.T_max * a.G < RU ? a.T_max * a.G : RU;
+  const int used = (long long)a.T_max * a.G < RU ? a.T_max * a.G : RU;
   const float* cpart = part;
   const int4* cinfo = info;
   const double partials = grid / ((double)a.B * a.Hkv * blocks);  // of a unit, about
 #define IG_TJ(WPR, RB)                                                                                                     \
-  e = launch_pdl(k_tree_join<BF, D, WPR, RB>, dim3(grid, (rows + RB - 1) / RB), dim3(WPR * RB * 32), 0, st, cpart, cinfo, a, RU, out, \
+  e = launch_pdl(k_tree_join<BF, D, WPR, RB>, dim3(grid, (used + RB - 1) / RB), dim3(WPR * RB * 32), 0, st, cpart, cinfo, a, RU, out, \
                  lse)
   if (partials >= 16) IG_TJ(4, 1);
   else IG_TJ(1, 4);
