@@ -7,7 +7,7 @@ namespace {
 constexpr int kMaxRequests = 8192;  // prefix sums in shared memory
 constexpr int kMaxTree = 64;        // drafted tokens of a request: bits of a mask
 constexpr int kSlotThreads = 256;
-constexpr int kSlotTokens = 4;      // of a thread
+constexpr int kSlotTokens = 1;      // of a thread, as long as four CTAs an SM have room
 
 struct SlotArgs {
   int n, seqs, page, n_pages, max_pages, T;
