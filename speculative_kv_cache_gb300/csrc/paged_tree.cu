@@ -81,7 +81,7 @@ constexpr int kTreeTile = 128;                 // tokens of a tile, rows of a bl
 constexpr int kTreeThreads = 384;
 constexpr int kTreeTmaV = 0, kTreeQueries = 1, kTreeTmaK = 2, kTreeMma = 3, kTreeSoftmax = 4;
 constexpr int kMaxTreeCtas = 160;              // upper bound of the grid (sizes the workspace)
-constexpr int kTreePartHead = 4;               // a partial: [m, l, -, -, o[D]]
+constexpr int kTreePartHead = 8;               // a partial: [m, l, -.., o[D]] (o in whole sectors)
 constexpr uint32_t kTreeTmem = 512;            // columns: S of either group, then O of either
 // Units that could have a CTA each are not cut where the longest has at most kTreeWhole tiles, or where there are enough
 // of them to keep HBM busy and the longest is at most kTreeEven tiles above the mean.
@@ -268,7 +268,7 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 template <bool BF, int D, bool PAIR>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const uint16_t* __restrict__ q,
-    const uint16_t* __restrict__ V, const TreeShape a, const int box, const int fat, uint16_t* __restrict__ out, float* __restrict__ lse,
+    const uint16_t* __restrict__ V, const TreeShape a, const int box, const int fat, const int most_blocks, uint16_t* __restrict__ out, float* __restrict__ lse,
     float* __restrict__ part, int4* __restrict__ info, int* err) {
   constexpr int NS = tree_slots<D>(), RU = PAIR ? 2 * kTreeTile : kTreeTile;
   constexpr uint32_t kSlot = tree_slot_bytes<D>(), kHalf = kTreeTile * 128;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     sh.scan[warp][1] = units_in;
     sh.scan[warp][2] = longest;
   }
-  if (threadIdx.x == 0) info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !most_blocks) info[blockIdx.x] = make_int4(-1, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -861,13 +861,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         __syncwarp();
         if (lane == 0) tree_arrive(&sh.o_free[1 - gs]);
       }
-      // what the second kernel joins: a unit that begins here and goes on in later CTAs
-      if (cut && row == 0 && (!PAIR || gs == 0)) {
-        const int end = r1 - left + nt - 1;  // its last tile: a cut unit is this CTA's last, `left` tiles long here
-        int last = min(ctas - 1, (int)((float)end * ((float)ctas / (float)total)));  // within 1
-        while (last + 1 < ctas && first_of(last + 1) <= end) ++last;
-        while (first_of(last) > end) --last;
-        info[cta] = make_int4(unit_r, unit_u, last, 0);
+      // what the second kernel joins: a unit that begins here and goes on in later CTAs (listed by unit, where there are fewer
+      // than CTAs, finished ones too; else by the CTA that it begins in)
+      if ((cut || (most_blocks && done)) && row == 0 && (!PAIR || gs == 0)) {
+        int last = cta;
+        if (cut) {
+          const int end = r1 - left + nt - 1;  // its last tile: a cut unit is this CTA's last, `left` tiles long here
+          last = min(ctas - 1, (int)((float)end * ((float)ctas / (float)total)));  // within 1
+          while (last + 1 < ctas && first_of(last + 1) <= end) ++last;
+          while (first_of(last) > end) --last;
+        }
+        if (most_blocks) info[(unit_r * a.Hkv + hk) * most_blocks + block] = make_int4(cut ? cta : -1, 0, last, 0);
+        else info[cta] = make_int4(unit_r, unit_u, last, 0);
       }
       at_tile += run;
     }
@@ -893,22 +898,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   }
 }
 
-// Joins the partials of the units that were cut: block (x, y) takes the unit that CTA x began and rows y * RB ... of it, WPR
-// warps a row; a warp takes every WPR-th partial in order, and the warps join in order.
+// Joins the partials of the units that were cut: block (x, y) takes unit x (or the one that CTA x began) and rows y * RB ... of it,
+// WPR warps a row (listed by CTA, 8 units of 128 rows in 152 CTAs take 19456 blocks, of which 1024 have anything to do: 12 us more); a warp takes every WPR-th partial in order, and the warps join in order.
 template <bool BF, int D, int WPR, int RB>
 __global__ void __launch_bounds__(WPR * RB * 32) k_tree_join(const float* __restrict__ part, const int4* __restrict__ info,
-                                                            const TreeShape a, int RU, uint16_t* __restrict__ out,
+                                                            const TreeShape a, int RU, int most_blocks, uint16_t* __restrict__ out,
                                                             float* __restrict__ lse) {
   constexpr int VEC = D / 32;
   __shared__ float sm[WPR * RB], sl[WPR * RB], so[WPR * RB][WPR > 1 ? D : 1];
   pdl_trigger();
   pdl_wait();
-  const int4 e = __ldca(info + blockIdx.x);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (e.x < 0) return;
-  const int c0 = blockIdx.x, n = e.z - c0 + 1;
-  const int f = __ldca(a.first + e.x), rows = (__ldca(a.first + e.x + 1) - f) * a.G, blocks = (rows + RU - 1) / RU;
-  const int hk = e.y / blocks, row = blockIdx.y * RB + warp / WPR, rr = e.y % blocks * RU + row;
+  TreeRequest x;
+  int c0, last, hk, block;
+  if (most_blocks) {
+    block = blockIdx.x % most_blocks, hk = blockIdx.x / most_blocks % a.Hkv;
+    // (units that there are have been listed, but for those of CTAs whose waits ran out)
+    if (!tree_request(a, blockIdx.x / most_blocks / a.Hkv, x) || block * RU >= x.n * a.G) return;
+    const int4 e = __ldca(info + blockIdx.x);
+    c0 = e.x, last = e.z;
+    if (c0 < 0 || last < c0 || last >= kMaxTreeCtas) return;
+  } else {
+    const int4 e = __ldca(info + blockIdx.x);
+    if (e.x < 0 || !tree_request(a, e.x, x)) return;
+    const int blocks = (x.n * a.G + RU - 1) / RU;
+    c0 = blockIdx.x, last = e.z, hk = e.y / blocks, block = e.y % blocks;
+  }
+  const int n = last - c0 + 1, f = x.f, rows = x.n * a.G, row = blockIdx.y * RB + warp / WPR, rr = block * RU + row;
   const bool live = row < RU && rr < rows;
   float m = -INFINITY, l = 0.f, o[VEC];
 #pragma unroll
@@ -1034,20 +1050,23 @@ ig_status launch_tree(cudaStream_t st, const TreeShape& a, const uint16_t* q, co
   int grid = sm_count(st);
   if (grid > kMaxTreeCtas) grid = kMaxTreeCtas;
   if (grid > most) grid = (int)most;
+  const double units = (double)a.B * a.Hkv * blocks;  // at most
+  const int most_blocks = units <= grid ? (int)blocks : 0;
   float* part = static_cast<float*>(ws);
   int4* info = reinterpret_cast<int4*>(static_cast<char*>(ws) + tree_part_bytes(RU, D));
-  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, fat, out, lse, part, info,
+  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, fat, most_blocks, out, lse, part, info,
                  error_word());
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   IG_CHECK_LAUNCH("tree attention launch");
-  if (grid == 1 || ((double)a.B * a.Hkv * blocks <= grid && tiles <= kTreeWhole)) return IG_OK;  // nothing can have been cut
+  if (grid == 1 || (most_blocks && tiles <= kTreeWhole)) return IG_OK;  // nothing can have been cut
   const int used = (long long)a.T_max * a.G < RU ? a.T_max * a.G : RU;
   const float* cpart = part;
   const int4* cinfo = info;
-  const double partials = grid / ((double)a.B * a.Hkv * blocks);  // of a unit, about
+  const double partials = grid / units;  // of a unit, about
+  const int list = most_blocks ? (int)units : grid;
 #define IG_TJ(WPR, RB)                                                                                                     \
-  e = launch_pdl(k_tree_join<BF, D, WPR, RB>, dim3(grid, (used + RB - 1) / RB), dim3(WPR * RB * 32), 0, st, cpart, cinfo, a, RU, out, \
-                 lse)
+  e = launch_pdl(k_tree_join<BF, D, WPR, RB>, dim3(list, (used + RB - 1) / RB), dim3(WPR * RB * 32), 0, st, cpart, cinfo, a, RU, \
+                 most_blocks, out, lse)
   if (partials >= 16) IG_TJ(4, 1);
   else IG_TJ(1, 4);
 #undef IG_TJ

@@ -1016,8 +1016,9 @@ def test_tree_short_waits_are_reported_and_leave_the_next_call_right(ig, limit, 
     ig.ig_check()
     ig.ig_set_wait_limit(limit)
     try:
-        for _ in range(3):
-            attend_tree(ig, c)
+        for fill in (0xff, 0, 1):
+            size = ig.ig_paged_tree_attend_workspace_bytes(c["B"], c["T_max"], c["Hq"], c["Hkv"], c["d"])
+            attend_tree(ig, c, ws=torch.full((size,), fill, dtype=torch.uint8, device=DEV))
         try:
             ig.ig_check()
             assert limit > 0  # logits may be there at the first probe
