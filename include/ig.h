@@ -66,7 +66,7 @@ int ig_version(void);
 ig_status ig_check(void* stream);
 
 /* Iteration limit of the score kernels' bounded waits for their staged copies (k2_scores,
- * k23_score_select), and of the paged attention's (k_paged_attend), on the current device: a wait
+ * k23_score_select), and of the paged attentions' (k_paged_attend, k_tree_attend), on the current device: a wait
  * that runs out records IG_DEVERR_TIMEOUT, the CTA then waits (with the fixed default limit) for its
  * copies in flight to land and leaves without scoring (the attention's output is then undefined),
  * and the next ig_check returns IG_ERR_TIMEOUT.  max_iters < 0
@@ -503,11 +503,12 @@ ig_status ig_paged_attend_picked(void* stream, int dtype, int B, int Hq, int Hkv
  * packed: request i's are first[i] .. first[i+1] - 1, n_i of them, the last n_i of the L_valid tokens of its sequence.  Token t
  * sees token j of its sequence when j < L - n_i, or when bit j - (L - n_i) of masks[t] is set; for each query head
  *   z_j = scale * q . K_j,  o = sum_j w_j V_j,  w = softmax over the tokens it sees,  lse = log(sum_j exp(z_j))
- * in one pass over K and V for up to 128 (two at a time: 256) queries of a key head; products in fp16/bf16 with fp32 sums, softmax in
- * fp32, the weights rounded to `dtype` for the second product (their sum is not), o rounded once.  In fp16, weights keep 11 bits down
- * to 2^-28 of the largest and fewer down to 2^-38.  A token that sees nothing has o = 0 and lse = -inf.  What the pages hold past a sequence's last
- * token, and in drafted rows that a token does not see, may be anything, NaN included; among what it sees, a logit
- * of -inf has weight zero, a logit that is NaN or +inf, or a value that is not finite, gives non-finite results.
+ * in one pass over K and V for 256 (drafted token, query head) pairs of a key head at a time; products in fp16/bf16 with
+ * fp32 sums, softmax in fp32, the weights rounded to `dtype` for the second product (their sum is not), o rounded
+ * once.  In fp16, weights keep 11 bits down to 2^-28 of the largest and fewer down to 2^-38.  A token that sees nothing
+ * has o = 0 and lse = -inf.  What the pages hold past a sequence's last token, and in drafted rows that a token does not
+ * see, may be anything, NaN included; among what it sees, a logit of -inf has weight zero, a logit that is NaN or +inf,
+ * or a value that is not finite, gives non-finite results.
  *   q           dev [T][Hq][d] of `dtype`, 16-byte aligned
  *   page_table  dev int32 [seqs][max_pages];  L_valid dev int32 [seqs]: as for ig_paged_attend
  *   seq         dev int32 [n]: the requests' sequences, or NULL (request i is sequence i)
@@ -542,25 +543,26 @@ ig_status ig_paged_tree_attend(void* stream, int dtype, int n, int T, int T_max,
  *   parents     dev int32 [T]: the parent of each token among the new tokens of its request, a lower number than its own, or
  *               -1 (it follows the sequence's earlier tokens); NULL: each follows the one before it
  *   first       dev int32 [n + 1] out;  slots, positions dev int32 [T] out;  masks dev uint64 [T] out, or NULL
- * A request that cannot be (a sequence or length out of range, a negative count, more tokens than its sequence has, tokens past T, with
- * parents or masks more than 64) sets IG_DEVERR_INDEX and its tokens get slot -1, position 0, mask 0; so does a page
- * number out of range for the slot alone, and a parent out of range, which counts as -1.  first never exceeds T.
- * 1 <= n <= 8192; T >= 0; page a positive multiple of 8; max_pages * page < 2^30, n_pages * page < 2^31.
+ * A request that cannot be (a sequence or length out of range, a negative count, more tokens than its sequence has, tokens
+ * past T, with parents or masks more than 64) sets IG_DEVERR_INDEX and its tokens get slot -1, position 0, mask 0; so
+ * does a page number out of range for the slot alone, and a parent out of range, which counts as -1.  first never
+ * exceeds T.  (A request of no tokens is not looked at.)
+ * 1 <= n <= 8192; 0 <= T < 2^30; page a positive multiple of 8; max_pages * page < 2^30, n_pages * page < 2^31.
  * (Outputs and inputs must not overlap.) */
 ig_status ig_page_slots(void* stream, int n, int seqs, int page, int n_pages, int max_pages, int T,
                         const int32_t* page_table, const int32_t* L_valid, const int32_t* seq,
                         const int32_t* counts, const int32_t* parents, int32_t* first, int32_t* slots,
                         int32_t* positions, uint64_t* masks);
 
-/* Of each request's drafted tokens the ones that are kept, moved to the front of them in every layer: row path[first[i] + k] of the drafted
- * rows goes to row k, for k < kept[i], for every head of K and V.  (The caller then cuts the sequence back to
- * L - n_i + kept[i] tokens: ig_pages_truncate.)
+/* Of each request's drafted tokens the ones that are kept, moved to the front of them in every layer: row
+ * path[first[i] + k] of the drafted rows goes to row k, for k < kept[i], for every head of K and V.  (The caller then cuts
+ * the sequence back to L - n_i + kept[i] tokens: ig_pages_truncate.)
  *   K, V    host arrays [layers] of dev pages [n_pages][Hkv][page][d] (16-bit elements of any type)
- *   page_table, L_valid, seq, first  as for ig_paged_tree_attend (L_valid with the drafted tokens); no sequence twice, and no other
- *           sequence shares the pages of the drafted rows (ig_pages_extend sees to that)
+ *   page_table, L_valid, seq, first  as for ig_paged_tree_attend (L_valid with the drafted tokens); no sequence twice, and
+ *           no other sequence shares the pages of the drafted rows (ig_pages_extend sees to that)
  *   path    dev int32 [T]: from first[i] on, request i's kept tokens, ascending;  kept dev int32 [n]
- * A request with a number out of range, more than 64 drafted tokens or a path that does not ascend sets IG_DEVERR_INDEX, and none
- * of its rows move.  At most 128 layers per call; d a multiple of 8; n >= 0 (0: nothing is done);
+ * A request with a number out of range, more than 64 drafted tokens or a path that does not ascend sets IG_DEVERR_INDEX,
+ * and none of its rows move.  At most 128 layers per call; d a multiple of 8; n >= 0 (0: nothing is done);
  * max_pages * page < 2^30, n_pages * Hkv * page < 2^31. */
 ig_status ig_tree_keep(void* stream, int layers, int n_pages, int Hkv, int page, int d,
                        uint16_t* const* K, uint16_t* const* V, int n, int seqs, int max_pages, int T,

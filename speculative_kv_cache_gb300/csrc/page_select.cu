@@ -21,7 +21,7 @@ __device__ __forceinline__ int unit_exponent(float most) {
   return max(e, -126);  // (a number that is not normal lies far below 127 * 2^-126)
 }
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
-// x in units of 2^e, exact but for what lies below a float's range (e <= 121)
+// x in units of 2^e, exact but for what lies below a float's range (e <= 122)
 __device__ __forceinline__ float in_units(float x, int e) { return x * power_of_two(-e); }
 
 template <bool BF>
@@ -57,7 +57,8 @@ constexpr int kBoundsThreads = 256;
 constexpr int kBoundsFly = 4;  // rows of a lane in flight
 
 // A warp a page and head: D/8 lanes hold a row's 16-byte pieces, so that 2 (or 4) rows go at a time; minima and
-// maxima in packed 16-bit form, exact.  Bound by HBM: the keys once.
+// maxima in packed 16-bit form, exact.  Bound by HBM, the keys once: 4000 pages of 16 rows, 8 heads of 128 (139 MB) 24.2 us,
+// 5.75 TB/s, 0.85 of the copy rate; 64 pages of 32 rows 3.4 us.
 template <bool BF, int D>
 __global__ void __launch_bounds__(kBoundsThreads) k_page_bounds(const uint4* __restrict__ K, int n_pages, int Hkv, int page, int n,
                                                                const int32_t* __restrict__ list, uint2* __restrict__ codes,
@@ -149,6 +150,7 @@ constexpr int kSelThreads = 256;
 constexpr int kMaxCluster = 16, kPortableCluster = 8;
 constexpr int kMaxGroup = 256;        // queries of a key head
 constexpr int kSelKeyBytes = 128 << 10;  // keys of a CTA's share, at most
+constexpr int kSelHalfBytes = 100 << 10; // what a CTA can have (beside 10 KB of its own) that shares an SM with another
 constexpr float kMostScore = 3.402823466e38f;
 
 struct SelArgs {
@@ -191,7 +193,11 @@ constexpr uint32_t kAlways = 0xffffffffu;
 // One cluster of CL CTAs a sequence and key head, each with a run of its pages: scores into shared memory, then the least key
 // that is taken, eight bits at a time from the first one in which the keys differ (histograms in shared memory, summed
 // over the cluster) until its bin is taken whole, then the pages above it, and of those equal to it the first, in
-// order.  Bound by latency: a page's number, its bounds, a few rounds through the cluster; U pages a thread's loads ahead.
+// order.  Bound by latency: a page's number, its bounds, a few rounds through the cluster (1600 cycles each); U pages a lane's
+// loads ahead.  8 rows of 8192 pages with 5 queries 13.7 us (17 MB of bounds, floor 2.5: 9100 cycles of 22500 are the
+// scores, 7300 the radix passes); 512 rows of up to 512 pages with 4 queries 14.6 us (floor 5); 64 pages of one sequence
+// 3.6 us.  Scores by mma.sync in fp16, exact as well, took longer (20.9 and 21.8 us), as did all keys sent to one CTA of the
+// cluster (20.4).
 template <bool BF, int D, int U>
 __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, int CL, int* err) {
   constexpr int LP = D / 32, PW = 32 / LP;  // lanes of a page (4 pieces of 16 bytes each), pages of a warp
@@ -463,13 +469,17 @@ ig_status launch_select_u(cudaStream_t st, const SelArgs& a, int CL, size_t smem
 template <bool BF, int D>
 ig_status launch_select(cudaStream_t st, SelArgs a) {
   // CTAs of a cluster: more where there are few rows, as long as each has 256 pages or more (not on a partition of the SMs,
-  // which need not have room for clusters side by side); and as many as the keys need
+  // which need not have room for clusters side by side; more than the portable number only where two CTAs share an SM, so that
+  // half as many SMs are enough); and as many as the keys need
   const long long rows = (long long)a.B * a.Hkv;
   auto share = [&](int CL) -> size_t { return (size_t)((a.max_pages + CL - 1) / CL); };
+  auto bytes = [&](int CL) -> size_t { return (size_t)a.G * (2 * D + 4) + share(CL) * 4; };
   int CL = 1;
-  while (CL < kMaxCluster && stream_sms(st) == 0 && rows * CL < sm_count(st) && a.max_pages / (2 * CL) >= 256) CL *= 2;
+  while (CL < kMaxCluster && stream_sms(st) == 0 && rows * CL < sm_count(st) && a.max_pages / (2 * CL) >= 256 &&
+         (CL < kPortableCluster || bytes(2 * CL) <= (size_t)kSelHalfBytes))
+    CL *= 2;
   while (CL < kPortableCluster && share(CL) * 4 > (size_t)kSelKeyBytes) CL *= 2;
-  const size_t smem = (size_t)a.G * (2 * D + 4) + share(CL) * 4;
+  const size_t smem = bytes(CL);
   return rows * CL > sm_count(st) ? launch_select_u<BF, D, 2>(st, a, CL, smem) : launch_select_u<BF, D, 4>(st, a, CL, smem);
 }
 

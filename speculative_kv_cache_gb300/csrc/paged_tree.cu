@@ -10,11 +10,11 @@
 // 280 rows and the tensor cores beyond.  Rows are the M = 128 of tcgen05.mma, tokens its N and the second product's K:
 //   S[rows][128 tokens] = Q K^T (both in shared memory),  O[rows][d] += P V (P in tensor memory, where S was).
 //
-// A CTA (one an SM): a warp moves tiles of 128 tokens with TMA into a ring, keys and values in turn, in the order they are used; one
-// thread issues the MMAs; a warp fetches the units' queries; two groups of four warps turn S into P, a row a thread, each
-// with S and O columns of its own, so that one works on its logits while the tensor cores work for the other.
-// Up to 128 rows the groups take tiles in turn and join their parts at the end (SPLIT); with more, a
-// unit is 256 rows, and each group has 128 of them and every tile (PAIR), which halves what is read.
+// A CTA (one an SM): a warp moves keys with TMA, 128 tokens a tile, through a ring, a warp values through a ring of theirs; a warp
+// issues the MMAs; a warp fetches the units' queries; two groups of four warps turn S into P, a row a thread, each with S and
+// O columns of its own, so that one works on its logits while the tensor cores work for the other.  Up to 128 rows the
+// groups take tiles in turn and join their parts at the end (SPLIT); with more, a unit is 256 rows, and each group has
+// 128 of them and every tile (PAIR), which halves what is read.
 //
 // Precision.  Weights are rounded to the type for the second product.  Fp16 has few exponents: the reference lies 2^14 below the
 // largest logit, so that weights keep their 11 bits down to 2^-28 of it.  The reference moves (and O is scaled by
@@ -28,6 +28,17 @@
 // Work split.  As in the attention of one token: all tiles of all units in order, cut in equal shares, one a CTA; a unit in
 // several CTAs leaves partials in the workspace (two slots a CTA: the unit it starts with, the unit it ends with), joined in
 // order by a second kernel.  No atomics: the result does not depend on timing.
+//
+// Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
+//   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 87 us with 16 rows (0.91 of the copy rate), 89 with
+//   64, 93 with 128, 126 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
+//   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 100 us, 0.82; the join, of 150 cuts, has 6 of them,
+//   and without any arithmetic of the softmax the rest takes as long.
+//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 149 us, 0.91 Pflop/s.  What is left is a group's chain of logits,
+//   weights and values: without exponentials and maxima 130, with an eighth of the products 127, without either 117.
+//   8 drafted tokens on 256, 4 key heads of 64: 8.4 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
+// Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
+// three values, no gain.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -268,8 +279,8 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 template <bool BF, int D, bool PAIR>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const uint16_t* __restrict__ q,
-    const uint16_t* __restrict__ V, const TreeShape a, const int box, const int fat, const int most_blocks, uint16_t* __restrict__ out, float* __restrict__ lse,
-    float* __restrict__ part, int4* __restrict__ info, int* err) {
+    const uint16_t* __restrict__ V, const TreeShape a, const int box, const int fat, const int most_blocks,
+    uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, int4* __restrict__ info, int* err) {
   constexpr int NS = tree_slots<D>(), RU = PAIR ? 2 * kTreeTile : kTreeTile;
   constexpr uint32_t kSlot = tree_slot_bytes<D>(), kHalf = kTreeTile * 128;
   // kind::f16, D fp32, A and B of the type; N >> 3 at bits 17-22, M >> 4 at bits 24-28; bit 16: B is MN-major
@@ -393,8 +404,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     const int halves = thin ? 1 : D / 64, box_at = lane / halves * box, col = lane % halves;
     const uint32_t box_bytes = (uint32_t)box * (thin ? D * 2 : 128);
     const int slots = values ? tree_v_slots<D>() : tree_k_slots<D>();
-    uint64_t *bars = values ? sh.v_full : sh.k_full, *free_bars = values ? sh.empty + tree_k_slots<D>() : sh.empty;
-    unsigned char* at_ring = ring + (values ? tree_k_slots<D>() * kSlot : 0u) + (thin ? box_at * D * 2 : col * kHalf + box_at * 128);
+    uint64_t* bars = values ? sh.v_full : sh.k_full;
+    uint64_t* free_bars = values ? sh.empty + tree_k_slots<D>() : sh.empty;
+    unsigned char* at_ring = ring + (values ? tree_k_slots<D>() * kSlot : 0u);
+    at_ring += thin ? box_at * D * 2 : col * kHalf + box_at * 128;
     struct Tile {
       int token0, L, hk, id;
       bool is;
@@ -466,8 +479,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     bool ok = true;
     const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(sq);
     // queries lie by halves; keys too, or box by box (boxes of 8: a group of rows a box); values box by box
-    const uint32_t q_high = desc_high(1024), k_high = desc_high(fat && box == 8 ? 16 * D : 1024), v_high = desc_high(box == 8 ? 16 * D : 1024);
-    const uint32_t low = desc_low(16), v_low = desc_low((uint32_t)box * 128), k_half = fat ? (uint32_t)box * 128 >> 4 : kHalf >> 4;
+    const uint32_t q_high = desc_high(1024), low = desc_low(16);
+    const uint32_t k_high = desc_high(fat && box == 8 ? 16 * D : 1024), k_half = fat ? (uint32_t)box * 128 >> 4 : kHalf >> 4;
+    const uint32_t v_high = desc_high(box == 8 ? 16 * D : 1024), v_low = desc_low((uint32_t)box * 128);
     uint32_t v_step[kTreeTile / 16];  // where 16 tokens begin
 #pragma unroll
     for (int ks = 0; ks < kTreeTile / 16; ++ks) v_step[ks] = (16 * ks / box * box * D * 2 + 16 * ks % box * 128) >> 4;
@@ -614,7 +628,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     const int gs = (warp - kTreeSoftmax) >> 2, quarter = warp & 3;  // a warp reads the tensor memory lanes of its quarter
     const int row = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_at = tmem + lanes + gs * kTreeTile, o_at = s_at + 2 * kTreeTile, o_other = tmem + lanes + 2 * kTreeTile + (1 - gs) * kTreeTile;
+    const uint32_t s_at = tmem + lanes + gs * kTreeTile, o_at = s_at + 2 * kTreeTile;
+    const uint32_t o_other = tmem + lanes + (3 - gs) * kTreeTile;
     const uint32_t limit = wait_limit(err);
     constexpr float kBelow = BF ? 0.f : 14.f, kAbove = BF ? 8.f : 15.f;  // of the reference: the largest weight, and what moves it
     const float sc = a.scale2 == 0.f ? 1.f : fabsf(a.scale2), sgn = a.scale2 > 0.f ? 1.f : a.scale2 < 0.f ? -1.f : 0.f;
@@ -899,7 +914,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
 }
 
 // Joins the partials of the units that were cut: block (x, y) takes unit x (or the one that CTA x began) and rows y * RB ... of it,
-// WPR warps a row (listed by CTA, 8 units of 128 rows in 152 CTAs take 19456 blocks, of which 1024 have anything to do: 12 us more); a warp takes every WPR-th partial in order, and the warps join in order.
+// WPR warps a row; a warp takes every WPR-th partial in order, and the warps join in order.  (Listed by CTA, 8 units of 128 rows
+// in 152 CTAs take 19456 blocks, of which 1024 have anything to do: 12 us more.)
 template <bool BF, int D, int WPR, int RB>
 __global__ void __launch_bounds__(WPR * RB * 32) k_tree_join(const float* __restrict__ part, const int4* __restrict__ info,
                                                             const TreeShape a, int RU, int most_blocks, uint16_t* __restrict__ out,
@@ -1054,8 +1070,8 @@ ig_status launch_tree(cudaStream_t st, const TreeShape& a, const uint16_t* q, co
   const int most_blocks = units <= grid ? (int)blocks : 0;
   float* part = static_cast<float*>(ws);
   int4* info = reinterpret_cast<int4*>(static_cast<char*>(ws) + tree_part_bytes(RU, D));
-  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, fat, most_blocks, out, lse, part, info,
-                 error_word());
+  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, fat, most_blocks, out,
+                 lse, part, info, error_word());
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   IG_CHECK_LAUNCH("tree attention launch");
   if (grid == 1 || (most_blocks && tiles <= kTreeWhole)) return IG_OK;  // nothing can have been cut

@@ -301,13 +301,16 @@ class PagedCache:
 
     @_on_its_gpu
     def summarise(self, layer):
-        """The bounds of ``layer``'s pages that have got tokens since the last time, from what the pages hold now."""
+        """The bounds of ``layer``'s pages that have got tokens since the last time, from what the pages hold now.  (Which ones is
+        decided on the host: not while a graph is captured, which would repeat that one list.)"""
         self._bounded()
         self._catch_up()
         seen = self._seen[layer]
         stale = np.nonzero(seen < self.L_host)[0]
         if not len(stale):
             return
+        if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+            raise ValueError("bounds are due, and a graph is being captured: summarise the layer before")
         made_for = (seen.tobytes(), self.L_host.tobytes(), self.table_host[stale].tobytes())
         if self._due[0] != made_for:
             ids, rows = [], []
@@ -329,7 +332,8 @@ class PagedCache:
     @_on_its_gpu
     def attend_picked(self, layer, q, picks, first=1, last=2, out=None, lse=None):
         """``attend`` over at most ``picks`` pages of each sequence and key head: its first ``first`` and last ``last`` ones, and
-        those whose bounds allow its queries the largest logits.  Bounds that are due are made first."""
+        those whose bounds allow its queries the largest logits.  Bounds that are due are made first; a captured call
+        replays with those that ``summarise`` has made since."""
         self._bounded()
         self._check("q", q, self.seqs, self.Hq, self.d)
         self._check("out", out, self.seqs, self.Hq, self.d, dtype=torch.float32)

@@ -323,6 +323,25 @@ def test_tree_splits_over_length_and_batch(ig, B, n, Hq, Hkv, d, page, dt, hi):
     ig.ig_check()
 
 
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("G,n", [(2, 64), (3, 43), (4, 64), (6, 43), (4, 32), (4, 33), (127, 1), (128, 1), (129, 1), (256, 1),
+                                 (257, 1), (256, 3), (17, 31)])
+def test_tree_rows_about_the_ends_of_blocks(ig, G, n, dt, d):
+    """A key head's rows, n G of them, at 128 and 256 and one past them, in short sequences and in one that many CTAs share."""
+    c = make_tree(21, dt, [n, 4001, n + 63, 300], [n, n, max(1, n - 1), n], 2 * G, 2, d, 32)
+    check_tree(c, *attend_tree(ig, c))
+    ig.ig_check()
+
+
+def test_tree_of_more_requests_than_threads(ig):
+    rng = np.random.default_rng(22)
+    lengths = [int(rng.integers(1, 40)) for _ in range(1000)]
+    drafted = [min(x, int(rng.integers(0, 4))) for x in lengths]
+    c = make_tree(22, "f16", lengths, drafted, 2, 1, 64, 8)
+    check_tree(c, *attend_tree(ig, c))
+    ig.ig_check()
+
+
 @pytest.mark.parametrize("G", [1, 4])
 @pytest.mark.parametrize("n", [1, 31, 32, 33, 63, 64])
 def test_tree_without_an_earlier_token_and_with_any_mask(ig, n, G):
@@ -773,6 +792,22 @@ def test_choice_of_a_very_long_table(ig):
     ig.ig_check()
 
 
+@pytest.mark.parametrize("d,Hq", [(64, 8), (64, 512), (128, 512)])
+def test_choice_with_the_most_keys_and_queries(ig, d, Hq):
+    """The longest table, whose pages repeat, with few queries a key head and with as many as there can be."""
+    c = make_picked(27, "f16", [8 * 2000], Hq, 2, d, 8)
+    bounds_of(ig, c)
+    scores = [np.tile(scores_of(c, 0, h), 132)[:262144] for h in range(2)]
+    c["table"] = c["table"].repeat(1, 132)[:, :262144].contiguous()
+    c["mp"], c["L"] = 262144, i32([262144 * 8 - 3])
+    chosen, tokens = select(ig, c, 700, 1, 2)
+    ig.ig_check()
+    for h in range(2):
+        rest = 1 + np.argsort(-scores[h][1:-2], kind="stable")[:697]
+        take = np.sort(np.concatenate([[0], rest, [262142, 262143]]))
+        assert torch.equal(chosen[0, h], c["table"][0, torch.from_numpy(take).to(DEV)]) and int(tokens[0, h]) == 700 * 8 - 3
+
+
 def test_choice_with_rows_that_are_not_finite_and_large_ones(ig):
     c = make_picked(4, "bf16", [1000, 1000], 4, 2, 64, 8)
     t = c["table"].tolist()
@@ -866,6 +901,79 @@ def test_choice_and_attention_replayed(ig):
 # ---------------------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------------------
+def test_on_a_partition_of_the_sms(ig):
+    """The same results, whatever the grid and the clusters: a tree's up to how its tiles are cut, a choice exactly."""
+    c = make_tree(23, "f16", [9000, 40, 700], [16, 9, 64], 8, 2, 128, 32)
+    p = make_picked(24, "bf16", [30000, 900], 8, 2, 64, 8)
+    bounds_of(ig, p)
+    want = select(ig, p, 50, 1, 2)
+    counts, up = i32([5, 0, 7]), i32(a_tree(np.random.default_rng(25), 5) + a_tree(np.random.default_rng(26), 7))
+    rows = i32(p["rows"])
+
+    def room():  # what a call writes; nothing is made or freed while another stream is at work
+        f, s, x = (torch.full((k,), -9, dtype=torch.int32, device=DEV) for k in (4, 12, 12))
+        return f, s, x, torch.full((12,), -9, dtype=torch.int64, device=DEV)
+
+    def slots(to, stream=None):
+        ig.ig_page_slots(stream, 3, 3, 32, c["n"], c["mp"], 12, c["table"], c["L"], None, counts, up, *to)
+        return to
+
+    full, ws = slots(room()), torch.empty(ig.ig_paged_tree_attend_workspace_bytes(3, 64, 8, 2, 128), dtype=torch.uint8, device=DEV)
+    codes, scales = p["codes"].clone(), p["scales"].clone()
+    h, compute, fetch, _, _ = ig.ig_sm_split_create(0, 16)
+    try:
+        for stream in (compute, fetch):
+            out, lse = (torch.full((c["T"], 8) + x, 77.0, dtype=t, device=DEV) for x, t in (((128,), torch.float16), ((), torch.float32)))
+            got = [torch.full_like(x, -9) for x in want]
+            part = room()
+            p["codes"].fill_(0)
+            torch.cuda.synchronize()
+            attend_tree(ig, c, out, lse, ws, stream)
+            ig.ig_page_bounds(stream, ig.IG_BF16, p["n"], 2, 8, 64, p["K"], len(p["rows"]), rows, p["codes"], p["scales"])
+            select(ig, p, 50, 1, 2, stream, got)
+            slots(part, stream)
+            torch.cuda.synchronize()
+            check_tree(c, out, lse)
+            assert torch.equal(p["codes"], codes) and torch.equal(p["scales"], scales)
+            assert all(torch.equal(x, y) for x, y in zip(got, want)) and all(torch.equal(x, y) for x, y in zip(part, full))
+    finally:
+        ig.ig_sm_split_destroy(h)
+    ig.ig_check()
+
+
+def test_cache_replays_the_choice_with_the_bounds_made_since(ig):
+    from speculative_kv_cache_gb300.paged import PagedCache
+
+    g = torch.Generator(device=DEV)
+    g.manual_seed(9)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV).to(torch.float16)  # noqa: E731
+    cache = PagedCache(layers=1, Hq=4, Hkv=2, d=64, n_pages=60, seqs=2, max_pages=25, page=16, bounds=True)
+    slots, positions = cache.extend({0: 300, 1: 150})
+    cache.write(0, rand(450, 4, 64), rand(450, 2, 64), rand(450, 2, 64), slots, positions)
+    q = rand(2, 4, 64)
+    out = torch.empty(2, 4, 64, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(ValueError, match="captured"):
+        with torch.cuda.graph(graph):
+            cache.attend_picked(0, q, 5, out=out)
+    want = cache.attend_picked(0, q, 5)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend_picked(0, q, 5, out=out)
+    graph.replay()
+    assert torch.equal(out, want)
+    for n in (1, 40, 17):
+        slots, positions = cache.extend({0: n, 1: 2 * n})
+        cache.write(0, rand(3 * n, 4, 64), rand(3 * n, 2, 64), rand(3 * n, 2, 64), slots, positions)
+        q.copy_(rand(2, 4, 64))
+        cache.summarise(0)
+        graph.replay()
+        got = out.clone()
+        assert torch.equal(cache.attend_picked(0, q, 5), got)
+    ig.ig_check()
+    cache.close()
+
+
 def test_cache_drafts_verifies_and_keeps(ig):
     """Rounds of drafting, checking and keeping, with forks and packing between: each attention is that of a sequence
     that grew token by token, and so are the rows that stay."""

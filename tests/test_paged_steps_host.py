@@ -83,7 +83,7 @@ def test_tree_attention_workspace(ig):
 
 
 @pytest.mark.parametrize("bad", _PAGES + [
-    dict(n=0), dict(n=8193, seqs=9000), dict(n=3), dict(seqs=0), dict(T=-1), dict(max_pages=0), dict(max_pages=1 << 27),
+    dict(n=0), dict(n=8193, seqs=9000), dict(n=3), dict(seqs=0), dict(T=-1), dict(T=1 << 30), dict(max_pages=0), dict(max_pages=1 << 27),
     dict(n_pages=1 << 28), dict(page_table=None), dict(L_valid=None), dict(counts=None), dict(first=None), dict(slots=None),
     dict(positions=None), dict(page_table=2), dict(L_valid=2), dict(seq=2), dict(counts=2), dict(parents=2), dict(first=2),
     dict(slots=2), dict(positions=2), dict(masks=4)])
