@@ -505,7 +505,7 @@ ig_status ig_paged_attend_picked(void* stream, int dtype, int B, int Hq, int Hkv
  *   z_j = scale * q . K_j,  o = sum_j w_j V_j,  w = softmax over the tokens it sees,  lse = log(sum_j exp(z_j))
  * in one pass over K and V for 256 (drafted token, query head) pairs of a key head at a time; products in fp16/bf16 with
  * fp32 sums, softmax in fp32, the weights rounded to `dtype` for the second product (their sum is not), o rounded
- * once.  In fp16, weights keep 11 bits down to 2^-28 of the largest and fewer down to 2^-38.  A token that sees nothing
+ * once.  In fp16, weights keep 11 bits down to 2^-24 of the largest and fewer down to 2^-34.  A token that sees nothing
  * has o = 0 and lse = -inf.  What the pages hold past a sequence's last token, and in drafted rows that a token does not
  * see, may be anything, NaN included; among what it sees, a logit of -inf has weight zero, a logit that is NaN or +inf,
  * or a value that is not finite, gives non-finite results.

@@ -16,9 +16,10 @@
 // groups take tiles in turn and join their parts at the end (SPLIT); with more, a unit is 256 rows, and each group has
 // 128 of them and every tile (PAIR), which halves what is read.
 //
-// Precision.  Weights are rounded to the type for the second product.  Fp16 has few exponents: the reference lies 2^14 below the
-// largest logit, so that weights keep their 11 bits down to 2^-28 of it.  The reference moves (and O is scaled by
-// the factor) only when a logit is more than 2^(1 or 8) above what it was set by.  Sums of weights are fp32, unrounded.
+// Precision.  Weights are rounded to the type for the second product.  Fp16 has few exponents: the reference lies 10 (log2) below the
+// largest logit that it was set by, so that weights keep their 11 bits down to 2^-24 of the largest, and moves (and O is
+// scaled by the factor) only when one is more than 5.75 above that (bf16: 8).  (With 14 and 1, a warp's 32 rows move in one
+// tile of three: two trees of 512 rows on 65536 tokens 149 us instead of 137.)  Sums of weights are fp32, unrounded.
 //
 // What is not attended.  Logits of tokens that a row does not see are left out by bits (the tile's tokens that hold
 // anything, the row's mask), whatever they are.  A value of zero weight must not be NaN in an MMA: rows without a token are
@@ -31,14 +32,15 @@
 //
 // Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
 //   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 87 us with 16 rows (0.91 of the copy rate), 89 with
-//   64, 93 with 128, 126 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
+//   64, 93 with 128, 121 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
 //   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 100 us, 0.82; the join, of 150 cuts, has 6 of them,
 //   and without any arithmetic of the softmax the rest takes as long.
-//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 149 us, 0.91 Pflop/s.  What is left is a group's chain of logits,
-//   weights and values: without exponentials and maxima 130, with an eighth of the products 127, without either 117.
+//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 135 us, 1.01 Pflop/s.  What is left is a group's chain: 1240 cycles
+//   for a tile's values and the next one's logits (1024 of them the products), some 1900 for the weights.
 //   8 drafted tokens on 256, 4 key heads of 64: 8.4 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
 // Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
-// three values, no gain.
+// three values, no gain; tiles in two pieces, whose logits are there ahead, 135 -> 151 (a product of 64 tokens takes as
+// long as one of 128, as its queries are read from shared memory again).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -117,7 +119,7 @@ struct TreeShared {
   uint64_t o_done[2];               // its last product of a unit
   uint64_t q_full[2], q_empty[2];   // queries
   uint64_t half[2], o_free[2];      // a group's part of a unit is there for the other, has been taken
-  uint64_t clean[8];                // a tile's values, which both groups use, hold nothing that they must not
+  uint64_t clean[8];                // values that had to be cleared, and that both groups use, are (by their count)
   uint64_t drain;
   uint32_t valid[8][4];             // tokens of a tile that hold anything
   float2 ml[kTreeTile];
@@ -631,9 +633,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     const uint32_t s_at = tmem + lanes + gs * kTreeTile, o_at = s_at + 2 * kTreeTile;
     const uint32_t o_other = tmem + lanes + (3 - gs) * kTreeTile;
     const uint32_t limit = wait_limit(err);
-    constexpr float kBelow = BF ? 0.f : 14.f, kAbove = BF ? 8.f : 15.f;  // of the reference: the largest weight, and what moves it
+    constexpr float kBelow = BF ? 0.f : 10.f, kAbove = BF ? 8.f : 15.75f;  // of the reference: the largest weight, and what moves it
     const float sc = a.scale2 == 0.f ? 1.f : fabsf(a.scale2), sgn = a.scale2 > 0.f ? 1.f : a.scale2 < 0.f ? -1.f : 0.f;
-    uint32_t at_tile = 0, s_seen = 0, o_seen = 0, half_seen = 0, free_seen = 0;
+    uint32_t dirty = 0, at_tile = 0, s_seen = 0, o_seen = 0, half_seen = 0, free_seen = 0;
     bool ok = true, lent = false, cut = false;  // lent: the other group still reads this one's O
     for (uint32_t seg = 0; ok && w.left > 0; ++seg) {
       const int run = w.run(), tile0 = w.tile, nt = w.nt, hk = w.u / w.blocks, block = w.u % w.blocks;
@@ -677,46 +679,20 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
         if (warp_live) {
           // (Loops over 32 logits at a time, read twice, keep the code small: unrolled over the row, all roles' code is more
           // than the instruction caches hold, and every instruction takes several times as long.)
-          float top = -INFINITY;
           uint32_t ya[32], yb[32];  // 32 logits are on their way while 32 are worked on
+          float top, sum[4], mx[4];
+          auto none = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sum[i] = 0.f;
+              mx[i] = -INFINITY;
+            }
+          };
           auto largest = [&](const uint32_t (&y)[32]) {
-            float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) mx[i / 2 % 4] = max3(mx[i / 2 % 4], __uint_as_float(y[i]), __uint_as_float(y[i + 1]));
-            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
           };
-          tm_ld32(ya, s_at);
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-            tm_wait_ld32(ya);
-            tm_ld32(yb, s_at + 32 * c + 32);
-            largest(ya);
-            tm_wait_ld32(yb);
-            tm_ld32(ya, s_at + (32 * c + 64) % 128);  // (at the end the first ones, for the weights)
-            largest(yb);
-          }
-          top *= sc;
-          const bool move = live && top > m + kAbove;  // (from -inf on: whenever there is anything)
-          if (__any_sync(0xffffffffu, move)) {
-            const float to = move ? top - kBelow : m, f = move ? ex2(m - to) : 1.f;
-            m = to;
-            l *= f;
-            if (k > k0) {
-#pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tm_ld32(o, o_at + 32 * c);
-                tm_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tm_st32(o_at + 32 * c, o);
-              }
-            }
-          }
-          const float m0 = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          auto weigh = [&](const uint32_t (&y)[32], int c) {  // weights go where logits were that have been read
-            uint32_t p[16];
+          auto weigh = [&](const uint32_t (&y)[32], uint32_t (&p)[16], float m0) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float y0 = ex2(fmaf(__uint_as_float(y[i]), sc, -m0)), y1 = ex2(fmaf(__uint_as_float(y[i + 1]), sc, -m0));
@@ -724,16 +700,84 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
               sum[i / 2 % 4] += y1;
               p[i / 2] = pack2<BF>(y0, y1);
             }
-            tm_st16(s_at + 16 * c, p);
           };
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
+          bool again = true;
+          none();
+          tm_ld32(ya, s_at);
+          if (PAIR && k > k0) {
+            // Weights by the reference that there is, and their largest with them: mostly it stays (read once, 181 -> 174 us for 8
+            // trees of 256 to 512 rows, 124 -> 121 for one; with SPLIT, which waits for HBM, no gain).  The logits stay until
+            // that is known.
+            const float m0 = m == -INFINITY ? 0.f : m;
+            uint32_t p0[16], p1[16], p2[16], p3[16];
             tm_wait_ld32(ya);
-            tm_ld32(yb, s_at + 32 * c + 32);
-            weigh(ya, c);
+            tm_ld32(yb, s_at + 32);
+            largest(ya);
+            weigh(ya, p0, m0);
             tm_wait_ld32(yb);
-            if (c == 0) tm_ld32(ya, s_at + 64);
-            weigh(yb, c + 1);
+            tm_ld32(ya, s_at + 64);
+            largest(yb);
+            weigh(yb, p1, m0);
+            tm_wait_ld32(ya);
+            tm_ld32(yb, s_at + 96);
+            largest(ya);
+            weigh(ya, p2, m0);
+            tm_wait_ld32(yb);
+            largest(yb);
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc;
+            again = __any_sync(0xffffffffu, live && top > m + kAbove);
+            if (!again) {
+              tm_st16(s_at, p0);
+              tm_st16(s_at + 16, p1);
+              tm_st16(s_at + 32, p2);
+              weigh(yb, p3, m0);
+              tm_st16(s_at + 48, p3);
+            } else {
+              none();
+              tm_ld32(ya, s_at);
+            }
+          }
+          if (again) {
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+              tm_wait_ld32(ya);
+              tm_ld32(yb, s_at + 32 * c + 32);
+              largest(ya);
+              tm_wait_ld32(yb);
+              tm_ld32(ya, s_at + (32 * c + 64) % 128);  // (at the end the first ones, for the weights)
+              largest(yb);
+            }
+            top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * sc;
+            const bool move = live && top > m + kAbove;  // (from -inf on: whenever there is anything)
+            if (__any_sync(0xffffffffu, move)) {
+              const float to = move ? top - kBelow : m, f = move ? ex2(m - to) : 1.f;
+              m = to;
+              l *= f;
+              if (k > k0) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                  uint32_t o[32];
+                  tm_ld32(o, o_at + 32 * c);
+                  tm_wait_ld32(o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tm_st32(o_at + 32 * c, o);
+                }
+              }
+            }
+            const float m0 = m == -INFINITY ? 0.f : m;
+            uint32_t p[16];
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {  // weights go where logits were that have been read
+              tm_wait_ld32(ya);
+              tm_ld32(yb, s_at + 32 * c + 32);
+              weigh(ya, p, m0);
+              tm_st16(s_at + 16 * c, p);
+              tm_wait_ld32(yb);
+              if (c == 0) tm_ld32(ya, s_at + 64);
+              weigh(yb, p, m0);
+              tm_st16(s_at + 16 * c + 16, p);
+            }
           }
           tm_wait_st();
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
@@ -766,14 +810,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        if (PAIR) {
+        if (PAIR && !plain && rows_all > kTreeTile) {
           if (gs == 0) {
             __syncwarp();
-            if (lane == 0) tree_arrive(&sh.clean[j & 7]);
-          } else if (!plain) {
-            ok = tree_wait(&sh.clean[j & 7], j >> 3 & 1, &sh.abort, most_iters, err);
+            if (lane == 0) tree_arrive(&sh.clean[dirty & 7]);
+          } else {
+            ok = tree_wait(&sh.clean[dirty & 7], dirty >> 3 & 1, &sh.abort, most_iters, err);
             if (!ok) break;
           }
+          ++dirty;
         }
         if (lent) {  // O is free again once the other group has taken what it needs
           ok = tree_wait(&sh.o_free[gs], free_seen++ & 1, &sh.abort, most_iters, err);
