@@ -35,7 +35,7 @@
 //   64, 93 with 128, 121 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
 //   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 100 us, 0.82; the join, of 150 cuts, has 6 of them,
 //   and without any arithmetic of the softmax the rest takes as long.
-//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 135 us, 1.01 Pflop/s.  What is left is a group's chain: 1240 cycles
+//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 129 us, 1.06 Pflop/s.  What is left is a group's chain: 1240 cycles
 //   for a tile's values and the next one's logits (1024 of them the products), some 1900 for the weights.
 //   8 drafted tokens on 256, 4 key heads of 64: 8.4 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
 // Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
@@ -219,13 +219,14 @@ __device__ __forceinline__ bool tree_wait(uint64_t* bar, uint32_t parity, volati
 struct TreeWalk {
   int RU;        // rows of a unit
   bool whole;    // shares of whole units
+  int team, member;  // CTAs that go side by side, one a block of rows (0: one after the other); the block of this one
   int r, left;   // request; tiles (whole units) left
   TreeRequest x;
   int blocks, units, nt, u, tile;  // blocks of rows of a key head, units of the request, tiles of a unit; unit and tile in it
 
   __device__ bool enter(const TreeShape& a) {
     if (!tree_request(a, r, x) || x.n == 0) return false;
-    blocks = (x.n * a.G + RU - 1) / RU;
+    blocks = team ? 1 : (x.n * a.G + RU - 1) / RU;  // (a walk's own)
     units = blocks * a.Hkv;
     nt = (x.L + kTreeTile - 1) / kTreeTile;
     return true;
@@ -241,6 +242,8 @@ struct TreeWalk {
     u = whole ? off : off / nt;
     tile = whole ? 0 : off % nt;
   }
+  __device__ int head() const { return u / blocks; }
+  __device__ int block() const { return member + u % blocks; }
   __device__ int run() const { return whole ? nt : min(nt - tile, left); }
   __device__ void next(const TreeShape& a) {
     left -= whole ? 1 : run();
@@ -331,14 +334,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   // ---- this CTA's share of all tiles, and the request it starts in
   TreeWalk w;
   w.RU = RU;
+  w.team = w.member = 0;
   const int per = (a.B + kTreeThreads - 1) / kTreeThreads;
   const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
   int tiles = 0, units = 0, longest = 0;
+  const int most = (a.T_max * a.G + RU - 1) / RU;
+  bool alike = true;  // all requests have that many blocks of rows
   for (w.r = b0; w.r < b1; ++w.r) {
     if (w.enter(a)) {
       tiles += w.units * w.nt;
       units += w.units;
       longest = max(longest, w.nt);
+      alike &= w.blocks == most;
     } else if (blockIdx.x == 0 && !tree_request(a, w.r, w.x)) {
       raise_error(err, IG_DEVERR_INDEX);
     }
@@ -360,7 +367,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   }
   if (threadIdx.x == 0 && !most_blocks) info[blockIdx.x] = make_int4(-1, 0, 0, 0);
   tc_fence_before();
-  __syncthreads();
+  alike = __syncthreads_and(alike);
   tc_fence_after();
   pdl_trigger();
   const uint32_t tmem = sh.tmem;
@@ -373,12 +380,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     all_units += sh.scan[i][1];
     longest = max(longest, sh.scan[i][2]);
   }
-  const int cta = blockIdx.x;
   w.whole = all_units <= (int)gridDim.x &&
             (longest <= kTreeWhole ||
              (2 * all_units >= (int)gridDim.x && (long long)longest * all_units <= (long long)all_tiles + kTreeEven * all_units));
+  // Where all requests have the same few blocks of rows, a team of CTAs takes the blocks of the same tiles side by side, which
+  // then come from HBM once and else from L2 (two trees of 512 rows on 65536 tokens: 135 -> 130 us; with heads of 64, which
+  // need half as much a tile, 182 -> 187, so not there).
+  if (PAIR && D == 128 && !w.whole && alike && most > 1 && (int)gridDim.x / most * most * 20 >= (int)gridDim.x * 19) {
+    w.team = most;
+    w.member = blockIdx.x % most;
+    tiles /= most;
+    tiles_before /= most;
+    all_tiles /= most;
+  }
+  const int stride = max(w.team, 1), cta = blockIdx.x / stride, places = (int)gridDim.x / stride;
   const int total = w.whole ? all_units : all_tiles, before = w.whole ? units_before : tiles_before,
-            mine = w.whole ? units : tiles, ctas = min((int)gridDim.x, total);
+            mine = w.whole ? units : tiles, ctas = min(places, total);
   const unsigned each = ctas ? (unsigned)total / ctas : 0, rest = ctas ? (unsigned)total % ctas : 0;
   auto first_of = [&](unsigned c) -> int { return (int)(each * c + rest * c / (unsigned)ctas); };  // CTA c's first share
   const int r0 = cta < ctas ? first_of(cta) : 0, r1 = cta < ctas ? first_of(cta + 1) : 0;
@@ -421,7 +438,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       t.is = true;
       t.token0 = (w.tile + at) * kTreeTile;
       t.L = w.x.L;
-      t.hk = w.u / w.blocks;
+      t.hk = w.head();
       const int token = t.token0 + box_at;
       if (box_at < kTreeTile && token < t.L) t.id = __ldca(a.table + (size_t)w.x.s * a.max_pages + token / a.page);
       if (++at == run) {
@@ -570,7 +587,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       // a tile's values and the next tile's logits, group by group; a unit begins with logits alone
       uint32_t j = 0;
       for (uint32_t seg = 0; ok && uniform(w.left) > 0; w.next(a), ++seg) {
-        const int run = uniform(w.run()), rows = uniform(w.x.n * a.G - w.u % w.blocks * RU);
+        const int run = uniform(w.run()), rows = uniform(w.x.n * a.G - w.block() * RU);
         const uint32_t groups = rows > kTreeTile ? 2 : 1;
         ok = wait(&sh.q_full[0], seg & 1) && wait(&sh.k_full[j & 7], j >> 3 & 1);
         if (!ok) break;
@@ -611,7 +628,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(a)) {
       const uint32_t buf = PAIR ? 0 : seg & 1, round = PAIR ? seg : seg >> 1;
       if (round > 0 && !tree_wait(&sh.q_empty[buf], (round - 1) & 1, &sh.abort, most_iters, err)) break;
-      const int row0 = w.u % w.blocks * RU, rows = min(RU, w.x.n * a.G - row0), hk = w.u / w.blocks;
+      const int row0 = w.block() * RU, rows = min(RU, w.x.n * a.G - row0), hk = w.head();
       const int ch = lane % (D / 8);
       for (int row = lane / (D / 8); row < rows; row += 32 / (D / 8)) {
         const int i = (row0 + row) / a.G, g = (row0 + row) % a.G;
@@ -638,9 +655,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     uint32_t dirty = 0, at_tile = 0, s_seen = 0, o_seen = 0, half_seen = 0, free_seen = 0;
     bool ok = true, lent = false, cut = false;  // lent: the other group still reads this one's O
     for (uint32_t seg = 0; ok && w.left > 0; ++seg) {
-      const int run = w.run(), tile0 = w.tile, nt = w.nt, hk = w.u / w.blocks, block = w.u % w.blocks;
+      const int run = w.run(), tile0 = w.tile, nt = w.nt, hk = w.head(), block = w.block();
       const TreeRequest x = w.x;
-      const int unit_r = w.r, unit_u = w.u, left = w.left;
+      const int unit_r = w.r, left = w.left;
       const int rows_all = min(RU, x.n * a.G - block * RU);
       const int my_row = PAIR ? gs * kTreeTile + row : row;  // in the unit
       const bool live = my_row < rows_all, warp_live = my_row - lane < rows_all;
@@ -860,7 +877,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       const bool poisoned = *(volatile int*)&sh.poison[seg & 7] == (int)seg + 1;
       const size_t at = live ? (size_t)(x.f + node) * a.Hq + (size_t)hk * a.G + head : 0;
       // the unit it starts with, begun by an earlier CTA, to slot 0; one it begins to slot 1
-      float* wp = part + ((size_t)(2 * cta + (tile0 == 0 ? 1 : 0)) * RU + my_row) * (D + kTreePartHead);
+      float* wp = part + ((size_t)(2 * blockIdx.x + (tile0 == 0 ? 1 : 0)) * RU + my_row) * (D + kTreePartHead);
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (warp_live) {
 #pragma unroll 1
@@ -931,8 +948,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           while (last + 1 < ctas && first_of(last + 1) <= end) ++last;
           while (first_of(last) > end) --last;
         }
-        if (most_blocks) info[(unit_r * a.Hkv + hk) * most_blocks + block] = make_int4(cut ? cta : -1, 0, last, 0);
-        else info[cta] = make_int4(unit_r, unit_u, last, 0);
+        last = last * stride + w.member;
+        if (most_blocks) info[(unit_r * a.Hkv + hk) * most_blocks + block] = make_int4(cut ? blockIdx.x : -1, 0, last, stride);
+        else info[blockIdx.x] = make_int4(unit_r, hk * ((x.n * a.G + RU - 1) / RU) + block, last, stride);
       }
       at_tile += run;
     }
@@ -971,21 +989,21 @@ __global__ void __launch_bounds__(WPR * RB * 32) k_tree_join(const float* __rest
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   TreeRequest x;
-  int c0, last, hk, block;
+  int c0, last, stride, hk, block;
   if (most_blocks) {
     block = blockIdx.x % most_blocks, hk = blockIdx.x / most_blocks % a.Hkv;
     // (units that there are have been listed, but for those of CTAs whose waits ran out)
     if (!tree_request(a, blockIdx.x / most_blocks / a.Hkv, x) || block * RU >= x.n * a.G) return;
     const int4 e = __ldca(info + blockIdx.x);
-    c0 = e.x, last = e.z;
-    if (c0 < 0 || last < c0 || last >= kMaxTreeCtas) return;
+    c0 = e.x, last = e.z, stride = e.w;
+    if (c0 < 0 || last < c0 || last >= kMaxTreeCtas || stride < 1) return;
   } else {
     const int4 e = __ldca(info + blockIdx.x);
     if (e.x < 0 || !tree_request(a, e.x, x)) return;
     const int blocks = (x.n * a.G + RU - 1) / RU;
-    c0 = blockIdx.x, last = e.z, hk = e.y / blocks, block = e.y % blocks;
+    c0 = blockIdx.x, last = e.z, stride = e.w, hk = e.y / blocks, block = e.y % blocks;
   }
-  const int n = last - c0 + 1, f = x.f, rows = x.n * a.G, row = blockIdx.y * RB + warp / WPR, rr = block * RU + row;
+  const int n = (last - c0) / stride + 1, f = x.f, rows = x.n * a.G, row = blockIdx.y * RB + warp / WPR, rr = block * RU + row;
   const bool live = row < RU && rr < rows;
   float m = -INFINITY, l = 0.f, o[VEC];
 #pragma unroll
@@ -997,7 +1015,7 @@ __global__ void __launch_bounds__(WPR * RB * 32) k_tree_join(const float* __rest
     const int w0 = warp % WPR, mine = (n - w0 + WPR - 1) / WPR;
     auto at = [&](int i) -> const float* {
       const int j = w0 + i * WPR;
-      return part + ((size_t)(2 * (c0 + j) + (j == 0 ? 1 : 0)) * RU + row) * (D + kTreePartHead);
+      return part + ((size_t)(2 * (c0 + j * stride) + (j == 0 ? 1 : 0)) * RU + row) * (D + kTreePartHead);
     };
     auto load = [&](int i0, float (&v)[U][VEC]) {
 #pragma unroll
