@@ -32,10 +32,10 @@
 //
 // Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
 //   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 87 us with 16 rows (0.91 of the copy rate), 89 with
-//   64, 93 with 128, 121 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
+//   64, 93 with 128, 116 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
 //   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 100 us, 0.82; the join, of 150 cuts, has 6 of them,
 //   and without any arithmetic of the softmax the rest takes as long.
-//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 129 us, 1.06 Pflop/s.  What is left is a group's chain: 1240 cycles
+//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 115 us, 1.18 Pflop/s.  What is left is a group's chain: 1240 cycles
 //   for a tile's values and the next one's logits (1024 of them the products), some 1900 for the weights.
 //   8 drafted tokens on 256, 4 key heads of 64: 8.4 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
 // Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
@@ -283,8 +283,9 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
 
 template <bool BF, int D, bool PAIR>
 __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
-    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const uint16_t* __restrict__ q,
-    const uint16_t* __restrict__ V, const TreeShape a, const int box, const int fat, const int most_blocks,
+    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q,
+    const uint16_t* __restrict__ q, const uint16_t* __restrict__ V, const TreeShape a, const int box, const int fat,
+    const int q_rows, const int most_blocks,
     uint16_t* __restrict__ out, float* __restrict__ lse, float* __restrict__ part, int4* __restrict__ info, int* err) {
   constexpr int NS = tree_slots<D>(), RU = PAIR ? 2 * kTreeTile : kTreeTile;
   constexpr uint32_t kSlot = tree_slot_bytes<D>(), kHalf = kTreeTile * 128;
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   if (threadIdx.x == 32) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 8; ++i) {
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   __syncthreads();
   w.start(a, sh.start_r, sh.start_off, r1 - r0);
   const uint32_t most_iters = (uint32_t)kDefaultWaitIters;
-  uint32_t sent = 0;  // tiles whose keys (or values) have been sent for
+  uint32_t sent = 0;  // tiles whose keys (or values) have been sent for, units whose queries have
 
   if (warp == kTreeTmaK || warp == kTreeTmaV) {
     // ---- tiles, a warp the keys and a warp the values (a copy's issue takes 130 cycles, whatever it moves: pages of 16 rows
@@ -624,18 +626,40 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     }
     __syncwarp();
   } else if (warp == kTreeQueries) {
-    // ---- queries, rows in the order (token, head), rows behind the last one left as they are
+    // ---- queries, rows in the order (token, head); rows behind the last one hold anything.  By TMA where the group is a power of
+    // two, so that 128 rows are a box of tokens and heads (a warp takes 5 us for 256 rows, and twice that beside the
+    // others' work: 512 rows on 2 x 65536 tokens 129 -> 115 us).
     for (uint32_t seg = 0; w.left > 0; ++seg, w.next(a)) {
       const uint32_t buf = PAIR ? 0 : seg & 1, round = PAIR ? seg : seg >> 1;
       if (round > 0 && !tree_wait(&sh.q_empty[buf], (round - 1) & 1, &sh.abort, most_iters, err)) break;
       const int row0 = w.block() * RU, rows = min(RU, w.x.n * a.G - row0), hk = w.head();
-      const int ch = lane % (D / 8);
-      for (int row = lane / (D / 8); row < rows; row += 32 / (D / 8)) {
-        const int i = (row0 + row) / a.G, g = (row0 + row) % a.G;
-        const uint16_t* p = q + ((size_t)(w.x.f + i) * a.Hq + (size_t)hk * a.G + g) * D + ch * 8;
-        unsigned char* to = sq + buf * kSlot + row / kTreeTile * kSlot + ch / 8 * kHalf + row % kTreeTile * 128 +
-                            (((ch & 7) ^ (row & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(p) : "memory");
+      if (q_rows) {
+        const int parts = rows > kTreeTile ? 2 : 1;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[buf], (uint32_t)(parts * (D / 64) * q_rows) * 128);
+        __syncwarp();
+        if (lane < parts * (D / 64)) {
+          const int part = lane / (D / 64), col = lane % (D / 64), at = row0 + part * kTreeTile;
+          tma_load_3d(sq + (buf + part) * kSlot + col * kHalf, &map_q, col * 64, hk * a.G + at % a.G, w.x.f + at / a.G,
+                      &sh.q_full[buf]);
+        }
+        ++sent;
+        continue;
+      }
+      constexpr int kRows = 32 / (D / 8);  // of the warp at a time
+      const int ch = lane % (D / 8), at = row0 + lane / (D / 8), i = at / a.G;
+      int g = at % a.G;
+      const uint16_t* p = q + ((size_t)(w.x.f + i) * a.Hq + (size_t)hk * a.G + g) * D + ch * 8;
+      const int heads = kRows % a.G, token = a.Hq * D, step = kRows / a.G * token + heads * D, wrap = token - a.G * D;
+      const uint32_t to = smem_addr(sq + buf * kSlot + ch / 8 * kHalf);
+#pragma unroll 4
+      for (int row = lane / (D / 8); row < rows; row += kRows) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + row / kTreeTile * kSlot + row % kTreeTile * 128 +
+                                                                      (((ch & 7) ^ (row & 7)) << 4)),
+                     "l"(p)
+                     : "memory");
+        g += heads;
+        p += g >= a.G ? step + wrap : step;
+        g -= g >= a.G ? a.G : 0;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -968,6 +992,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     if (warp == kTreeTmaK || warp == kTreeTmaV)
       for (uint32_t x = sent > 8 ? sent - 8 : 0; x < sent; ++x)
         mbar_wait_bounded(warp == kTreeTmaV ? &sh.v_full[x & 7] : &sh.k_full[x & 7], x >> 3 & 1);
+    if (warp == kTreeQueries)
+      for (uint32_t x = sent > 2 ? sent - 2 : 0; x < sent; ++x)
+        mbar_wait_bounded(&sh.q_full[PAIR ? 0 : x & 1], (PAIR ? x : x >> 1) & 1);
     __syncthreads();
   }
   if (warp == kTreeMma) {
@@ -1119,10 +1146,15 @@ ig_status launch_tree(cudaStream_t st, const TreeShape& a, const uint16_t* q, co
   // Values lie box by box, both halves of its columns in one copy: their product takes 16 rows at a time, wherever they are.  Keys' 128
   // rows have to lie evenly, so theirs do so where a box is a tile or a group of 8 rows, else a half a copy.
   const int fat = D == 64 || box == 8 || box == kTreeTile ? 1 : 0, rows = a.n_pages * a.Hkv * a.page;
-  CUtensorMap mk, mv;
+  // queries, 128 rows a box of whole tokens (or of a token's heads)
+  const bool even = (a.G & (a.G - 1)) == 0;
+  const int heads = a.G < kTreeTile ? a.G : kTreeTile, tokens = kTreeTile / heads < a.T_max ? kTreeTile / heads : a.T_max;
+  CUtensorMap mk, mv, mq;
   ig_status r = fat ? make_map_halves(&mk, K, rows, D, box) : make_map(&mk, K, rows, D, box);
   if (r == IG_OK) r = make_map_halves(&mv, V, rows, D, box);
+  if (r == IG_OK && even) r = make_map_heads(&mq, q, a.T, a.Hq, D, tokens, heads);
   if (r != IG_OK) return r;
+  if (!even) mq = mk;  // (not used)
   constexpr size_t smem = tree_smem<D>();
   cudaError_t e = cudaFuncSetAttribute(k_tree_attend<BF, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_fail(e, "tree attention smem attribute");
@@ -1133,8 +1165,8 @@ ig_status launch_tree(cudaStream_t st, const TreeShape& a, const uint16_t* q, co
   const int most_blocks = units <= grid ? (int)blocks : 0;
   float* part = static_cast<float*>(ws);
   int4* info = reinterpret_cast<int4*>(static_cast<char*>(ws) + tree_part_bytes(RU, D));
-  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, q, V, a, box, fat, most_blocks, out,
-                 lse, part, info, error_word());
+  e = launch_pdl(k_tree_attend<BF, D, PAIR>, dim3(grid), dim3(kTreeThreads), smem, st, mk, mv, mq, q, V, a, box, fat,
+                 even ? tokens * heads : 0, most_blocks, out, lse, part, info, error_word());
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   IG_CHECK_LAUNCH("tree attention launch");
   if (grid == 1 || (most_blocks && tiles <= kTreeWhole)) return IG_OK;  // nothing can have been cut

@@ -16,6 +16,10 @@ ig_status make_map(CUtensorMap* m, const void* base, int rows, int cols, int box
 // a box is all columns of box_rows rows, one half after the other, each 128B-swizzled.
 ig_status make_map_halves(CUtensorMap* m, const void* base, int rows, int cols, int box_rows);
 
+// Heads of tokens, [tokens][heads][cols] (of 16-bit elements, cols 64 or 128), by columns, heads and tokens: a box is 64 columns
+// of box_heads heads of box_tokens tokens, a head a row, 128B-swizzled; tokens past the last are zero.
+ig_status make_map_heads(CUtensorMap* m, const void* base, int tokens, int heads, int cols, int box_tokens, int box_heads);
+
 // Shared-memory matrix descriptor of a K-major, 128B-swizzled tile whose 8-row groups are
 // 1024 bytes apart: start address >> 4 (bits 0-13), leading offset 16 B (unused for swizzled
 // K-major tiles), stride offset 1024 B (bits 32-45), descriptor version 1 (bit 46), layout

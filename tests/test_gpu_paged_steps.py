@@ -335,6 +335,21 @@ def test_tree_rows_about_the_ends_of_blocks(ig, G, n, dt, d):
     ig.ig_check()
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("lengths,n,G,Hkv", [([9000], 64, 8, 1), ([5000, 77, 2600], 64, 8, 2), ([4000, 64], 64, 12, 2),
+                                             ([2500, 900, 43, 44, 3000], 43, 24, 1), ([1500, 70, 1300, 300], 64, 16, 8),
+                                             ([6000, 6001], 64, 33, 1), ([130] * 30, 33, 8, 3)])
+def test_tree_of_several_blocks_of_rows(ig, lengths, n, G, Hkv, dt):
+    """All requests with as many blocks of rows (2 to 9 of them), which CTAs take side by side where that leaves few idle."""
+    drafted = [n] * len(lengths)
+    c = make_tree(28, dt, lengths + [40], drafted + [0], G * Hkv, Hkv, 128, 64)
+    out = attend_tree(ig, c)
+    check_tree(c, *out)
+    again = attend_tree(ig, c)
+    assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1])
+    ig.ig_check()
+
+
 def test_tree_of_more_requests_than_threads(ig):
     rng = np.random.default_rng(22)
     lengths = [int(rng.integers(1, 40)) for _ in range(1000)]
