@@ -32,10 +32,10 @@
 //
 // Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
 //   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 87 us with 16 rows (0.91 of the copy rate), 89 with
-//   64, 93 with 128, 116 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
+//   64, 93 with 128, 114 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
 //   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 100 us, 0.82; the join, of 150 cuts, has 6 of them,
 //   and without any arithmetic of the softmax the rest takes as long.
-//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 115 us, 1.18 Pflop/s.  What is left is a group's chain: 1240 cycles
+//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 111 us, 1.23 Pflop/s.  What is left is a group's chain: 1240 cycles
 //   for a tile's values and the next one's logits (1024 of them the products), some 1900 for the weights.
 //   8 drafted tokens on 256, 4 key heads of 64: 8.4 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
 // Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
@@ -944,9 +944,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
               to[i] = make_uint4(h[0], h[1], h[2], h[3]);
             }
           } else if (live) {
-            uint4* to = reinterpret_cast<uint4*>(wp + kTreePartHead + 32 * c);
+            float* to = wp + kTreePartHead + 32 * c;  // (a row a thread, so a sector at a time: 115 -> 111 us)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 32; i += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + i), "r"(o[i]), "r"(o[i + 1]), "r"(o[i + 2]),
+                           "r"(o[i + 3]), "r"(o[i + 4]), "r"(o[i + 5]), "r"(o[i + 6]), "r"(o[i + 7])
+                           : "memory");
           }
         }
         if (live) {
