@@ -32,12 +32,12 @@
 //
 // Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
 //   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 87 us with 16 rows (0.91 of the copy rate), 89 with
-//   64, 93 with 128, 114 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
+//   64, 90 with 128, 114 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
 //   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 100 us, 0.82; the join, of 150 cuts, has 6 of them,
 //   and without any arithmetic of the softmax the rest takes as long.
 //   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 111 us, 1.23 Pflop/s.  What is left is a group's chain: 1240 cycles
 //   for a tile's values and the next one's logits (1024 of them the products), some 1900 for the weights.
-//   8 drafted tokens on 256, 4 key heads of 64: 8.4 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
+//   8 drafted tokens on 256, 4 key heads of 64: 8.1 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
 // Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
 // three values, no gain; tiles in two pieces, whose logits are there ahead, 135 -> 151 (a product of 64 tokens takes as
 // long as one of 128, as its queries are read from shared memory again).
@@ -126,7 +126,8 @@ struct TreeShared {
   int poison[8];                    // by unit: 1 + its number, if it has drafted values that are not finite
   int scan[kTreeThreads / 32][3];
   uint32_t tmem;
-  int start_r, start_off, abort;
+  int start[10];                    // where this CTA's share begins
+  int abort;
 };
 
 template <int D>
@@ -231,16 +232,15 @@ struct TreeWalk {
     nt = (x.L + kTreeTile - 1) / kTreeTile;
     return true;
   }
-  __device__ void start(const TreeShape& a, int request, int off, int n) {
-    r = request;
+  // One thread finds the beginning, and the others take it from shared memory: `off` into request r, which it has entered.
+  __device__ void put(int* to, int off) const {
+    const int v[10] = {r, x.f, x.n, x.L, x.s, blocks, units, nt, whole ? off : off / nt, whole ? 0 : off % nt};
+#pragma unroll
+    for (int i = 0; i < 10; ++i) to[i] = v[i];
+  }
+  __device__ void get(const int* from, int n) {
+    r = from[0], x = {from[1], from[2], from[3], from[4]}, blocks = from[5], units = from[6], nt = from[7], u = from[8], tile = from[9];
     left = n;
-    u = tile = 0;
-    if (left <= 0 || !enter(a)) {
-      left = 0;
-      return;
-    }
-    u = whole ? off : off / nt;
-    tile = whole ? 0 : off % nt;
   }
   __device__ int head() const { return u / blocks; }
   __device__ int block() const { return member + u % blocks; }
@@ -403,18 +403,22 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   const int r0 = cta < ctas ? first_of(cta) : 0, r1 = cta < ctas ? first_of(cta + 1) : 0;
   if (r1 > r0 && r0 >= before && r0 < before + mine) {
     int at = before;
-    for (w.r = b0; w.r < b1; ++w.r) {
-      const int n = w.enter(a) ? w.units * (w.whole ? 1 : w.nt) : 0;
-      if (r0 < at + n) {
-        sh.start_r = w.r;
-        sh.start_off = r0 - at;
-        break;
+    if (per == 1 && !w.team) {  // (this thread's one request, which it has entered)
+      w.r = b0;
+      w.put(sh.start, r0 - at);
+    } else {
+      for (w.r = b0; w.r < b1; ++w.r) {
+        const int n = w.enter(a) ? w.units * (w.whole ? 1 : w.nt) : 0;
+        if (r0 < at + n) {
+          w.put(sh.start, r0 - at);
+          break;
+        }
+        at += n;
       }
-      at += n;
     }
   }
   __syncthreads();
-  w.start(a, sh.start_r, sh.start_off, r1 - r0);
+  w.get(sh.start, r1 - r0);
   const uint32_t most_iters = (uint32_t)kDefaultWaitIters;
   uint32_t sent = 0;  // tiles whose keys (or values) have been sent for, units whose queries have
 
