@@ -31,16 +31,17 @@
 // order by a second kernel.  No atomics: the result does not depend on timing.
 //
 // Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
-//   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 87 us with 16 rows (0.91 of the copy rate), 89 with
-//   64, 90 with 128, 114 with 256 (PAIR).  Pages of 16: 90 with 16 rows.  Heads of 64, 128 rows, 268 MB: 62 us.
-//   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 100 us, 0.82; the join, of 150 cuts, has 6 of them,
-//   and without any arithmetic of the softmax the rest takes as long.
-//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 111 us, 1.23 Pflop/s.  What is left is a group's chain: 1240 cycles
-//   for a tile's values and the next one's logits (1024 of them the products), some 1900 for the weights.
-//   8 drafted tokens on 256, 4 key heads of 64: 8.1 us, of which 2 are the plan and tensor memory, 2.4 the first logits.
+//   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 86 us with 16 rows (0.92 of the copy rate), 87 with
+//   64, 90 with 128, 111 with 256 (PAIR), 194 with 512.  64 rows in pages of 16 or 8: 91.  Heads of 64, 128 rows, 268 MB: 60.
+//   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 99 us, 0.83; 6 are the join, of 150 cuts, 6 the plan
+//   and the first tile, and without any arithmetic of the softmax the rest takes as long.
+//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 111 us, 1.22 Pflop/s; a tile takes 3110 cycles, of which the
+//   products are 2048.  The rest is a group's chain, 1240 cycles for a tile's values and the next one's logits and some 1900 for
+//   its weights, which two groups cannot hide in each other altogether: an eighth of the products 88 us, no exponentials 111.
+//   8 drafted tokens on 256, 4 key heads of 64: 8.1 us: a chain of the plan, a page's number, the first tile, its weights.
 // Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
 // three values, no gain; tiles in two pieces, whose logits are there ahead, 135 -> 151 (a product of 64 tokens takes as
-// long as one of 128, as its queries are read from shared memory again).
+// long as one of 128, as its queries are read from shared memory again); the page table's entries fetched by the plan, no gain.
 #include <cuda_bf16.h>
 #include <math.h>
 
