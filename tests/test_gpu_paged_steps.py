@@ -350,6 +350,17 @@ def test_tree_of_several_blocks_of_rows(ig, lengths, n, G, Hkv, dt):
     ig.ig_check()
 
 
+@pytest.mark.parametrize("G", [1, 2, 3, 8])
+@pytest.mark.parametrize("lengths,drafted", [([5], [1]), ([700, 90], [2, 3]), ([4000], [33])])
+def test_tree_with_room_for_more_tokens(ig, lengths, drafted, G):
+    """T_max above every count, and above all tokens."""
+    for d in (64, 128):
+        c = make_tree(29, "bf16", lengths, drafted, 2 * G, 2, d, 16)
+        c["T_max"] = 64
+        check_tree(c, *attend_tree(ig, c))
+    ig.ig_check()
+
+
 def test_tree_of_more_requests_than_threads(ig):
     rng = np.random.default_rng(22)
     lengths = [int(rng.integers(1, 40)) for _ in range(1000)]
