@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     sh.scan[warp][1] = units_in;
     sh.scan[warp][2] = longest;
   }
-  if (threadIdx.x == 0 && !most_blocks) info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0 && !most_blocks) info[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   tc_fence_before();
   alike = __syncthreads_and(alike);
   tc_fence_after();
@@ -981,8 +981,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           while (first_of(last) > end) --last;
         }
         last = last * stride + w.member;
-        if (most_blocks) info[(unit_r * a.Hkv + hk) * most_blocks + block] = make_int4(cut ? blockIdx.x : -1, 0, last, stride);
-        else info[blockIdx.x] = make_int4(unit_r, hk * ((x.n * a.G + RU - 1) / RU) + block, last, stride);
+        const int at = most_blocks ? (unit_r * a.Hkv + hk) * most_blocks + block : blockIdx.x;
+        info[2 * at] = make_int4(cut ? blockIdx.x : -1, last, stride, 0);
+        info[2 * at + 1] = make_int4(x.f, x.n, hk, block);
       }
       at_tile += run;
     }
@@ -1021,24 +1022,21 @@ __global__ void __launch_bounds__(WPR * RB * 32) k_tree_join(const float* __rest
   constexpr int VEC = D / 32;
   __shared__ float sm[WPR * RB], sl[WPR * RB], so[WPR * RB][WPR > 1 ? D : 1];
   pdl_trigger();
-  pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Listed by unit, a unit that there is has an entry, but for those of CTAs whose waits ran out.  (What the first kernel was given
+  // is there already: it lets this one start only when those before it have ended.)
   TreeRequest x;
-  int c0, last, stride, hk, block;
+  int f = 0, rows = 0, hk = 0, block = 0;
   if (most_blocks) {
     block = blockIdx.x % most_blocks, hk = blockIdx.x / most_blocks % a.Hkv;
-    // (units that there are have been listed, but for those of CTAs whose waits ran out)
-    if (!tree_request(a, blockIdx.x / most_blocks / a.Hkv, x) || block * RU >= x.n * a.G) return;
-    const int4 e = __ldca(info + blockIdx.x);
-    c0 = e.x, last = e.z, stride = e.w;
-    if (c0 < 0 || last < c0 || last >= kMaxTreeCtas || stride < 1) return;
-  } else {
-    const int4 e = __ldca(info + blockIdx.x);
-    if (e.x < 0 || !tree_request(a, e.x, x)) return;
-    const int blocks = (x.n * a.G + RU - 1) / RU;
-    c0 = blockIdx.x, last = e.z, stride = e.w, hk = e.y / blocks, block = e.y % blocks;
+    if (tree_request(a, blockIdx.x / most_blocks / a.Hkv, x)) f = x.f, rows = x.n * a.G;
   }
-  const int n = (last - c0) / stride + 1, f = x.f, rows = x.n * a.G, row = blockIdx.y * RB + warp / WPR, rr = block * RU + row;
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 e = __ldca(info + 2 * blockIdx.x), unit = __ldca(info + 2 * blockIdx.x + 1);
+  const int c0 = e.x, last = e.y, stride = e.z;
+  if (c0 < 0 || last < c0 || last >= kMaxTreeCtas || stride < 1) return;
+  if (!most_blocks) f = unit.x, rows = unit.y * a.G, hk = unit.z, block = unit.w;
+  const int n = (last - c0) / stride + 1, row = blockIdx.y * RB + warp / WPR, rr = block * RU + row;
   const bool live = row < RU && rr < rows;
   float m = -INFINITY, l = 0.f, o[VEC];
 #pragma unroll
@@ -1208,7 +1206,7 @@ using namespace ig;
 
 extern "C" size_t ig_paged_tree_attend_workspace_bytes(int n, int T_max, int Hq, int Hkv, int d) {
   if (n <= 0 || T_max <= 0 || T_max > kTreeMost || Hq <= 0 || Hkv <= 0 || Hq % Hkv || (d != 64 && d != 128)) return 0;
-  return tree_part_bytes(tree_rows(T_max, Hq / Hkv), d) + round_up(kMaxTreeCtas * sizeof(int4), 256);
+  return tree_part_bytes(tree_rows(T_max, Hq / Hkv), d) + round_up(2 * kMaxTreeCtas * sizeof(int4), 256);
 }
 
 extern "C" ig_status ig_paged_tree_attend(void* stream, int dtype, int n, int T, int T_max, int Hq, int Hkv, int d, int page,
