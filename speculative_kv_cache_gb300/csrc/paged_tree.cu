@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
   pdl_trigger();
   const uint32_t tmem = sh.tmem;
   int tiles_before = tiles_in - tiles, units_before = units_in - units, all_tiles = 0, all_units = 0;
-#pragma unroll
-  for (int i = 0; i < kTreeThreads / 32; ++i) {
+  const int full = per == 1 ? (a.B + 31) / 32 : kTreeThreads / 32;  // warps that have requests
+#pragma unroll 1
+  for (int i = 0; i < full; ++i) {
     tiles_before += i < warp ? sh.scan[i][0] : 0;
     units_before += i < warp ? sh.scan[i][1] : 0;
     all_tiles += sh.scan[i][0];
@@ -427,7 +428,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     // ---- tiles, a warp the keys and a warp the values (a copy's issue takes 130 cycles, whatever it moves: pages of 16 rows
     // 112 -> 97 us, of 8 rows 159 -> 99, for 131072 tokens, 64 rows).  A lane moves a box; a page's number is read a tile ahead.
     const bool values = warp == kTreeTmaV, thin = values || fat;
-    const int halves = thin ? 1 : D / 64, box_at = lane / halves * box, col = lane % halves;
+    constexpr int kCols = D / 64;
+    const int box_at = (thin ? lane : lane / kCols) * box, col = thin ? 0 : lane % kCols;
     const uint32_t box_bytes = (uint32_t)box * (thin ? D * 2 : 128);
     const int slots = values ? tree_v_slots<D>() : tree_k_slots<D>();
     uint64_t* bars = values ? sh.v_full : sh.k_full;
@@ -435,23 +437,45 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
     unsigned char* at_ring = ring + (values ? tree_k_slots<D>() * kSlot : 0u);
     at_ring += thin ? box_at * D * 2 : col * kHalf + box_at * 128;
     struct Tile {
-      int token0, L, hk, id;
+      int token0, L, hk, id, row;
       bool is;
     };
-    int at = 0, run = w.left > 0 ? w.run() : 0;
+    // the box's page and its row there, from tile to tile without a division
+    const int pages = kTreeTile / a.page, rest_rows = kTreeTile % a.page, pg0 = box_at / a.page, row0 = box_at % a.page;
+    int at = 0, run = w.left > 0 ? w.run() : 0, hk = 0, pg = pg0, row = row0;
+    if (w.left > 0) {
+      hk = w.head();
+      if (w.tile > 0) {
+        const int token = w.tile * kTreeTile + box_at;
+        pg = token / a.page;
+        row = token % a.page;
+      }
+    }
     auto fetch = [&]() -> Tile {
-      Tile t{0, 0, 0, -1, false};
+      Tile t{0, 0, 0, -1, 0, false};
       if (w.left <= 0) return t;
       t.is = true;
       t.token0 = (w.tile + at) * kTreeTile;
       t.L = w.x.L;
-      t.hk = w.head();
-      const int token = t.token0 + box_at;
-      if (box_at < kTreeTile && token < t.L) t.id = __ldca(a.table + (size_t)w.x.s * a.max_pages + token / a.page);
+      t.hk = hk;
+      t.row = row;
+      if (box_at < kTreeTile && t.token0 + box_at < t.L) t.id = __ldca(a.table + (size_t)w.x.s * a.max_pages + pg);
       if (++at == run) {
         w.next(a);
         at = 0;
-        run = w.left > 0 ? w.run() : 0;
+        pg = pg0;
+        row = row0;
+        if (w.left > 0) {
+          run = w.run();
+          hk = w.head();
+        }
+      } else {
+        pg += pages;
+        row += rest_rows;
+        if (row >= a.page) {
+          row -= a.page;
+          ++pg;
+        }
       }
       return t;
     };
@@ -472,7 +496,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           if (bad) {
             raise_error(err, IG_DEVERR_INDEX);
             for (unsigned m = bad; m; m &= m - 1) {
-              const int b = (__ffs(m) - 1) / halves * box;
+              const int b = (thin ? __ffs(m) - 1 : (__ffs(m) - 1) / kCols) * box;
               for (int i = 0; i < box; i += 8) v[(b + i) >> 5] &= ~(0xffu << ((b + i) & 31));
             }
           }
@@ -483,7 +507,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
       }
       __syncwarp();
       if (ok) {
-        const int y = (t.id * a.Hkv + t.hk) * a.page + token % a.page;
+        const int y = (t.id * a.Hkv + t.hk) * a.page + t.row;
         if (thin) tma_load_3d(at_ring + slot * kSlot, values ? &map_v : &map_k, 0, y, 0, &bars[sent & 7]);
         else tma_load_2d(at_ring + slot * kSlot, &map_k, col * 64, y, &bars[sent & 7]);
       }
