@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
   // (the next write to `found` or `warp_sum` comes after a barrier that follows every read of them)
   __syncthreads();
   // ---- keys above the threshold are taken, and the first `want` of those equal to it
-  auto judge = [&](int i, bool& gt, bool& eq) {
+  auto place = [&](int i, bool& gt, bool& eq) {
     const uint32_t k = i < mine ? key[i] : 0u, y = begins(k, shift);
     gt = i < mine && (k == kAlways || y > prefix);
     eq = i < mine && k != kAlways && y == prefix;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
     uint32_t above = 0, equal = 0;
     for (int i = tid; i < mine; i += kSelThreads) {
       bool gt, eq;
-      judge(i, gt, eq);
+      place(i, gt, eq);
       above += gt;
       equal += eq;
     }
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
   for (int i0 = 0; i0 < mine; i0 += kSelThreads, turn ^= 1) {
     const int i = i0 + tid;
     bool gt, eq;
-    judge(i, gt, eq);
+    place(i, gt, eq);
     const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq), lt = (1u << lane) - 1;
     if (lane == 0) warp_sum[turn][warp] = __popc(bg) | __popc(be) << 16;
     __syncthreads();
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
       all += warp_sum[turn][w];
     }
     const uint32_t g_at = (before & 0xffff) + __popc(bg & lt), e_at = (before >> 16) + __popc(be & lt);
-    // equal ones taken before this page: of those in this round, as many as the first `want` reach
+    // equal ones taken before this page: of those in this turn, as many as the first `want` reach
     const uint32_t e_taken = min(ties + e_at, want) - min(ties, want);
     if (gt || (eq && ties + e_at < want)) chosen[pos + g_at + e_taken] = __ldca(table + p0 + i);
     pos += (all & 0xffff) + min(ties + (all >> 16), want) - min(ties, want);

@@ -32,13 +32,15 @@
 //
 // Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
 //   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 86 us with 16 rows (0.92 of the copy rate), 87 with
-//   64, 90 with 128, 111 with 256 (PAIR), 194 with 512.  64 rows in pages of 16 or 8: 91.  Heads of 64, 128 rows, 268 MB: 60.
-//   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 99 us, 0.83; 6 are the join, of 150 cuts, 6 the plan
+//   64, 89 with 128, 109 with 256 (PAIR), 192 with 512.  64 rows in pages of 16: 89, of 8: 90.  Heads of 64, 268 MB: 51 us with 64
+//   rows, 53 with 128, 91 with 256.
+//   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 98 us, 0.84; 4 are the join, of 150 cuts, 6 the plan
 //   and the first tile, and without any arithmetic of the softmax the rest takes as long.
-//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 111 us, 1.22 Pflop/s; a tile takes 3110 cycles, of which the
+//   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 110 us, 1.24 Pflop/s; a tile takes 3100 cycles, of which the
 //   products are 2048.  The rest is a group's chain, 1240 cycles for a tile's values and the next one's logits and some 1900 for
-//   its weights, which two groups cannot hide in each other altogether: an eighth of the products 88 us, no exponentials 111.
-//   8 drafted tokens on 256, 4 key heads of 64: 8.1 us: a chain of the plan, a page's number, the first tile, its weights.
+//   its weights, which two groups cannot hide in each other altogether: with an eighth of the products 88 us, without
+//   exponentials no less than with them.
+//   8 drafted tokens on 256, 4 key heads of 64: 7.7 us: a chain of the plan, a page's number, the first tile, its weights.
 // Tried and left out: a row in two threads (16 softmax warps), 155 -> 167 us; weights announced in halves, and rings of two keys and
 // three values, no gain; tiles in two pieces, whose logits are there ahead, 135 -> 151 (a product of 64 tokens takes as
 // long as one of 128, as its queries are read from shared memory again); the page table's entries fetched by the plan, no gain.
@@ -774,10 +776,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           bool again = true;
           none();
           tm_ld32(ya, s_at);
-          if (PAIR && k > k0) {
-            // Weights by the reference that there is, and their largest with them: mostly it stays (read once, 181 -> 174 us for 8
-            // trees of 256 to 512 rows, 124 -> 121 for one; with SPLIT, which waits for HBM, no gain).  The logits stay until
-            // that is known.
+          if (k > k0) {
+            // Weights by the reference that there is, and the largest logit with them: mostly it stays, and one look at the logits
+            // is enough (8 trees of 256 to 512 rows 181 -> 174 us; 64 rows, heads of 64, 131072 tokens 54 -> 51; no gain where HBM
+            // is waited for).  They stay where they are until that is known.
             const float m0 = m == -INFINITY ? 0.f : m;
             uint32_t p0[16], p1[16], p2[16], p3[16];
             tm_wait_ld32(ya);
