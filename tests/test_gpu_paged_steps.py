@@ -969,6 +969,34 @@ def test_on_a_partition_of_the_sms(ig):
     ig.ig_check()
 
 
+def test_buffers_on_another_gpu_than_the_current_one_are_refused(ig, monkeypatch):
+    c = make_tree(30, "f16", [40], [4], 4, 2, 64, 16)
+    p = make_picked(31, "f16", [90], 4, 2, 64, 16)
+    path, kept = i32([0] * 4), i32([1])
+    want, before = attend_tree(ig, c), c["K"].clone()
+    codes = p["codes"].clone()
+    torch.cuda.synchronize()
+    n = ig.ig_launch_count()
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device=DEV)
+    rows, out = i32(p["rows"]), (torch.empty(1, 2, 4, dtype=torch.int32, device=DEV), torch.empty(1, 2, dtype=torch.int32, device=DEV))
+    calls = [lambda: attend_tree(ig, c, *want, ws, 0), lambda: select(ig, p, 4, 1, 2, 0, out),
+             lambda: ig.ig_page_bounds(0, 0, p["n"], 2, 16, 64, p["K"], len(rows), rows, p["codes"], p["scales"]),
+             lambda: ig.ig_page_slots(0, 1, 1, 16, c["n"], c["mp"], 4, c["table"], c["L"], None, kept, None, path, path, path),
+             lambda: ig.ig_tree_keep(0, 1, c["n"], 2, 16, 64, [c["K"]], [c["V"]], 1, 1, c["mp"], 4, c["table"], c["L"], None, c["dfirst"],
+                                     path, kept),
+             lambda: ig.ig_paged_attend_picked(0, 0, 1, 4, 2, 64, 16, p["n"], 4, 0.125, p["q"], p["K"], p["V"], *out, want[1], None, ws,
+                                               ws.numel())]
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: 1)  # as on a machine with two
+        for call in calls:
+            with pytest.raises(ValueError, match="cuda:0"):
+                call()
+    assert ig.ig_launch_count() == n
+    torch.cuda.synchronize()
+    assert torch.equal(c["K"].view(torch.int16), before.view(torch.int16)) and torch.equal(p["codes"], codes)
+    ig.ig_check()
+
+
 def test_cache_replays_the_choice_with_the_bounds_made_since(ig):
     from speculative_kv_cache_gb300.paged import PagedCache
 
