@@ -66,11 +66,14 @@ struct TreeRequest {
   int f, n, L, s;  // first drafted token in the packed order, their number, all tokens, sequence
 };
 
+// Early: read before the kernel has waited for the one before it, so not from an L1 that may hold older numbers.
+template <bool Early = false>
 __device__ __forceinline__ bool tree_request(const TreeShape& a, int r, TreeRequest& x) {
-  x.f = __ldca(a.first + r);
-  x.n = __ldca(a.first + r + 1) - x.f;
-  x.s = a.seq ? __ldca(a.seq + r) : r;
-  x.L = x.s >= 0 && x.s < a.seqs ? __ldca(a.L + x.s) : -1;
+  auto get = [](const int32_t* p) { return Early ? __ldcg(p) : __ldca(p); };
+  x.f = get(a.first + r);
+  x.n = get(a.first + r + 1) - x.f;
+  x.s = a.seq ? get(a.seq + r) : r;
+  x.L = x.s >= 0 && x.s < a.seqs ? get(a.L + x.s) : -1;
   return x.f >= 0 && x.n >= 0 && x.n <= a.T_max && x.f <= a.T - x.n && x.L >= x.n && x.L <= a.max_pages * a.page;
 }
 
@@ -1054,7 +1057,7 @@ __global__ void __launch_bounds__(WPR * RB * 32) k_tree_join(const float* __rest
   int f = 0, rows = 0, hk = 0, block = 0;
   if (most_blocks) {
     block = blockIdx.x % most_blocks, hk = blockIdx.x / most_blocks % a.Hkv;
-    if (tree_request(a, blockIdx.x / most_blocks / a.Hkv, x)) f = x.f, rows = x.n * a.G;
+    if (tree_request<true>(a, blockIdx.x / most_blocks / a.Hkv, x)) f = x.f, rows = x.n * a.G;
   }
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
