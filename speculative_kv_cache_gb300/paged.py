@@ -171,7 +171,8 @@ class PagedCache:
         """Sequence ``dst`` (empty) becomes a copy of ``src``, sharing its pages."""
         self._catch_up()
         ig.ig_pages_fork(self.pages, src, dst)
-        self._drafts.pop(src, None)
+        for seq in (src, dst):  # (an empty sequence with an empty tree is of its draft too)
+            self._drafts.pop(seq, None)
         if self.codes is not None:
             self._seen[:, dst] = self._seen[:, src]
         self._sync()

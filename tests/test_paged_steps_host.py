@@ -325,6 +325,25 @@ def test_a_draft_is_over_when_its_sequences_change(ig, monkeypatch, end):
         c.keep(draft, {0: [0]})
 
 
+def test_a_draft_is_over_when_one_of_its_sequences_becomes_a_copy(ig, monkeypatch):
+    """An empty sequence with an empty tree is of the draft too: what is forked into it stays."""
+    h = HostSteps(ig, monkeypatch)
+    c = h.cache
+    h.put({0: 9, 3: 4})
+    draft = c.draft({3: [-1, 0], 1: []})
+    h.want[3] += h.fill(draft.slots)
+    c.fork(0, 1)
+    h.want[1] = list(h.want[0])
+    with pytest.raises(ValueError, match="over"):
+        c.keep(draft, {3: [0]})
+    with pytest.raises(ValueError, match="over"):
+        c.attend_tree(0, None, draft)
+    h.check()
+    c.truncate(3, 4)  # the way out: the drafted tokens go
+    h.want[3] = h.want[3][:4]
+    h.check()
+
+
 def test_a_draft_outlives_what_other_sequences_do(ig, monkeypatch):
     h = HostSteps(ig, monkeypatch)
     c = h.cache
