@@ -46,6 +46,7 @@ class Draft:
         self.seqs, self.parents, self.base = seqs, parents, base
         self.n, self.T = len(seqs), sum(len(p) for p in parents)
         self.T_max = max([len(p) for p in parents] + [1])
+        self.kept, self.moved = None, 0  # paths of a keep that has begun, and layers that have their rows
 
 
 class PagedCache:
@@ -247,9 +248,11 @@ class PagedCache:
         self._drafts.update((s, x) for s in seqs)
         return x
 
-    def _drafted(self, draft):
+    def _drafted(self, draft, paths=None):
         if any(self._drafts.get(s) is not draft for s in draft.seqs):
             raise ValueError("the draft is over: its sequences have been extended, forked or cut since, or the pages packed")
+        if draft.moved and paths != draft.kept:
+            raise ValueError("rows of the draft have moved in some layers: a keep of the same paths goes on with the others")
 
     @_on_its_gpu
     def attend_tree(self, layer, q, draft, out=None, lse=None):
@@ -270,12 +273,13 @@ class PagedCache:
     def keep(self, draft, paths):
         """Keeps ``paths[sequence]`` of each of the draft's sequences, in every layer: the numbers of its accepted drafted tokens
         from the first level on, each the parent of the next (none where a sequence is not named).  The other
-        drafted tokens go."""
-        self._drafted(draft)
+        drafted tokens go.  Where that fails, the sequences have their drafted tokens still, and it can be tried again: with
+        other paths too, unless rows have moved already (in some of more than 128 layers)."""
         paths = {operator.index(s): [operator.index(i) for i in p] for s, p in paths.items()}
         if not set(paths) <= set(draft.seqs):
             raise ValueError("a path for a sequence that the draft does not have")
         paths = [paths.get(s, []) for s in draft.seqs]
+        self._drafted(draft, paths)
         for seq, path, tree in zip(draft.seqs, paths, draft.parents):
             if any(not 0 <= i < len(tree) for i in path) or any(tree[i] != p for p, i in zip([-1] + path, path)):
                 raise ValueError(f"sequence {seq}: {path} is no path of its tree from the first level on")
@@ -285,10 +289,11 @@ class PagedCache:
             for path, tree in zip(paths, draft.parents):
                 up += path + [0] * (len(tree) - len(path))
             up = torch.from_numpy(np.array(up, dtype=np.int32)).to(self.dev)
-            for l in range(0, self.layers, 128):
+            for l in range(draft.moved, self.layers, 128):  # (a second move would start from rows that are others by now)
                 K, V = self.K[l:l + 128], self.V[l:l + 128]
                 ig.ig_tree_keep(None, len(K), self.n_pages, self.Hkv, self.page, self.d, K, V, draft.n, self.seqs, self.max_pages,
                                 draft.T, self.table, self.L, draft.seq, draft.first, up[draft.n:], up[:draft.n])
+                draft.kept, draft.moved = paths, l + len(K)
         for seq, path, base in zip(draft.seqs, paths, draft.base):
             self._cut(seq, base + len(path))
             if self.codes is not None:

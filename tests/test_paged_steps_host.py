@@ -311,6 +311,37 @@ def test_cache_takes_a_failed_draft_back(ig, monkeypatch):
     h.check()
 
 
+def test_cache_goes_on_with_a_keep_that_failed_between_its_layers(ig, monkeypatch):
+    """Rows move 128 layers a call: those that have moved do not move again, and the draft stands for nothing else."""
+    h = HostSteps(ig, monkeypatch, layers=300)
+    c = h.cache
+    h.put({0: 13, 1: 8})
+    draft = c.draft({0: [-1, -1, 1, 2, 2], 1: [-1, -1]})
+    rows = h.fill(draft.slots)
+    keep, calls = ig.ig_tree_keep, []
+
+    def now_and_then(*a):
+        calls.append(a[1])
+        if len(calls) in (2, 4):
+            raise RuntimeError("no launch")
+        keep(*a)
+
+    monkeypatch.setattr(ig, "ig_tree_keep", now_and_then)
+    for _ in range(2):
+        with pytest.raises(RuntimeError, match="no launch"):
+            c.keep(draft, {0: [1, 2, 4], 1: [1]})
+        for other in ({}, {0: [1, 2, 4]}, {0: [1, 2, 3], 1: [1]}):
+            with pytest.raises(ValueError, match="moved"):
+                c.keep(draft, other)
+        with pytest.raises(ValueError, match="moved"):
+            c.attend_tree(0, None, draft)
+    c.keep(draft, {1: [1], 0: (1, 2, 4)})
+    assert calls == [128, 128, 128, 44, 44]
+    h.want[0] += [rows[1], rows[2], rows[4]]
+    h.want[1] += [rows[6]]
+    h.check()
+
+
 @pytest.mark.parametrize("end", ["extend", "fork", "truncate", "compact", "draft"])
 def test_a_draft_is_over_when_its_sequences_change(ig, monkeypatch, end):
     h = HostSteps(ig, monkeypatch)
