@@ -477,7 +477,7 @@ ig_status ig_page_bounds(void* stream, int dtype, int n_pages, int Hkv, int page
  *   q           dev [B][Hq][d] of `dtype`, 16-byte aligned
  *   codes, scales  as ig_page_bounds has written them for the sequences' pages
  *   page_table  dev int32 [B][max_pages];  L_valid dev int32 [B] (both as for ig_paged_attend; a page number out of
- *               range scores lowest and sets IG_DEVERR_INDEX)
+ *               range scores lowest and sets IG_DEVERR_INDEX; where it is taken all the same, chosen has it as it is)
  *   chosen      dev int32 [B][Hkv][picks] out: page numbers in the sequence's order, then -1
  *   tokens      dev int32 [B][Hkv] out: the tokens they hold (all are full but the sequence's last one)
  * chosen and tokens are what ig_paged_attend_picked takes.  d must be 64 or 128; Hq / Hkv at most 256; last >= 1,

@@ -229,7 +229,11 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
   for (int i = take + rank * kSelThreads + tid; i < a.picks; i += CL * kSelThreads) chosen[i] = -1;
   if (rank == 0 && tid == 0) a.tokens[row] = P ? (take - 1) * a.page + L - (P - 1) * a.page : 0;
   if (P <= a.picks) {  // all of them (the same for the whole cluster)
-    for (int i = rank * kSelThreads + tid; i < P; i += CL * kSelThreads) chosen[i] = __ldca(table + i);
+    for (int i = rank * kSelThreads + tid; i < P; i += CL * kSelThreads) {
+      const int id = __ldca(table + i);
+      chosen[i] = id;
+      if (id < 0 || id >= a.n_pages) raise_error(err, IG_DEVERR_INDEX);
+    }
     return;
   }
   if (CL > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA is there, its sums begin at zero

@@ -870,6 +870,33 @@ def test_choice_bounds_bad_lengths_and_pages_and_says_so(ig):
     assert torch.equal(chosen[1:], good[0][1:]) and not (chosen[0] == c["n"]).any()
 
 
+@pytest.mark.parametrize("lengths,max_pages", [([40, 300, 0], 38), ([90, 60], 12), ([8], 3000)])
+@pytest.mark.parametrize("entry", ["first", "last"])
+def test_choice_of_all_pages_looks_at_their_numbers_too(ig, lengths, max_pages, entry):
+    """A sequence with no more pages than are taken, in a CTA and in a cluster: its numbers go as they are, and it is said."""
+    c = make_picked(8, "f16", lengths, 4, 2, 64, 8)
+    bounds_of(ig, c)
+    c["table"] = torch.cat([c["table"], torch.full((c["B"], max_pages - c["mp"]), -1, dtype=torch.int32, device=DEV)], 1).contiguous()
+    c["mp"] = max_pages
+    good = select(ig, c, 12, 1, 2)
+    ig.ig_check()
+    assert good[0][0, 0].tolist() == (c["table"][0].tolist() + [-1] * 12)[:12]
+    at = 0 if entry == "first" else -(-lengths[0] // 8) - 1
+    for number in (c["n"], -1, -(2 ** 31), 2 ** 31 - 1):
+        c["table"][0, at] = number
+        chosen, tokens = select(ig, c, 12, 1, 2)
+        refused_on_device(ig)
+        assert torch.equal(tokens, good[1]) and torch.equal(chosen[1:], good[0][1:])
+        assert torch.all(chosen[0, :, at] == number)
+        chosen[0, :, at] = good[0][0, 0, at]
+        assert torch.equal(chosen, good[0])
+    if len(lengths) > 1:  # entries past a sequence's pages are not looked at
+        c["table"][0, at] = good[0][0, 0, at]
+        c["table"][0, -(-lengths[0] // 8):] = c["n"]
+        assert torch.equal(select(ig, c, 12, 1, 2)[0], good[0])
+        ig.ig_check()
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("lengths,Hq,Hkv,d,page,picks", [([1000, 0, 17, 300], 4, 2, 64, 16, 6), ([9000], 40, 8, 128, 32, 33),
                                                          ([2000] * 50, 6, 3, 128, 8, 40), ([700, 701], 34, 2, 64, 24, 5),
