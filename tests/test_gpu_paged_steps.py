@@ -434,6 +434,45 @@ def test_tree_unseen_rows_may_be_anything(ig, dt, d, what):
                 assert torch.equal(lse[f + i], wlse[f + i])
 
 
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("lengths,drafted,G,Hkv,page", [
+    ([5000], [64], 2, 2, 16),                 # 128 rows, cut
+    ([5000], [64], 4, 2, 24),                 # 256 rows, cut: one group clears for both
+    ([5000], [64], 8, 1, 64),                 # 512 rows in CTAs side by side, cut
+    ([5000, 3000], [64, 64], 5, 1, 32),       # 320 rows, the last 64 in a group's own unit
+    ([5000, 3000, 64, 700], [64, 20, 64, 33], 8, 2, 8),  # of several numbers of blocks, so one after the other
+    ([200, 64, 190, 321], [64, 64, 7, 64], 8, 3, 40)])   # few tiles, none cut
+def test_tree_unseen_rows_may_be_anything_in_blocks_and_parts(ig, dt, d, what, lengths, drafted, G, Hkv, page):
+    """As above, where a key head has more than 128 rows, and where several CTAs share a sequence's tiles: drafted rows on both
+    sides of a tile's end, their keys and values not finite."""
+    bad = [(b, j) for b, n in enumerate(drafted) for j in (2, 19, 55, 56, 63) if j < n]
+    masks = [m for x in drafted for m in ancestors([i - 1 if i % 2 else -1 for i in range(x)])]
+    c = make_tree(31, dt, lengths, drafted, G * Hkv, Hkv, d, page, masks=masks)
+    clean = dict(c, K=c["K"].clone(), V=c["V"].clone())
+    for b, j in bad:
+        t = lengths[b] - drafted[b] + j
+        at = (int(c["table"][b, t // page]), slice(None), t % page)
+        c["V"][at][:, 3::7] = float(what)
+        c["K"][at] = float("nan") if what == "nan" else 0.0
+        clean["V"][at][:, 3::7] = 0
+        clean["K"][at] = 0
+    (out, lse), (want, wlse) = attend_tree(ig, c), attend_tree(ig, clean)
+    ig.ig_check()
+    check_tree(clean, want, wlse)
+    touched = torch.zeros(d, dtype=torch.bool, device=DEV)
+    touched[3::7] = True
+    hit = torch.tensor([any(c["bits"][c["first"][b] + i] >> j & 1 for bb, j in bad if bb == b)
+                        for b, n in enumerate(drafted) for i in range(n)], device=DEV)
+    assert hit.any() and not hit.all()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse[~hit], wlse[~hit])
+    if what == "nan":
+        assert not torch.isfinite(out[hit]).any()
+    else:
+        assert torch.all(out[hit][:, :, touched] == float(what))
+        assert torch.equal(out[hit][:, :, ~touched], want[hit][:, :, ~touched]) and torch.equal(lse[hit], wlse[hit])
+
+
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 def test_tree_large_logits_and_small_weights_beside_a_large_one(ig, dt):
     """Logits up to some hundreds; and a first token whose value is zero takes nearly all the weight."""
