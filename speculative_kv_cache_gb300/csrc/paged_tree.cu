@@ -174,7 +174,7 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) 
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Waits for the loads, and ties their registers to the wait.
+// Waits for the loads, and ties registers that they fill to the wait (else nothing keeps arithmetic on them behind it).
 __device__ __forceinline__ void tm_wait_ld32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
@@ -185,7 +185,14 @@ __device__ __forceinline__ void tm_wait_ld32(uint32_t (&r)[32]) {
                : "memory");
   asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
-__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_ld32(uint32_t (&r)[32], uint32_t (&r2)[32]) {
+  tm_wait_ld32(r);
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile(""
+                 : "+r"(r2[i]), "+r"(r2[i + 1]), "+r"(r2[i + 2]), "+r"(r2[i + 3]), "+r"(r2[i + 4]), "+r"(r2[i + 5]), "+r"(r2[i + 6]),
+                   "+r"(r2[i + 7]));
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
@@ -744,7 +751,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
             const uint32_t vis = va[c] & seen_bits(mask, t0 + 32 * c - drafted);
             uint32_t y[32];
             tm_ld32(y, s_at + 32 * c);
-            tm_wait_ld();
+            tm_wait_ld32(y);
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = vis >> i & 1 ? __float_as_uint(__uint_as_float(y[i]) * sgn) : 0xff800000u;
             tm_st32(s_at + 32 * c, y);
@@ -946,11 +953,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) k_tree_attend(
           if (joined) {
             uint32_t o2[32];
             tm_ld32(o2, o_other + 32 * c);
-            tm_wait_ld();
+            tm_wait_ld32(o, o2);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f + __uint_as_float(o2[i]) * f2);
           } else {
-            tm_wait_ld();
+            tm_wait_ld32(o);
           }
           if (poisoned && live) {
             // drafted values that are not finite, of the tiles here: to the rows that see them
