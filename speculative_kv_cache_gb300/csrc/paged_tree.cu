@@ -174,25 +174,6 @@ __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) 
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Waits for the loads, and ties registers that they fill to the wait (else nothing keeps arithmetic on them behind it).
-__device__ __forceinline__ void tm_wait_ld32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
-               :
-               : "memory");
-  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-__device__ __forceinline__ void tm_wait_ld32(uint32_t (&r)[32], uint32_t (&r2)[32]) {
-  tm_wait_ld32(r);
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile(""
-                 : "+r"(r2[i]), "+r"(r2[i + 1]), "+r"(r2[i + 2]), "+r"(r2[i + 3]), "+r"(r2[i + 4]), "+r"(r2[i + 5]), "+r"(r2[i + 6]),
-                   "+r"(r2[i + 7]));
-}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;
