@@ -197,7 +197,7 @@ constexpr uint32_t kAlways = 0xffffffffu;
 // loads ahead.  8 rows of 8192 pages with 5 queries 13.7 us (17 MB of bounds, floor 2.5: 9100 cycles of 22500 are the
 // scores, 7300 the radix passes); 512 rows of up to 512 pages with 4 queries 14.6 us (floor 5); 64 pages of one sequence
 // 3.6 us.  Scores by mma.sync in fp16, exact as well, took longer (20.9 and 21.8 us), as did all keys sent to one CTA of the
-// cluster (20.4).
+// cluster (20.4, beside an earlier form of this kernel that took 17).
 template <bool BF, int D, int U>
 __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, int CL, int* err) {
   constexpr int LP = D / 32, PW = 32 / LP;  // lanes of a page (4 pieces of 16 bytes each), pages of a warp
@@ -443,8 +443,8 @@ __global__ void __launch_bounds__(kSelThreads) k_page_select(const SelArgs a, in
   }
 }
 
-// U: with many rows two pages a lane, so that three CTAs share an SM (64 sequences of up to 512 pages, 8 key heads: 14.8 us, with
-// four 18.4); with few four, so that more is on its way (8 rows of 8192: 17 us, with two 22).
+// U: with many rows two pages a lane, so that three CTAs share an SM (64 sequences of up to 512 pages, 8 key heads: 14.7 us, with
+// four 18.2); with few four, so that more is on its way (8 rows of 8192: 13.7 us, with two 17.4).
 template <bool BF, int D, int U>
 ig_status launch_select_u(cudaStream_t st, const SelArgs& a, int CL, size_t smem) {
   cudaError_t e = cudaFuncSetAttribute(k_page_select<BF, D, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

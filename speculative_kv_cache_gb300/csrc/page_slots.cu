@@ -7,7 +7,6 @@ namespace {
 constexpr int kMaxRequests = 8192;  // prefix sums in shared memory
 constexpr int kMaxTree = 64;        // drafted tokens of a request: bits of a mask
 constexpr int kSlotThreads = 256;
-constexpr int kSlotTokens = 1;      // of a thread, as long as four CTAs an SM have room
 
 struct SlotArgs {
   int n, seqs, page, n_pages, max_pages, T;
@@ -39,7 +38,7 @@ __device__ __forceinline__ int slot_of(const SlotArgs& a, int s, int at, int* er
 // request) a warp has a request, a lane the tokens lane and lane + 32: their ancestors' bits double with
 // every look at the parent's parent, six at most, all in registers.  Bound by latency: the counts, the sequence's
 // length, its page's number, one after the other: 64 trees of up to 16 tokens 3.3 us, 48 prompts of 100 000 tokens in all
-// 3.9 us (with four tokens a thread, one after the other, 6.1).
+// 3.9 us (a thread has a token, as long as four CTAs an SM have room; with four, one after the other, 6.1).
 template <bool TREE>
 __global__ void __launch_bounds__(kSlotThreads) k_page_slots(const SlotArgs a, int* err) {
   __shared__ int first[kMaxRequests + 1];
@@ -245,7 +244,7 @@ extern "C" ig_status ig_page_slots(void* stream, int n, int seqs, int page, int 
   const bool tree = parents || masks;
   const SlotArgs a{n, seqs, page, n_pages, max_pages, T, page_table, L_valid, seq, counts, parents, first, slots, positions,
                    reinterpret_cast<unsigned long long*>(masks)};
-  const long long work = tree ? ((long long)n * 32) : ((long long)T + kSlotTokens - 1) / kSlotTokens;
+  const long long work = tree ? (long long)n * 32 : T;
   long long grid = (work + kSlotThreads - 1) / kSlotThreads;
   const long long most = 4ll * sm_count(as_stream(stream));
   grid = grid < 1 ? 1 : grid > most ? most : grid;

@@ -10,8 +10,9 @@ keeps bounds of each page's keys (``summarise``: ``ig_page_bounds``), and ``atte
 a score from the bounds picks (``ig_page_select``, ``ig_paged_attend_picked``).
 All device work is queued on the current stream of the cache's GPU, whichever GPU is the current one.  The
 device tensors ``table`` and ``L`` stay in place, so a captured ``write`` + ``attend`` replays with what
-``extend`` put there since.  A cache's calls share its tables and one workspace, so they run one after
-another: on one stream, or on streams that wait for each other.
+``extend`` put there since.  (A draft's slots, positions, masks and numbers of tokens are its own: a captured
+``attend_tree`` replays that one draft, which has to be kept, and live, as long.)  A cache's calls share its
+tables and one workspace, so they run one after another: on one stream, or on streams that wait for each other.
 """
 from __future__ import annotations
 
