@@ -33,7 +33,7 @@
 // Measured (device time; the copy rate of HBM is 6.75 TB/s; rows: queries of a key head).
 //   One request of 131072 tokens, 8 key heads of 128, 537 MB, pages of 64: 86 us with 16 rows (0.92 of the copy rate), 87 with
 //   64, 89 with 128, 110 with 256 (PAIR), 192 with 512.  64 rows in pages of 16: 89, of 8: 90.  Heads of 64, 268 MB: 51 us with 64
-//   rows, 53 with 128, 91 with 256.
+//   rows, 53 with 128, 92 with 256.
 //   32 requests of 64 to 8192 tokens, 1 to 16 drafted, 558 MB, pages of 32: 98 us, 0.84; 4 are the join, of 150 cuts, 6 the plan
 //   and the first tile, and without any arithmetic of the softmax the rest takes as long.
 //   Two requests of 65536 tokens, 64 drafted, 512 rows, 136 Gflop: 110 us, 1.24 Pflop/s; a tile takes 3100 cycles, of which the
